@@ -10,7 +10,9 @@ from ._lib import (QGError, check_device_error, debug_block_sums, debug_wait_tim
                    linear_noalloc_scratch_bytes, linear_w8a8_q8_0,
                    linear_w8a8_q8_0_noalloc, linear_workspace_bytes, load, pack_q4k, pack_q8_0,
                    q4k_packed_bytes, q8_0_packed_bytes, quantize_act, quantize_act_static,
-                   small_m_max)
+                   small_m_max,
+                   gemm_fp8, linear_fp8, linear_fp8_workspace_bytes, quantize_act_fp8,
+                   token_logprobs, token_logprobs_workspace_bytes)
 
 __all__ = ["QGError", "check_device_error", "debug_block_sums", "debug_wait_timeout",
            "declared_symbols", "gemm_launch_count",
@@ -19,4 +21,6 @@ __all__ = ["QGError", "check_device_error", "debug_block_sums", "debug_wait_time
            "linear_noalloc_scratch_bytes", "linear_w8a8_q8_0",
            "linear_w8a8_q8_0_noalloc", "linear_workspace_bytes", "load", "pack_q4k", "pack_q8_0",
            "q4k_packed_bytes", "q8_0_packed_bytes", "quantize_act", "quantize_act_static",
-           "small_m_max"]
+           "small_m_max",
+           "gemm_fp8", "linear_fp8", "linear_fp8_workspace_bytes", "quantize_act_fp8",
+           "token_logprobs", "token_logprobs_workspace_bytes"]

@@ -68,6 +68,12 @@ def load():
         "qg_pack_mxfp4_q8_0": ([P, I64, I64, P, P], I),
         "qg_gemm_w4a8_mxfp4": ([P, P, P, I64, I64, P, I64, P, I, I64, P], I),
         "qg_linear_w4a8_mxfp4": ([P, I, I64, I64, I64, P, I64, P, I, I64, P, P, SZ, P], I),
+        "qg_quantize_act_fp8": ([P, I, I64, I64, I64, P, P, I64, P], I),
+        "qg_gemm_fp8": ([P, P, I64, I64, I64, P, I64, P, I64, P, I, I64, P], I),
+        "qg_linear_fp8_workspace_bytes": ([I64, I64], SZ),
+        "qg_linear_fp8": ([P, I, I64, I64, I64, P, I64, P, I64, P, I, I64, P, SZ, P], I),
+        "qg_token_logprobs_workspace_bytes": ([I64, I64, I], SZ),
+        "qg_token_logprobs": ([P, I, I64, I64, I64, P, I64, P, P, I, P, P, P, SZ, P], I),
     }
     for name, (args, res) in sigs.items():
         f = getattr(L, name)
@@ -289,6 +295,133 @@ def linear_w4a8_mxfp4(x, packed, N, out=None, out_dtype=torch.bfloat16, scale_ou
     """As linear_w8a8_q8_0, on weights from pack_mxfp4_q8_0."""
     return _linear("q8_0", x, packed, N, out, out_dtype, scale_out, workspace, stream,
                    fn=load().qg_linear_w4a8_mxfp4)
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory for work on `stream`: taken from that stream's pool, so that its reuse follows that work."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(t, name, dtypes):
+    """A cuda matrix of one of `dtypes` whose rows are contiguous."""
+    if not t.is_cuda or t.dim() != 2 or t.dtype not in dtypes or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be a 2-D cuda tensor of %s with contiguous rows" %
+                         (name, " or ".join(str(d) for d in dtypes)))
+    return t
+
+
+def _ld(t):
+    """Row stride of a matrix (of a single row: its length, whatever stride torch keeps for it)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+_FP8 = (torch.float8_e4m3fn,)
+
+
+def _fp8_weights(w, w_scale, K, out, M, out_dtype, stream):
+    _rows(w, "w", _FP8)
+    N = w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError("w has rows of %d values, the activations of %d" % (w.shape[1], K))
+    if (not w_scale.is_cuda or w_scale.dtype != torch.float32 or not w_scale.is_contiguous()
+            or tuple(w_scale.shape) != ((N + 127) // 128, (K + 127) // 128)):
+        raise ValueError("w_scale must be a contiguous cuda fp32 tensor of shape [ceil(N/128), ceil(K/128)]")
+    if out is None:
+        return _empty((M, N), out_dtype, w.device, stream)
+    if tuple(_rows(out, "out", _FLOATS).shape) != (M, N):
+        raise ValueError("out must have the shape (%d, %d)" % (M, N))
+    return out
+
+
+def quantize_act_fp8(x, out=None, stream=None):
+    """x: cuda [M, K] bf16/fp32 (rows may be strided; K % 16 == 0) -> (q float8_e4m3fn [M, K],
+    scale fp32 [ceil(K/128), M], one per token and 128 values of K; its rows start on 16-byte
+    boundaries). `out` may supply preallocated (q, scale)."""
+    M, K = _rows(x, "x", _FLOATS).shape
+    if out is None:
+        q = _empty((M, K), torch.float8_e4m3fn, x.device, stream)
+        scale = _empty(((K + 127) // 128, (M + 3) // 4 * 4), torch.float32, x.device, stream)[:, :M]
+    else:
+        q, scale = out
+        if _rows(q, "q", _FP8).shape != x.shape or not q.is_contiguous():
+            raise ValueError("q must be contiguous and of the shape of x")
+        if tuple(_rows(scale, "scale", (torch.float32,)).shape) != ((K + 127) // 128, M):
+            raise ValueError("scale must have the shape [ceil(K/128), M]")
+    _check(load().qg_quantize_act_fp8(_ptr(x), _dtype_code(x.dtype), M, K, _ld(x), _ptr(q),
+                                      _ptr(scale), _fp8_lds(scale), _stream(stream)))
+    return q, scale
+
+
+def _fp8_lds(scale):
+    # a single block of K has one row of scales: any stride does
+    return scale.stride(0) if scale.shape[0] > 1 else (scale.shape[1] + 3) // 4 * 4
+
+
+def gemm_fp8(q, scale, w, w_scale, out=None, out_dtype=torch.bfloat16, stream=None):
+    """q, scale from quantize_act_fp8; w: cuda float8_e4m3fn [N, K] as stored (rows may be strided);
+    w_scale: cuda fp32 [ceil(N/128), ceil(K/128)] -> out [M, N]."""
+    M, K = _rows(q, "q", _FP8).shape
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    if tuple(_rows(scale, "scale", (torch.float32,)).shape) != ((K + 127) // 128, M):
+        raise ValueError("scale must have the shape [ceil(K/128), M]")
+    out = _fp8_weights(w, w_scale, K, out, M, out_dtype, stream)
+    _check(load().qg_gemm_fp8(_ptr(q), _ptr(scale), _fp8_lds(scale), M, K, _ptr(w), _ld(w),
+                              _ptr(w_scale), w.shape[0], _ptr(out), _dtype_code(out.dtype), _ld(out),
+                              _stream(stream)))
+    return out
+
+
+def linear_fp8_workspace_bytes(M, K):
+    """Workspace bytes a linear_fp8 call of these sizes needs (0: invalid sizes)."""
+    return int(load().qg_linear_fp8_workspace_bytes(M, K))
+
+
+def linear_fp8(x, w, w_scale, out=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """The whole layer: x cuda [M, K] bf16/fp32 -> out [M, N] with e4m3 weights (see gemm_fp8).
+    Quantize, then GEMM, through `workspace` (allocated here when not given)."""
+    M, K = _rows(x, "x", _FLOATS).shape
+    out = _fp8_weights(w, w_scale, K, out, M, out_dtype, stream)
+    if workspace is None:
+        workspace = _empty((linear_fp8_workspace_bytes(M, K),), torch.uint8, x.device, stream)
+    _check(load().qg_linear_fp8(_ptr(x), _dtype_code(x.dtype), M, K, _ld(x), _ptr(w), _ld(w),
+                                _ptr(w_scale), w.shape[0], _ptr(out), _dtype_code(out.dtype), _ld(out),
+                                _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                _stream(stream)))
+    return out
+
+
+def token_logprobs_workspace_bytes(M, V, top):
+    """Workspace bytes a token_logprobs call of these sizes needs (0: invalid sizes)."""
+    return int(load().qg_token_logprobs_workspace_bytes(M, V, top))
+
+
+def token_logprobs(logits, ids, top=0, workspace=None, stream=None):
+    """logits: cuda [M, V] bf16/fp32 (rows may be strided); ids: cuda int64 [M, G] or [M] (-1: no
+    token) -> (logprobs fp32 of ids' shape, entropy fp32 [M], top_ids int64 [M, top], top_logprobs
+    fp32 [M, top]): log probabilities of the given tokens, the rows' entropies in nats and their
+    `top` likeliest tokens, ties to the lowest id; -1 where a row has fewer (see include/qgemm.h)."""
+    M, V = _rows(logits, "logits", _FLOATS).shape
+    if (not ids.is_cuda or ids.dtype != torch.int64 or ids.dim() not in (1, 2) or ids.shape[0] != M
+            or not ids.is_contiguous()):
+        raise ValueError("ids must be a contiguous cuda int64 tensor of shape [M] or [M, G]")
+    G = ids.shape[1] if ids.dim() == 2 else 1
+    dev = logits.device
+    logprobs = _empty(ids.shape, torch.float32, dev, stream)
+    entropy = _empty((M,), torch.float32, dev, stream)
+    top_ids = _empty((M, max(top, 0)), torch.int64, dev, stream)
+    top_logprobs = _empty((M, max(top, 0)), torch.float32, dev, stream)
+    if workspace is None:
+        workspace = _empty((token_logprobs_workspace_bytes(M, V, top),), torch.uint8, dev, stream)
+    _check(load().qg_token_logprobs(_ptr(logits), _dtype_code(logits.dtype), M, V, _ld(logits), _ptr(ids),
+                                    G, _ptr(logprobs), _ptr(entropy), top, _ptr(top_ids),
+                                    _ptr(top_logprobs), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream)))
+    return logprobs, entropy, top_ids, top_logprobs
 
 
 def linear_noalloc_scratch_bytes():

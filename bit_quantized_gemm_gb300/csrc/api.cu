@@ -45,6 +45,17 @@ cudaError_t launch_prefill_q4k(const uint16_t* q16, const float* sa, const int32
                                int64_t M, int64_t K, const void* packed, int64_t N, void* out,
                                bool out_f32, int64_t ldo, int32_t* dbg, uint32_t* err,
                                bool pdl, cudaStream_t st);
+cudaError_t launch_quantize_act_fp8(const void* x, bool bf16, int64_t M, int64_t K, int64_t ldx,
+                                    uint8_t* q, float* scale, int64_t lds, cudaStream_t st);
+cudaError_t launch_gemm_fp8(const uint8_t* q, const float* scale, int64_t lds, int64_t M, int64_t K,
+                            const uint8_t* w, int64_t ldw, const float* w_scale, int64_t N,
+                            void* out, bool out_f32, int64_t ldo, uint32_t* err, bool pdl,
+                            cudaStream_t st);
+int64_t token_logprobs_ws_bytes(int64_t M, int64_t V, int top);
+cudaError_t launch_token_logprobs(const void* logits, bool bf16, int64_t M, int64_t V, int64_t ldl,
+                                  const int64_t* ids, int64_t G, float* logprobs, float* entropy,
+                                  int top, int64_t* top_ids, float* top_logprobs, void* ws,
+                                  cudaStream_t st);
 }  // namespace qg
 
 using namespace qg;
@@ -66,6 +77,9 @@ constexpr int64_t kSmallMMax = 16;     // AUTO: decode kernel for M <= 16
 constexpr int64_t kDecodeRows = 16;    // rows per decode launch
 constexpr int64_t kMaxN = int64_t(1) << 24;
 constexpr int64_t kMaxM = int64_t(1) << 24;
+constexpr int64_t kMaxV = int64_t(1) << 24;
+constexpr int64_t kMaxGiven = int64_t(1) << 16;
+constexpr int kFp8Block = 128;         // values of K (and rows of N) that share an FP8 scale
 
 thread_local char t_last_error[256] = "";
 
@@ -217,6 +231,52 @@ qg_status linear(bool q4k, const void* x, qg_dtype xdt, int64_t M, int64_t K, in
                                             error_word(), true, st),
                    "decode GEMM launch");
 }
+
+// K of the FP8 calls: rows of e4m3 values start on 16-byte boundaries
+qg_status check_fp8_k(int64_t K) { return check_k(K, 16); }
+
+qg_status check_fp8_x(const void* x, qg_dtype xdt, int64_t M, int64_t K, int64_t ldx) {
+  if (xdt != QG_BF16 && xdt != QG_F32) return fail(QG_EINVAL, "x_dtype must be QG_BF16 or QG_F32");
+  if (M < 1 || M > kMaxM) return fail(QG_EINVAL, "M=%lld out of range [1, 2^24]", (long long)M);
+  qg_status s = check_fp8_k(K);
+  if (s != QG_OK) return s;
+  if (ldx < K) return fail(QG_EINVAL, "ldx=%lld < K=%lld", (long long)ldx, (long long)K);
+  if (!aligned(x, 16) || (ldx * (xdt == QG_BF16 ? 2 : 4)) % 16 != 0)
+    return fail(QG_EALIGN, "x needs 16-byte alignment and a row stride that is a multiple of 16 bytes");
+  return QG_OK;
+}
+
+qg_status check_fp8_scale(const float* scale, int64_t lds, int64_t M) {
+  if (lds < M) return fail(QG_EINVAL, "lds=%lld < M=%lld", (long long)lds, (long long)M);
+  if (!aligned(scale, 16) || lds % 4 != 0)
+    return fail(QG_EALIGN, "scale needs 16-byte alignment and lds a multiple of 4");
+  return QG_OK;
+}
+
+qg_status check_fp8_w(const uint8_t* w, int64_t ldw, const float* w_scale, int64_t N, int64_t K,
+                      const void* out, qg_dtype odt, int64_t ldo) {
+  if (N < 1 || N > kMaxN) return fail(QG_EINVAL, "N=%lld out of range [1, 2^24]", (long long)N);
+  if (odt != QG_BF16 && odt != QG_F32) return fail(QG_EINVAL, "out_dtype must be QG_BF16 or QG_F32");
+  if (ldw < K) return fail(QG_EINVAL, "ldw=%lld < K=%lld", (long long)ldw, (long long)K);
+  if (ldo < N) return fail(QG_EINVAL, "ldo=%lld < N=%lld", (long long)ldo, (long long)N);
+  if (!aligned(w, 16) || ldw % 16 != 0)
+    return fail(QG_EALIGN, "w needs 16-byte alignment and ldw a multiple of 16");
+  if (!aligned(w_scale, 4) || !aligned(out, 16))
+    return fail(QG_EALIGN, "w_scale needs 4-byte, out 16-byte alignment");
+  return QG_OK;
+}
+
+// Workspace of qg_linear_fp8: the scales [ceil(K/128)][M up to a multiple of
+// 4], then the e4m3 activations [M][K], each 256-byte aligned.
+struct LinearFp8Ws {
+  int64_t lds, off_scale, off_q, total;
+  LinearFp8Ws(int64_t M, int64_t K) {
+    lds = align_up(M, 4);
+    off_scale = 0;
+    off_q = align_up(ceil_div(K, kFp8Block) * lds * 4, 256);
+    total = align_up(off_q + M * K, 256);
+  }
+};
 
 // Device address of g_linear_scratch on the current device, looked up once
 // per device (with that device current) and cached; nullptr if the lookup
@@ -520,6 +580,102 @@ qg_status qg_linear_w8a8_q8_0_noalloc(const void* x, qg_dtype x_dtype, int64_t M
   }
   return linear(false, x, x_dtype, M, K, ldx, w_packed, N, out, out_dtype, ldo, scale_out, ws,
                 ws ? QG_LINEAR_NOALLOC_SCRATCH_BYTES : 0, stream);
+}
+
+qg_status qg_quantize_act_fp8(const void* x, qg_dtype x_dtype, int64_t M, int64_t K, int64_t ldx,
+                              uint8_t* q, float* scale, int64_t lds, void* stream) {
+  if (!x || !q || !scale) return fail(QG_EINVAL, "null pointer argument");
+  qg_status s = check_fp8_x(x, x_dtype, M, K, ldx);
+  if (s == QG_OK) s = check_fp8_scale(scale, lds, M);
+  if (s != QG_OK) return s;
+  if (!aligned(q, 16)) return fail(QG_EALIGN, "q needs 16-byte alignment");
+  return from_cuda(launch_quantize_act_fp8(x, x_dtype == QG_BF16, M, K, ldx, q, scale, lds,
+                                           reinterpret_cast<cudaStream_t>(stream)),
+                   "FP8 quantize launch");
+}
+
+qg_status qg_gemm_fp8(const uint8_t* q, const float* scale, int64_t lds, int64_t M, int64_t K,
+                      const uint8_t* w, int64_t ldw, const float* w_scale, int64_t N, void* out,
+                      qg_dtype out_dtype, int64_t ldo, void* stream) {
+  if (!q || !scale || !w || !w_scale || !out) return fail(QG_EINVAL, "null pointer argument");
+  if (M < 1 || M > kMaxM) return fail(QG_EINVAL, "M=%lld out of range [1, 2^24]", (long long)M);
+  qg_status s = check_fp8_k(K);
+  if (s == QG_OK) s = check_fp8_scale(scale, lds, M);
+  if (s == QG_OK) s = check_fp8_w(w, ldw, w_scale, N, K, out, out_dtype, ldo);
+  if (s != QG_OK) return s;
+  if (!aligned(q, 16)) return fail(QG_EALIGN, "q needs 16-byte alignment");
+  return from_cuda(launch_gemm_fp8(q, scale, lds, M, K, w, ldw, w_scale, N, out,
+                                   out_dtype == QG_F32, ldo, error_word(), false,
+                                   reinterpret_cast<cudaStream_t>(stream)),
+                   "FP8 GEMM launch");
+}
+
+size_t qg_linear_fp8_workspace_bytes(int64_t M, int64_t K) {
+  if (M < 1 || M > kMaxM || check_fp8_k(K) != QG_OK) return 0;
+  return (size_t)LinearFp8Ws(M, K).total;
+}
+
+qg_status qg_linear_fp8(const void* x, qg_dtype x_dtype, int64_t M, int64_t K, int64_t ldx,
+                        const uint8_t* w, int64_t ldw, const float* w_scale, int64_t N, void* out,
+                        qg_dtype out_dtype, int64_t ldo, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  if (!x || !w || !w_scale || !out) return fail(QG_EINVAL, "null pointer argument");
+  qg_status s = check_fp8_x(x, x_dtype, M, K, ldx);
+  if (s == QG_OK) s = check_fp8_w(w, ldw, w_scale, N, K, out, out_dtype, ldo);
+  if (s != QG_OK) return s;
+  const LinearFp8Ws L(M, K);
+  if (!workspace || workspace_bytes < (size_t)L.total)
+    return fail(QG_EINVAL,
+                "workspace of %lld bytes needed for M=%lld (qg_linear_fp8_workspace_bytes)",
+                (long long)L.total, (long long)M);
+  if (!aligned(workspace, 256)) return fail(QG_EALIGN, "workspace needs 256-byte alignment");
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  char* base = reinterpret_cast<char*>(workspace);
+  float* scale = reinterpret_cast<float*>(base + L.off_scale);
+  uint8_t* q = reinterpret_cast<uint8_t*>(base + L.off_q);
+  s = from_cuda(launch_quantize_act_fp8(x, x_dtype == QG_BF16, M, K, ldx, q, scale, L.lds, st),
+                "FP8 quantize launch");
+  if (s != QG_OK) return s;
+  return from_cuda(launch_gemm_fp8(q, scale, L.lds, M, K, w, ldw, w_scale, N, out,
+                                   out_dtype == QG_F32, ldo, error_word(), true, st),
+                   "FP8 GEMM launch");
+}
+
+static bool logprobs_sizes_ok(int64_t M, int64_t V, int top) {
+  return M >= 1 && M <= kMaxM && V >= 1 && V <= kMaxV && top >= 0 && top <= QG_LOGPROBS_MAX_TOP;
+}
+
+size_t qg_token_logprobs_workspace_bytes(int64_t M, int64_t V, int top) {
+  return logprobs_sizes_ok(M, V, top) ? (size_t)token_logprobs_ws_bytes(M, V, top) : 0;
+}
+
+qg_status qg_token_logprobs(const void* logits, qg_dtype dtype, int64_t M, int64_t V, int64_t ldl,
+                            const int64_t* ids, int64_t G, float* logprobs, float* entropy,
+                            int top, int64_t* top_ids, float* top_logprobs, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (!logits) return fail(QG_EINVAL, "null pointer argument");
+  if (dtype != QG_BF16 && dtype != QG_F32) return fail(QG_EINVAL, "dtype must be QG_BF16 or QG_F32");
+  if (!logprobs_sizes_ok(M, V, top))
+    return fail(QG_EINVAL, "M=%lld, V=%lld must be in [1, 2^24] and top=%d in [0, %d]", (long long)M,
+                (long long)V, top, QG_LOGPROBS_MAX_TOP);
+  if (G < 0 || G > kMaxGiven) return fail(QG_EINVAL, "G=%lld out of range [0, 2^16]", (long long)G);
+  if (ldl < V) return fail(QG_EINVAL, "ldl=%lld < V=%lld", (long long)ldl, (long long)V);
+  if (G > 0 && (!ids || !logprobs)) return fail(QG_EINVAL, "ids and logprobs are needed for G > 0");
+  if (top > 0 && (!top_ids || !top_logprobs))
+    return fail(QG_EINVAL, "top_ids and top_logprobs are needed for top > 0");
+  if (!aligned(logits, dtype == QG_BF16 ? 2 : 4) || (ids && !aligned(ids, 8)) ||
+      (logprobs && !aligned(logprobs, 4)) || (entropy && !aligned(entropy, 4)) ||
+      (top_ids && !aligned(top_ids, 8)) || (top_logprobs && !aligned(top_logprobs, 4)))
+    return fail(QG_EALIGN, "every array needs the alignment of its elements");
+  const int64_t need = token_logprobs_ws_bytes(M, V, top);
+  if (!workspace || workspace_bytes < (size_t)need)
+    return fail(QG_EINVAL, "workspace of %lld bytes needed (qg_token_logprobs_workspace_bytes)",
+                (long long)need);
+  if (!aligned(workspace, 256)) return fail(QG_EALIGN, "workspace needs 256-byte alignment");
+  return from_cuda(launch_token_logprobs(logits, dtype == QG_BF16, M, V, ldl, ids, G, logprobs,
+                                         entropy, top, top_ids, top_logprobs, workspace,
+                                         reinterpret_cast<cudaStream_t>(stream)),
+                   "log-probability launch");
 }
 
 // A single bounded wait on a barrier that nothing arrives at: after `polls`

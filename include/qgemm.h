@@ -290,6 +290,80 @@ qg_status qg_linear_w8a8_q8_0_noalloc(const void* x, qg_dtype x_dtype, int64_t M
                                       void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* FP8 (e4m3) operands with an fp32 scale for each block of 128: the layer    */
+/* for weights stored as e4m3 with one scale per 128 x 128 block, activations */
+/* quantized per token and per 128 values of K.                               */
+/*   Activation quantization, row m, block b (128 consecutive k; the last     */
+/*   block of a row may be shorter):                                          */
+/*     s[b][m] = max |x[m,k]| * fl(1/448)    (one fp32 product)               */
+/*     q[m,k]  = e4m3(clamp(x[m,k] / s, -448, 448))  (IEEE quotient, then to   */
+/*                                            nearest, ties to even)          */
+/*     s = 0 gives q = 0; NaN and infinities spread by IEEE rules (a row that  */
+/*     holds one has NaN products).                                           */
+/*   Product:                                                                 */
+/*     sum = sum_{k in b} q[m,k] * w[n,k]    (exact products, fp32 tensor sum)*/
+/*     acc = fmaf(sum, s[b][m] * ws[n/128][b], acc)   for b = 0, 1, ... in order*/
+/*     out = bf16(acc) (round to nearest even) or acc (fp32)                  */
+/*   The K chain of an output is never split, so a row's result does not      */
+/*   depend on the other rows of its call.                                    */
+/* K is a positive multiple of 16, at most 65536; 1 <= M, N <= 2^24.          */
+/* ------------------------------------------------------------------------ */
+/*   x      [M][ldx] of x_dtype, 16-byte aligned, ldx >= K,                   */
+/*          ldx*elem_size % 16 == 0.                                          */
+/*   q      [M][K] e4m3 out, 16-byte aligned.                                 */
+/*   scale  [ceil(K/128)][lds] fp32 out: s[b][m] at scale[b*lds + m];         */
+/*          16-byte aligned, lds >= M a multiple of 4. Columns M.. are left.  */
+qg_status qg_quantize_act_fp8(const void* x, qg_dtype x_dtype, int64_t M, int64_t K, int64_t ldx,
+                              uint8_t* q, float* scale, int64_t lds, void* stream);
+/*   q, scale, lds  as written by qg_quantize_act_fp8.                        */
+/*   w        [N][ldw] e4m3, rows of K values, as stored (no packing); 16-byte */
+/*            aligned, ldw >= K a multiple of 16.                             */
+/*   w_scale  [ceil(N/128)][ceil(K/128)] fp32, 4-byte aligned: the value of w  */
+/*            at (n, k) is w * w_scale[n/128][k/128].                         */
+/*   out      [M][ldo] of out_dtype, 16-byte aligned, ldo >= N.               */
+qg_status qg_gemm_fp8(const uint8_t* q, const float* scale, int64_t lds, int64_t M, int64_t K,
+                      const uint8_t* w, int64_t ldw, const float* w_scale, int64_t N, void* out,
+                      qg_dtype out_dtype, int64_t ldo, void* stream);
+/* The whole layer: qg_quantize_act_fp8 into the caller's workspace (at least  */
+/* qg_linear_fp8_workspace_bytes(M, K) bytes, 256-byte aligned; 0 if the sizes */
+/* are invalid), then qg_gemm_fp8, with the bits of the two calls.            */
+size_t qg_linear_fp8_workspace_bytes(int64_t M, int64_t K);
+qg_status qg_linear_fp8(const void* x, qg_dtype x_dtype, int64_t M, int64_t K, int64_t ldx,
+                        const uint8_t* w, int64_t ldw, const float* w_scale, int64_t N, void* out,
+                        qg_dtype out_dtype, int64_t ldo, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Log probabilities of given tokens, entropy and top alternatives, from the  */
+/* logits that an output head writes. Row by row, with m = max x,             */
+/* S = sum e^(x-m), T = sum e^(x-m) (x-m):                                    */
+/*   logprobs[m][g] = x[id] - m - log S, id = ids[m][g]                       */
+/*   entropy[m]     = log S - T / S      (nats)                               */
+/*   top_ids[m][], top_logprobs[m][]  the first `top` values in the order     */
+/*                    (value descending, index ascending).                    */
+/*   A row of -inf alone (a mask that leaves nothing): -inf, entropy 0, no    */
+/*   alternatives. A row with a NaN or +inf has no distribution: every float  */
+/*   is NaN, no alternatives. An alternative that is none has index -1 and    */
+/*   -inf (NaN in such a row); a value of -inf is never an alternative.       */
+/*   An id below 0 asks for nothing and gives 0; an id >= V gives NaN.        */
+/*   logits   [M][ldl] of dtype (QG_BF16 or QG_F32), rows of V values, ldl >= */
+/*            V; aligned to its element (rows need no alignment).             */
+/*   ids      [M][G] int64, logprobs [M][G] fp32; both may be NULL when G is 0.*/
+/*   entropy  [M] fp32, or NULL.                                              */
+/*   top_ids  [M][top] int64, top_logprobs [M][top] fp32, 0 <= top <=         */
+/*            QG_LOGPROBS_MAX_TOP; both may be NULL when top is 0.            */
+/*   workspace  at least qg_token_logprobs_workspace_bytes(M, V, top) bytes,  */
+/*            256-byte aligned (0 bytes: the sizes are invalid).              */
+/* 1 <= M <= 2^24, 1 <= V <= 2^24, 0 <= G <= 2^16.                            */
+/* ------------------------------------------------------------------------ */
+#define QG_LOGPROBS_MAX_TOP 32
+size_t qg_token_logprobs_workspace_bytes(int64_t M, int64_t V, int top);
+qg_status qg_token_logprobs(const void* logits, qg_dtype dtype, int64_t M, int64_t V, int64_t ldl,
+                            const int64_t* ids, int64_t G, float* logprobs, float* entropy,
+                            int top, int64_t* top_ids, float* top_logprobs, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Test support: the exact per-block integer sums as the chosen kernel sees   */
 /* them, isum[m][n][b] (int32, [M][N][K/32]), taken from the same kernels     */
 /* (decode: the int8 MMA accumulators; prefill: the tensor-memory block       */
