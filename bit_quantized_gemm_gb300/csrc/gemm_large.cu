@@ -742,6 +742,23 @@ bool make_tmap(CUtensorMap* map, const void* base, int64_t rows, int64_t K,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Matrix of `rows` rows of `cols` elements at a pitch of `pitch` bytes, box =
+// box_cols x box_rows, 128- or 64-byte swizzle (the FP8 kernels' operands and
+// outputs). False when the base or the pitch is not 16-byte aligned.
+bool make_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t cols,
+                  int64_t rows, int64_t pitch, uint32_t box_cols, uint32_t box_rows,
+                  CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc || !base || (reinterpret_cast<uintptr_t>(base) & 15) || pitch % 16) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)pitch};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // rows of `row_bytes` bytes (a multiple of 16), read as 8-byte words:
 // box = box_words x box_rows, no swizzle, so the box lands row after row at a
 // pitch of 8 * box_words bytes; words past a row's end read as zero (used by
