@@ -17,9 +17,10 @@
 // half of the W weight rows, and holds the accumulators of its own tokens, so
 // that per MMA a pair brings in W/2 instead of W weight rows per SM.
 //
-// Warps (384 threads, one CTA per SM, persistent): 0 TMA producer, 1 MMA
-// issuer (leader CTA of a pair) and tensor memory, 2-3 idle, 4..11 epilogue:
-// warp w reads lanes 32*(w%4).. and half (w-4)/4 of the columns. Outputs are
+// Warps (384 threads, one CTA per SM, persistent): 0 TMA producer, 1 and 2 MMA
+// issuers (of a pair's leader CTA; even and odd blocks: an MMA's issue blocks
+// while the tensor core is busy, so one issuer's barrier waits have to overlap
+// the other's MMAs), 3 idle, 4..11 epilogue: warp w reads lanes 32*(w%4).. and half (w-4)/4 of the columns. Outputs are
 // staged per warp in shared memory (32 rows of 128 bytes, swizzled) and leave
 // by TMA, or by coalesced element stores where the row length or the pitch is
 // not a multiple of 16 bytes.
@@ -63,11 +64,11 @@ struct Fp8LargeCfg {
   static constexpr int kRound = kF32 ? 32 : (kCols % 64 == 0 ? 64 : 32);
   static constexpr int kRowBytes = kRound * (kF32 ? 4 : 2);
   static constexpr int kStaging = 8 * 32 * kRowBytes;
-  static constexpr int kStages = (226 * 1024 - kStaging - 2048) / (int)(kABytes + kBBytes) > 12
-                                     ? 12
-                                     : (226 * 1024 - kStaging - 2048) / (int)(kABytes + kBBytes);
+  // an even ring: each of the two issuers owns half of its stages
+  static constexpr int kFit = (226 * 1024 - kStaging - 2048) / (int)(kABytes + kBBytes) & ~1;
+  static constexpr int kStages = kFit > 12 ? 12 : kFit;
   static constexpr size_t kSmem = (size_t)kStages * (kABytes + kBBytes) + kStaging + 1024;
-  static_assert(W % 64 == 0 && W <= 256 && kCols % kRound == 0 && kStages >= 3, "tile");
+  static_assert(W % 64 == 0 && W <= 256 && kCols % kRound == 0 && kStages >= 4, "tile");
 };
 
 template <bool kPair, int W, bool kF32>
@@ -77,7 +78,7 @@ __global__ void __launch_bounds__(kFp8LargeThreads, 1)
                           const __grid_constant__ CUtensorMap tmO, const Fp8LargeArgs a) {
   using C = Fp8LargeCfg<kPair, W, kF32>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], mdrain;
+  __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], mdrain[2];
   __shared__ uint32_t tmem_slot, tmem_busy;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -99,8 +100,8 @@ __global__ void __launch_bounds__(kFp8LargeThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], 8 * C::kCtas);  // epilogue warps of both CTAs
+      mbar_init(&mdrain[i], 1);
     }
-    mbar_init(&mdrain, 1);
     tmem_busy = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmQ);
@@ -129,10 +130,6 @@ __global__ void __launch_bounds__(kFp8LargeThreads, 1)
     mt = g * a.tile_group + idx % gm;
     nt = idx / gm;
   };
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if constexpr (kPair) return mbar_wait_cluster(bar, parity, a.err);
-    else return mbar_wait(bar, parity, a.err);
-  };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -147,7 +144,7 @@ __global__ void __launch_bounds__(kFp8LargeThreads, 1)
         coords(tile, mt, nt);
         const int m = mt * C::kTileM + (int)rank * 128, n = nt * W + (int)rank * C::kWRows;
         for (int b = 0; b < KB; ++b) {
-          ok = wait(&empty[s], phase);
+          ok = mbar_wait(&empty[s], phase, a.err);
           if (!ok) break;
           // both CTAs' bytes complete on the leader's barrier
           if (rank == 0) mbar_arrive_expect_tx(&full[s], C::kCtas * (C::kABytes + C::kBBytes));
@@ -169,53 +166,60 @@ __global__ void __launch_bounds__(kFp8LargeThreads, 1)
       for (int i = max(0, loads - C::kStages); i < loads; ++i) {
         const int r = i % C::kStages;
         const uint32_t par = (uint32_t)(i / C::kStages) & 1u;
-        if (ok) ok = wait(&empty[r], par);
-        if (!ok && rank == 0) wait(&full[r], par);
+        if (ok) ok = mbar_wait(&empty[r], par, a.err);
+        if (!ok && rank == 0) mbar_wait(&full[r], par, a.err);
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+  } else if (warp <= 2) {
+    // issuer `par` takes the blocks g = par, par + 2, ... of this CTA's tiles,
+    // into buffer par; the even ring depth gives it the same stages each round
+    if (rank == 0) {
       constexpr uint32_t idesc = idesc_e4m3_f32(C::kTileM, W);
-      int s = 0, t = 0;
+      const int par = warp - 1;
+      const int total = first < tiles ? (tiles - first + step - 1) / step * KB : 0;
+      int s = par;
       uint32_t phase = 0, tphase = 1;
       bool ok = true;
-      for (int tile = first; tile < tiles && ok; tile += step) {
-        for (int b = 0; b < KB; ++b) {
-          ok = wait(&tempty[t], tphase) && wait(&full[s], phase);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t aa = smem_u32(sa + s * C::kABytes), ba = smem_u32(sb + s * C::kBBytes);
+      for (int g = par; g < total; g += 2) {
+        ok = mbar_wait(&full[s], phase, a.err) && mbar_wait(&tempty[par], tphase, a.err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t aa = smem_u32(sa + s * C::kABytes), ba = smem_u32(sb + s * C::kBBytes);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if constexpr (kPair)
-              mma_e4m3_ss_pair(tmem + t * 256, smem_desc_sw128(aa + k * 32),
+              mma_e4m3_ss_pair(tmem + par * 256, smem_desc_sw128(aa + k * 32),
                                smem_desc_sw128(ba + k * 32), idesc, k);
             else
-              mma_e4m3_ss(tmem + t * 256, smem_desc_sw128(aa + k * 32),
+              mma_e4m3_ss(tmem + par * 256, smem_desc_sw128(aa + k * 32),
                           smem_desc_sw128(ba + k * 32), idesc, k);
           }
           if constexpr (kPair) {
+            mma_commit_pair(&tfull[par]);
             mma_commit_pair(&empty[s]);
-            mma_commit_pair(&tfull[t]);
           } else {
+            mma_commit(&tfull[par]);
             mma_commit(&empty[s]);
-            mma_commit(&tfull[t]);
           }
-          if (++s == C::kStages) { s = 0; phase ^= 1; }
-          t ^= 1;
-          if (t == 0) tphase ^= 1;
         }
+        __syncwarp();
+        s += 2;
+        if (s >= C::kStages) { s = par; phase ^= 1; }
+        tphase ^= 1;
       }
       if (!ok) {
         // the MMAs issued so far may still run: wait (bounded) before tensor
         // memory is freed; if that gives up too, it stays allocated
-        if constexpr (kPair) mma_commit_pair(&mdrain);
-        else mma_commit(&mdrain);
-        if (!wait(&mdrain, 0)) atomicExch(&tmem_busy, 1u);
+        if (elect_one()) {
+          if constexpr (kPair) mma_commit_pair(&mdrain[par]);
+          else mma_commit(&mdrain[par]);
+        }
+        __syncwarp();
+        if (!mbar_wait(&mdrain[par], 0, a.err)) atomicExch(&tmem_busy, 1u);
       }
     }
-    __syncwarp();
   } else if (warp >= 4) {
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     if (a.pdl) griddep_wait();  // the scales come from the quantize kernel
@@ -252,7 +256,7 @@ __global__ void __launch_bounds__(kFp8LargeThreads, 1)
           w0_next = ldg_f32_pinned(wp0 + b + 1);
           if (kCross) w1_next = ldg_f32_pinned(wp1 + b + 1);
         }
-        ok = wait(&tfull[t], tphase);
+        ok = mbar_wait(&tfull[t], tphase, a.err);
         if (!ok) break;
         tc_fence_after();
         const uint32_t taddr =

@@ -406,6 +406,20 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n) {
          ((uint32_t)(m >> 4) << 24);
 }
 
+// True in one lane of a converged warp. Tensor-core instructions take their
+// descriptors from warp-uniform registers: issued under this predicate, inside
+// otherwise uniform control flow, they cost fewer issue cycles than under
+// `lane == 0`.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------------------
 // CTA pairs: two CTAs of a cluster whose tensor cores work on one tile. The
 // even-ranked CTA (the leader) issues the MMAs; each CTA loads its own half of
@@ -426,25 +440,12 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
+// Arrive on a barrier of either CTA. No ordering of memory at cluster scope is
+// asked for: these barriers hand over tensor memory (ordered by the tcgen05
+// fences) and tiles written by the async proxy, and a cluster-scope release
+// costs a fence per block.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t* err,
-                                                  uint32_t limit = (1u << 24)) {
-  for (uint32_t i = 0; i < limit; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
-  }
-  set_error(err, kErrTimeout);
-  return false;
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // 2-D TMA load into this CTA, completing on a barrier of either CTA of the pair
 __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const void* tmap, uint32_t bar_cluster,
