@@ -51,7 +51,13 @@ struct Fp8LargeArgs {
   uint32_t* err;
 };
 
-constexpr int kFp8LargeThreads = 384;
+constexpr int kFp8Epi = 8;    // epilogue warps
+// The epilogue's 128 accumulators and two 32-column loads do not fit the 168
+// registers of an even split: 208 for its warps and 88 for the other four
+// (together no more than the 384 * 168 of the launch).
+constexpr int kFp8EpiRegs = 208, kFp8RestRegs = 88;
+static_assert(32 * (kFp8Epi * kFp8EpiRegs + 4 * kFp8RestRegs) <= (128 + 32 * kFp8Epi) * 168, "registers");
+constexpr int kFp8LargeThreads = 128 + 32 * kFp8Epi;
 
 template <bool kPair, int W, bool kF32>
 struct Fp8LargeCfg {
@@ -59,17 +65,21 @@ struct Fp8LargeCfg {
   static constexpr int kTileM = 128 * kCtas;
   static constexpr int kWRows = W / kCtas;       // weight rows loaded by a CTA
   static constexpr uint32_t kABytes = 128 * 128, kBBytes = kWRows * 128;
-  static constexpr int kCols = W / 2;            // columns per epilogue thread
-  // columns per staging round: rows of 128 bytes, or of 64 where the span is odd
-  static constexpr int kRound = kF32 ? 32 : (kCols % 64 == 0 ? 64 : 32);
-  static constexpr int kRowBytes = kRound * (kF32 ? 4 : 2);
-  static constexpr int kStaging = 8 * 32 * kRowBytes;
+  static constexpr int kCols = W / (kFp8Epi / 4);  // columns per epilogue thread
+  static constexpr int kRowBytes = 512 / kFp8Epi;  // staging rows: 64 (or 32) bytes
+  static constexpr int kRound = kRowBytes / (kF32 ? 4 : 2);  // columns per staging round
+  static constexpr int kStaging = kFp8Epi * 32 * kRowBytes;
+  static constexpr int kScales = 2 * 2 * 128 * 4;  // s * ws: two buffers, two blocks of rows, 128 tokens
+  static constexpr int kFixed = kStaging + kScales + 1024;
   // an even ring: each of the two issuers owns half of its stages
-  static constexpr int kFit = (226 * 1024 - kStaging - 2048) / (int)(kABytes + kBBytes) & ~1;
+  static constexpr int kFit = (226 * 1024 - kFixed) / (int)(kABytes + kBBytes) & ~1;
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
-  static constexpr size_t kSmem = (size_t)kStages * (kABytes + kBBytes) + kStaging + 1024;
+  static constexpr size_t kSmem = (size_t)kStages * (kABytes + kBBytes) + kFixed;
   static_assert(W % 64 == 0 && W <= 256 && kCols % kRound == 0 && kStages >= 4, "tile");
 };
+
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[16]) { tmem_ld16(taddr, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld32(taddr, v); }
 
 template <bool kPair, int W, bool kF32>
 __global__ void __launch_bounds__(kFp8LargeThreads, 1)
@@ -78,13 +88,14 @@ __global__ void __launch_bounds__(kFp8LargeThreads, 1)
                           const __grid_constant__ CUtensorMap tmO, const Fp8LargeArgs a) {
   using C = Fp8LargeCfg<kPair, W, kF32>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], mdrain[2];
+  __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], sempty[2], mdrain[2];
   __shared__ uint32_t tmem_slot, tmem_busy;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* sa = base;                              // token tiles
   uint8_t* sb = sa + C::kStages * C::kABytes;      // weight tiles
-  uint8_t* so = sb + C::kStages * C::kBBytes;      // output staging, 4 KB (2 KB) per warp
+  uint8_t* so = sb + C::kStages * C::kBBytes;      // output staging, kRowBytes x 32 per warp
+  float* sf = reinterpret_cast<float*>(so + C::kStaging);  // s * ws [buffer][row block][token]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = kPair ? cluster_ctarank() : 0;
   const int KB = a.KB;
@@ -98,8 +109,9 @@ __global__ void __launch_bounds__(kFp8LargeThreads, 1)
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 8 * C::kCtas);  // epilogue warps of both CTAs
+      mbar_init(&tfull[i], 2);                    // the MMAs' commit and the scale warp
+      mbar_init(&tempty[i], kFp8Epi * C::kCtas);  // epilogue warps of both CTAs
+      mbar_init(&sempty[i], kFp8Epi);
       mbar_init(&mdrain[i], 1);
     }
     tmem_busy = 0;
@@ -131,6 +143,7 @@ __global__ void __launch_bounds__(kFp8LargeThreads, 1)
     nt = idx / gm;
   };
 
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFp8RestRegs));
   if (warp == 0) {
     if (lane == 0) {
       // as a programmatic dependent of the quantize kernel: nothing of the
@@ -220,9 +233,73 @@ __global__ void __launch_bounds__(kFp8LargeThreads, 1)
         if (!mbar_wait(&mdrain[par], 0, a.err)) atomicExch(&tmem_busy, 1u);
       }
     }
-  } else if (warp >= 4) {
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
+  } else if (warp == 3) {
+    // scale warp: s * ws of block g for this CTA's 128 tokens and the (at most
+    // two) blocks of weight rows of the tile, into buffer g % 2. Four blocks
+    // are loaded ahead, across tiles: a load from L2 takes about as long as
+    // two blocks of MMAs.
     if (a.pdl) griddep_wait();  // the scales come from the quantize kernel
+    const int total = first < tiles ? (tiles - first + step - 1) / step * KB : 0;
+    int lt = first, lb = 0;  // the next block to load
+    const float *lp = nullptr, *lw0 = nullptr, *lw1 = nullptr;
+    bool valid = false;
+    float4 s_cur[4], s_nxt[4];
+    float2 w_cur[4], w_nxt[4];
+    auto load = [&](float4& s4, float2& w2) {
+      if (lt >= tiles) return;
+      if (lb == 0) {
+        int mt, nt;
+        coords(lt, mt, nt);
+        const int m = mt * C::kTileM + (int)rank * 128 + lane * 4;
+        valid = m < a.M;  // whole quads: lds is a multiple of 4
+        lp = a.scale + m;
+        const int nb = (nt * W) >> 7;
+        lw0 = a.w_scale + (int64_t)nb * KB;
+        lw1 = a.w_scale + (int64_t)min(nb + 1, a.NB - 1) * KB;
+      }
+      s4 = valid ? ldg_f32x4_pinned(lp + (int64_t)lb * a.lds) : make_float4(0.f, 0.f, 0.f, 0.f);
+      w2.x = ldg_f32_pinned(lw0 + lb);
+      w2.y = W > 128 ? ldg_f32_pinned(lw1 + lb) : 0.0f;
+      if (++lb == KB) {
+        lb = 0;
+        lt += step;
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load(s_nxt[j], w_nxt[j]);
+    bool ok = true;
+    uint32_t phase = 1;
+    for (int g0 = 0; g0 < total && ok; g0 += 4) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s_cur[j] = s_nxt[j];
+        w_cur[j] = w_nxt[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) load(s_nxt[j], w_nxt[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (g0 + j >= total) break;
+        constexpr int kT[4] = {0, 1, 0, 1};
+        const int t = kT[j];
+        ok = mbar_wait(&sempty[t], phase, a.err);
+        if (!ok) break;
+        float* f = sf + t * 256 + lane * 4;
+        const float4 v = s_cur[j];
+        const float2 w = w_cur[j];
+        *reinterpret_cast<float4*>(f) = make_float4(v.x * w.x, v.y * w.x, v.z * w.x, v.w * w.x);
+        if (W > 128)
+          *reinterpret_cast<float4*>(f + 128) =
+              make_float4(v.x * w.y, v.y * w.y, v.z * w.y, v.w * w.y);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tfull[t]);
+        if (t == 1) phase ^= 1;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFp8EpiRegs));
+    const int quarter = warp & 3, part = (warp - 4) >> 2;
+    if (a.pdl) griddep_wait();  // the output may be what an earlier kernel still reads
     uint8_t* stage = so + (warp - 4) * 32 * C::kRowBytes;
     uint32_t tempty_addr[2];
 #pragma unroll
@@ -235,76 +312,87 @@ __global__ void __launch_bounds__(kFp8LargeThreads, 1)
       int mt, nt;
       coords(tile, mt, nt);
       const int mrow0 = mt * C::kTileM + (int)rank * 128 + quarter * 32;  // this warp's first token
-      const int nc0 = nt * W + half * C::kCols;                          // and first column
-      const float* sp = a.scale + min(mrow0 + lane, a.M - 1);
-      // a span of W/2 columns lies in one block of 128 weight rows, or (W =
-      // 192) in two
+      const int nc0 = nt * W + part * C::kCols;                          // and first column
+      // column c of this thread uses the scale of the tile's row block
+      // (coff + c) / 128; a span that is a power of two lies in one
       constexpr bool kCross = (C::kCols & (C::kCols - 1)) != 0;
-      const int nb0 = min(nc0 >> 7, a.NB - 1), nb1 = min(nb0 + 1, a.NB - 1);
-      const float* wp0 = a.w_scale + (int64_t)nb0 * KB;
-      const float* wp1 = a.w_scale + (int64_t)nb1 * KB;
-      const int split = kCross ? 128 - (nc0 & 127) : 0;  // columns in the first block
+      const int coff = ((nt * W) & 127) + part * C::kCols;
       float acc[C::kCols];
 #pragma unroll
       for (int j = 0; j < C::kCols; ++j) acc[j] = 0.0f;
-      float s_next = __ldg(sp), w0_next = __ldg(wp0), w1_next = kCross ? __ldg(wp1) : 0.0f;
-      for (int b = 0; b < KB; ++b) {
-        const float f0 = s_next * w0_next, f1 = kCross ? s_next * w1_next : 0.0f;
-        if (b + 1 < KB) {
-          sp += a.lds;
-          s_next = ldg_f32_pinned(sp);
-          w0_next = ldg_f32_pinned(wp0 + b + 1);
-          if (kCross) w1_next = ldg_f32_pinned(wp1 + b + 1);
-        }
-        ok = mbar_wait(&tfull[t], tphase, a.err);
-        if (!ok) break;
+      // kChunk columns per load, the next load in flight during the FMAs, also
+      // across blocks: the next block's barrier is looked at a few chunks
+      // early, so that its first load can follow this block's last one
+      constexpr int kChunk = C::kCols % 64 == 0 ? 32 : 16;
+      constexpr int kN = C::kCols / kChunk;
+      static_assert(kN % 2 == 0, "a block's first load goes to v[0]");
+      uint32_t v[2][kChunk];
+      float f0 = 0.0f, f1 = 0.0f;
+      uint32_t taddr = 0;
+      auto begin = [&]() {  // buffer t is complete: its first load and its scales
         tc_fence_after();
-        const uint32_t taddr =
-            tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(t * 256 + half * C::kCols);
-        // 16 columns per load, the next load in flight during the FMAs
-        uint32_t v[2][16];
-        tmem_ld16(taddr, v[0]);
+        taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(t * 256 + part * C::kCols);
+        tmem_ld(taddr, v[0]);
+        const float* fp = sf + t * 256 + quarter * 32 + lane;
+        f0 = kCross ? fp[0] : fp[(coff >> 7) * 128];
+        f1 = kCross ? fp[128] : 0.0f;
+      };
+      ok = mbar_wait(&tfull[t], tphase, a.err);
+      if (!ok) break;
+      begin();
+      for (int b = 0; b < KB; ++b) {
+        const int tc = t;
+        t ^= 1;  // the next block's buffer and phase
+        if (t == 0) tphase ^= 1;
+        bool ready = false;
 #pragma unroll
-        for (int c = 0; c < C::kCols / 16; ++c) {
+        for (int c = 0; c < kN; ++c) {
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(v[c & 1][i]));
-          if (c + 1 < C::kCols / 16) {
-            tmem_ld16(taddr + (c + 1) * 16, v[(c + 1) & 1]);
+          for (int i = 0; i < kChunk; ++i) asm volatile("" : "+r"(v[c & 1][i]));
+          const float g0 = f0, g1 = f1;
+          if (c + 1 < kN) {
+            tmem_ld(taddr + (c + 1) * kChunk, v[(c + 1) & 1]);
+            if (c == (kN > 4 ? kN - 4 : 0)) ready = mbar_test(&tfull[t], tphase);
           } else {
             tc_fence_before();
-            __syncwarp();
+            ready = __all_sync(0xffffffffu, ready) && b + 1 < KB;
             if (lane == 0) {
-              if constexpr (kPair) mbar_arrive_cluster(tempty_addr[t]);
-              else mbar_arrive(&tempty[t]);
+              if constexpr (kPair) mbar_arrive_cluster(tempty_addr[tc]);
+              else mbar_arrive(&tempty[tc]);
+              mbar_arrive(&sempty[tc]);
             }
+            __syncwarp();
+            if (ready) begin();
           }
-          const float f = kCross && c * 16 >= split ? f1 : f0;
-          const float2 f2 = make_float2(f, f);
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            float* ac = acc + c * 16 + i;
+          for (int i = 0; i < kChunk; i += 2) {
+            const float f = kCross && coff + c * kChunk + (i & ~15) >= 128 ? g1 : g0;
+            float* ac = acc + c * kChunk + i;
             const float2 r = __ffma2_rn(make_float2(__uint_as_float(v[c & 1][i]),
                                                     __uint_as_float(v[c & 1][i + 1])),
-                                        f2, make_float2(ac[0], ac[1]));
+                                        make_float2(f, f), make_float2(ac[0], ac[1]));
             ac[0] = r.x;
             ac[1] = r.y;
           }
         }
-        t ^= 1;
-        if (t == 0) tphase ^= 1;
+        if (!ready && b + 1 < KB) {
+          ok = mbar_wait(&tfull[t], tphase, a.err);
+          if (!ok) break;
+          begin();
+        }
       }
       if (!ok) break;
       // outputs: kRound columns of this warp's 32 tokens at a time through its
-      // staging rows; a 16-byte chunk lands at chunk ^ (row % 8), or for
-      // 64-byte rows chunk ^ (row / 2 % 4), the TMA swizzles
+      // staging rows; a 16-byte chunk lands at chunk ^ (row / 2 % 4), for
+      // 32-byte rows chunk ^ (row / 4 % 2), the TMA swizzles
 #pragma unroll
       for (int c = 0; c < C::kCols; c += C::kRound) {
         if (a.tma_out) {
           if (lane == 0) bulk_wait_read_all();  // the previous store has read the rows
         }
         __syncwarp();
-        const uint32_t sw = C::kRowBytes == 128 ? (lane & 7) : ((lane >> 1) & 3);
+        const uint32_t sw = C::kRowBytes == 64 ? ((lane >> 1) & 3) : ((lane >> 2) & 1);
 #pragma unroll
         for (int i = 0; i < C::kRowBytes / 16; ++i) {
           uint4 o;
@@ -334,11 +422,10 @@ __global__ void __launch_bounds__(kFp8LargeThreads, 1)
           __syncwarp();
           const int rows = min(32, a.M - mrow0);
           for (int r = 0; r < rows; ++r) {
-            const uint32_t rsw = C::kRowBytes == 128 ? (r & 7) : ((r >> 1) & 3);
-#pragma unroll
-            for (int j = lane; j < C::kRound; j += 32) {
+            const uint32_t rsw = C::kRowBytes == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
+            const int j = lane;
+            if (j < C::kRound && nc0 + c + j < a.N) {
               const int n = nc0 + c + j;
-              if (n >= a.N) continue;
               const int byte = j * (kF32 ? 4 : 2);
               const uint8_t* p =
                   stage + r * C::kRowBytes + (((byte >> 4) ^ rsw) << 4) + (byte & 15);
@@ -394,12 +481,19 @@ static cudaError_t launch_large(const uint8_t* q, int64_t K, const uint8_t* w, i
   a.tma_out = a.N * (kF32 ? 4 : 2) % 16 == 0 &&
               make_tmap_2d(&to, kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                            a.out, a.N, a.M, a.ldo * (kF32 ? 4 : 2), C::kRound, 32,
-                           C::kRowBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+                           C::kRowBytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
   a.tile_group = 2048 / C::kTileM;
   auto kern = gemm_fp8_large_kernel<kPair, W, kF32>;
   static std::atomic<uint64_t> attr_set{0};
   cudaError_t e = smem_attr_once_per_device(kern, (int)C::kSmem, attr_set);
   if (e != cudaSuccess) return e;
+  // the register split takes from what the block was launched with
+  static const int regs = [&] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (regs * kFp8LargeThreads < 32 * (kFp8Epi * kFp8EpiRegs + 4 * kFp8RestRegs))
+    return cudaErrorInvalidConfiguration;
   const int64_t tiles = ceil_div(a.M, C::kTileM) * ceil_div(a.N, W);
   const int64_t slots = num_sms() / C::kCtas;
   cudaLaunchConfig_t cfg = {};
