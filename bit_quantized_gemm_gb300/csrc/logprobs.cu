@@ -4,128 +4,559 @@
 // With m = max x, S = sum e^(x-m), T = sum e^(x-m) (x-m) over a row of V:
 //   log p[i] = x[i] - m - log S,   H = -sum p log p = log S - T / S
 // (both terms of H are >= 0: nothing cancels). The alternatives are the first
-// `top` values in the order (value descending, index ascending).
-// Statistics are held in fp32.
+// `top` values in the order (value descending, index ascending). Statistics
+// are held in fp32 relative to a running maximum.
 //
 // Rows without a distribution: -inf everywhere (a mask that leaves nothing)
 // gives log p = -inf, H = 0 and no alternatives (index -1, -inf); a row with a
-// NaN or +inf gives NaN and no alternatives (index -1, NaN). An alternative of
-// -inf is none: its index is -1. An id below 0 asks for nothing and gives 0; an
-// id >= V gives NaN.
+// NaN or +inf gives NaN and no alternatives (index -1, NaN): either makes S a
+// NaN, which is how it is told. An alternative of -inf is none: its index is
+// -1. An id below 0 asks for nothing and gives 0; an id >= V gives NaN.
 //
-// The plain form: one CTA per row, one pass for m, S, T and one pass for each
-// alternative.
+// Bound by reading the logits once: 2 (bf16) or 4 bytes a value. The rows are
+// cut into `splits` pieces where there are too few of them for the SMs; a CTA
+// reads its piece in chunks of 128 threads x 64 bytes, the next chunk in
+// flight, and each thread keeps (m, S, T) of its own values. For the
+// alternatives a CTA keeps its `top` best so far as 64-bit keys (value, then
+// inverted index) and only looks at values above the last of them: the first
+// chunk, where a threshold comes from the warps' maxima, is ranked at once, and
+// from then on the few values that pass (about `top` for each doubling of the
+// length) are collected without a barrier and ranked now and then. A second
+// kernel joins the pieces.
 #include <math_constants.h>
 
 #include "qg_common.cuh"
 
 namespace qg {
 
+// Small CTAs, eight on an SM: one's barriers hide behind the others (4096 x 131072
+// bf16, no alternatives: 167 us, 175 with 256 threads, 209 with 512).
+constexpr int kLpThreads = 128, kLpWarps = kLpThreads / 32, kLpCtas = 8;
+constexpr int kLpVecs = 4;                   // 16-byte loads per thread and chunk
+constexpr int kLpCap = 512;                 // candidates of a chunk that are ranked at once
+constexpr int kLpTop = QG_LOGPROBS_MAX_TOP;
+constexpr int kLpMaxSplits = 32;             // a lane each in the joining warp
+static_assert(kLpTop <= 32 && kLpTop % kLpWarps == 0, "a lane per alternative");
+
+struct LpArgs {
+  const void* logits;
+  int64_t V, ldl;
+  const int64_t* ids;
+  float* logprobs;
+  float* entropy;
+  int64_t* top_ids;
+  float* top_logprobs;
+  float4* stats;      // [M][splits] m, S, T
+  uint64_t* keys;     // [M][splits][top], descending, 0: none
+  int G, top, splits;
+};
+
+// Order of the alternatives as an unsigned key: larger value first (both zeros
+// are equal), then smaller index. 0 is below every value.
+__device__ __forceinline__ uint64_t lp_key(float x, uint32_t i) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  const uint32_t o = (u >> 31) ? ~u : u | 0x80000000u;
+  return (uint64_t)o << 32 | (uint32_t)~i;
+}
+__device__ __forceinline__ float lp_value(uint64_t key) {
+  const uint32_t o = (uint32_t)(key >> 32);
+  return __uint_as_float((o >> 31) ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ uint64_t warp_max_u64(uint64_t k) {
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+  return (uint64_t)hi << 32 | lo;
+}
+
+// (m, S, T) of two sets of values as one
+__device__ __forceinline__ void lp_join(float& m, float& S, float& T, float m2, float S2, float T2) {
+  const float mm = fmaxf(m, m2);
+  // S = 0 marks an empty set (m = -inf); a NaN in S stays. A difference below
+  // -200 (or one that overflows) stands for a factor of 0.
+  const float c1 = S == 0.0f ? 0.0f : __expf(m - mm), c2 = S2 == 0.0f ? 0.0f : __expf(m2 - mm);
+  const float d1 = S == 0.0f ? 0.0f : fmaxf(m - mm, -200.0f), d2 = S2 == 0.0f ? 0.0f : fmaxf(m2 - mm, -200.0f);
+  T = c1 * fmaf(S, d1, T) + c2 * fmaf(S2, d2, T2);
+  S = c1 * S + c2 * S2;
+  m = mm;
+}
+__device__ __forceinline__ void lp_join_warp(float& m, float& S, float& T) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), S2 = __shfl_xor_sync(0xffffffffu, S, o),
+                T2 = __shfl_xor_sync(0xffffffffu, T, o);
+    lp_join(m, S, T, m2, S2, T2);
+  }
+}
+
 template <bool kBf16>
-__device__ __forceinline__ float load_logit(const void* row, int64_t i) {
+__device__ __forceinline__ float lp_load(const void* row, int64_t i) {
   if (kBf16) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << 16);
   return reinterpret_cast<const float*>(row)[i];
 }
 
+// One row's outputs from its statistics and its keys (descending, 0: none).
+// id0, x0: the thread's first given id and its logit, loaded ahead.
 template <bool kBf16>
-__global__ void __launch_bounds__(256) logprobs_plain_kernel(
-    const void* __restrict__ logits, int64_t V, int64_t ldl, const int64_t* __restrict__ ids, int G,
-    float* __restrict__ logprobs, float* __restrict__ entropy, int top,
-    int64_t* __restrict__ top_ids, float* __restrict__ top_logprobs) {
-  const int64_t m = blockIdx.x;
-  const int tid = threadIdx.x;
-  const char* row = reinterpret_cast<const char*>(logits) + m * ldl * (kBf16 ? 2 : 4);
-  __shared__ float fs[256];
-  __shared__ float ft[256];
-  __shared__ int64_t is[256];
-  float mx = -CUDART_INF_F;
-  bool bad = false;
-  for (int64_t i = tid; i < V; i += 256) {
-    const float x = load_logit<kBf16>(row, i);
-    bad |= !(x < CUDART_INF_F);
-    mx = fmaxf(mx, x);
-  }
-  fs[tid] = mx;
-  bad = __syncthreads_or(bad);
-  for (int i = 0; i < 256; ++i) mx = fmaxf(mx, fs[i]);
-  __syncthreads();
-  const bool empty = mx == -CUDART_INF_F;
-  float S = 0.0f, T = 0.0f;
-  if (!bad && !empty)
-    for (int64_t i = tid; i < V; i += 256) {
-      const float d = load_logit<kBf16>(row, i) - mx;
-      const float e = expf(d);
-      S += e;
-      if (e > 0.0f) T += e * d;
-    }
-  fs[tid] = S;
-  ft[tid] = T;
-  __syncthreads();
-  S = T = 0.0f;
-  for (int i = 0; i < 256; ++i) {
-    S += fs[i];
-    T += ft[i];
-  }
-  __syncthreads();
+__device__ __forceinline__ void lp_outputs(const LpArgs& a, int64_t m, const void* row, float mx, float S,
+                                           float T, const uint64_t* keys, int tid, int threads,
+                                           int64_t id0, float x0) {
+  const bool empty = mx == -CUDART_INF_F && S == 0.0f, bad = !(S == S);
   const float shift = empty ? 0.0f : mx, lse = empty ? 0.0f : logf(S);
   auto logp = [&](float x) {
     if (bad) return CUDART_NAN_F;
     return x == -CUDART_INF_F ? x : (x - shift) - lse;
   };
-  if (tid == 0 && entropy) entropy[m] = bad ? CUDART_NAN_F : empty ? 0.0f : lse - T / S;
-  for (int g = tid; g < G; g += 256) {
-    const int64_t id = ids[m * G + g];
-    logprobs[m * G + g] = id < 0 ? 0.0f : id >= V ? CUDART_NAN_F : logp(load_logit<kBf16>(row, id));
+  if (tid == 0 && a.entropy) a.entropy[m] = bad ? CUDART_NAN_F : empty ? 0.0f : lse - T / S;
+  for (int g = tid; g < a.G; g += threads) {
+    const int64_t id = g == tid ? id0 : a.ids[m * a.G + g];
+    const float x = g == tid || id < 0 || id >= a.V ? x0 : lp_load<kBf16>(row, id);
+    a.logprobs[m * a.G + g] = id < 0 ? 0.0f : id >= a.V ? CUDART_NAN_F : logp(x);
   }
-  float last = CUDART_INF_F;
-  int64_t last_i = -1;
-  for (int t = 0; t < top; ++t) {
-    float best = -CUDART_INF_F;
-    int64_t best_i = V;
-    if (!bad)
-      for (int64_t i = tid; i < V; i += 256) {
-        const float x = load_logit<kBf16>(row, i);
-        if ((x < last || (x == last && i > last_i)) && x > best) {
-          best = x;
-          best_i = i;
-        }
+  for (int t = tid; t < a.top; t += threads) {
+    const uint64_t k = keys[t];
+    const bool none = bad || k == 0;
+    a.top_ids[m * a.top + t] = none ? -1 : (int64_t)(uint32_t)~(uint32_t)k;
+    a.top_logprobs[m * a.top + t] = logp(k == 0 ? -CUDART_INF_F : lp_value(k));
+  }
+}
+
+template <bool kBf16>
+struct LpChunk {
+  static constexpr int kVec = kBf16 ? 8 : 4;           // values per 16-byte load
+  static constexpr int kPer = kLpVecs * kVec;          // values per thread
+  uint4 v[kLpVecs];
+
+  static __device__ __forceinline__ float value(const uint4& q, int j) {  // value j (a constant) of a load
+    if (kBf16) {
+      const uint32_t w = j < 2 ? q.x : j < 4 ? q.y : j < 6 ? q.z : q.w;
+      return __uint_as_float((j & 1) ? w & 0xFFFF0000u : w << 16);
+    }
+    return __uint_as_float(j == 0 ? q.x : j == 1 ? q.y : j == 2 ? q.z : q.w);
+  }
+  __device__ __forceinline__ float at(int i) const { return value(v[i / kVec], i % kVec); }
+  static __device__ __forceinline__ float max_of(const uint4& q) {  // largest value, NaNs aside
+    if (kBf16) {
+      const __nv_bfloat162 a = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&q.x),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&q.y));
+      const __nv_bfloat162 b = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&q.z),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&q.w));
+      const __nv_bfloat162 m = __hmax2(a, b);
+      return fmaxf(__low2float(m), __high2float(m));
+    }
+    return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)),
+                 fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+  }
+  static constexpr uint32_t kNone = kBf16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+  // the thread's vectors of a chunk of n (whole: n = 4 * 128)
+  __device__ __forceinline__ void load(const uint4* chunk, int64_t n) {
+    if (n >= kLpVecs * kLpThreads) {
+#pragma unroll
+      for (int i = 0; i < kLpVecs; ++i) v[i] = __ldcs(chunk + i * kLpThreads + threadIdx.x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLpVecs; ++i) {
+        const int q = i * kLpThreads + threadIdx.x;
+        v[i] = q < n ? __ldcs(chunk + q) : make_uint4(kNone, kNone, kNone, kNone);
       }
-    fs[tid] = best;
-    is[tid] = best_i;
-    __syncthreads();
-    for (int i = 0; i < 256; ++i)
-      if (fs[i] > best || (fs[i] == best && is[i] < best_i)) {
-        best = fs[i];
-        best_i = is[i];
-      }
-    __syncthreads();
-    last = best;
-    last_i = best_i;
-    if (tid == 0) {
-      const bool none = bad || best == -CUDART_INF_F;
-      top_ids[m * top + t] = none ? -1 : best_i;
-      top_logprobs[m * top + t] = logp(best);
     }
   }
+  // one value, or none
+  __device__ __forceinline__ void load_one(const void* row, int64_t e, bool valid) {
+#pragma unroll
+    for (int i = 0; i < kLpVecs; ++i) v[i] = make_uint4(kNone, kNone, kNone, kNone);
+    if (!valid) return;
+    if (kBf16) v[0].x = (kNone & 0xFFFF0000u) | reinterpret_cast<const uint16_t*>(row)[e];
+    else v[0].x = reinterpret_cast<const uint32_t*>(row)[e];
+  }
+  // largest value (NaNs aside)
+  __device__ __forceinline__ float max() const {
+    if (kBf16) {
+      __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&v[0].x);
+#pragma unroll
+      for (int i = 0; i < kLpVecs; ++i) {
+        m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].x));
+        m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].y));
+        m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].z));
+        m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].w));
+      }
+      return fmaxf(__low2float(m), __high2float(m));
+    }
+    float m = at(0);
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) m = fmaxf(m, at(i));
+    return m;
+  }
+};
+
+struct LpShared {
+  uint4 own[kLpVecs][kLpThreads];  // values of the threads that have candidates
+  uint64_t cand[kLpCap + kLpTop];  // candidates, then (to be ranked) the list so far
+  uint64_t list[kLpTop];           // the best so far, descending, 0: none
+  uint64_t red[kLpWarps];
+  float wm[kLpWarps], wS[kLpWarps], wT[kLpWarps];
+  int count;                       // candidates, also those past the buffer's end
+};
+
+// value i of the thread, from S.own, and its row index (i0: that of value 0)
+template <bool kBf16>
+__device__ __forceinline__ float lp_own(const LpShared& S, int i) {
+  return lp_load<kBf16>(&S.own[i / LpChunk<kBf16>::kVec][threadIdx.x], i % LpChunk<kBf16>::kVec);
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t lp_index(uint32_t i0, int i) {
+  constexpr int kVec = LpChunk<kBf16>::kVec;
+  return i0 + (uint32_t)((i / kVec) * kLpThreads * kVec + i % kVec);
+}
+
+// Appends this thread's values above `low` (with `ties`, at it as well) to the
+// candidates, in no particular order: they are ranked by their keys. (Calls of
+// their own from here on: rare, and inlined they took the main loop's registers.)
+template <bool kBf16>
+__device__ __noinline__ void lp_append(LpShared& S, float low, bool ties, uint32_t i0) {
+  using C = LpChunk<kBf16>;
+#pragma unroll 1
+  for (int i = 0; i < kLpVecs; ++i) {
+    const uint4 q = S.own[i][threadIdx.x];
+    const float vm = C::max_of(q);
+    if (!(vm > low || (ties && vm == low))) continue;
+#pragma unroll
+    for (int j = 0; j < C::kVec; ++j) {
+      const float x = C::value(q, j);
+      if (x > low || (ties && x == low)) {
+        const int p = atomicAdd(&S.count, 1);
+        if (p < kLpCap) S.cand[p] = lp_key(x, lp_index<kBf16>(i0, i * C::kVec + j));
+      }
+    }
+  }
+}
+
+// The candidates (no more than fit) and the list as the new list; returns its
+// last value, -inf while it is not full. Called by the whole CTA after a
+// barrier that follows the last append.
+__device__ __noinline__ float lp_rank(LpShared& S, int top) {
+  const int tid = threadIdx.x, n = S.count;
+  if (tid < top) S.cand[n + tid] = S.list[tid];
+  __syncthreads();
+  if (tid < top) S.list[tid] = 0;
+  if (tid == 0) S.count = 0;
+  __syncthreads();
+  // the rank of a key is the number of larger ones (keys differ, empty ones aside)
+  for (int i = tid; i < n + top; i += kLpThreads) {
+    const uint64_t k = S.cand[i];
+    if (k == 0) continue;
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n + top; ++j) rank += S.cand[j] > k;
+    if (rank < top) S.list[rank] = k;
+  }
+  __syncthreads();
+  const uint64_t k = S.list[top - 1];
+  return k == 0 ? -CUDART_INF_F : lp_value(k);
+}
+
+// Takes a chunk's values above `tau` (the last of the list's values, -inf while
+// it is not full; with `ties`, values at tau as well) into the list, whatever
+// their number, and returns the new tau. Threads whose maximum mx qualifies
+// have left their values in S.own. No candidates are pending. Called by the
+// whole CTA.
+template <bool kBf16>
+__device__ __noinline__ float lp_take(LpShared& S, float mx, float tau, bool ties, uint32_t i0, int top) {
+  using C = LpChunk<kBf16>;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // While the list is not full, a lower bound of its last value: with r =
+  // ceil(top / warps), the smallest over the warps of their r-th largest
+  // thread maximum has at least `top` values at or above it.
+  float low = tau;
+  if (tau == -CUDART_INF_F) {
+    float x = mx, r = -CUDART_INF_F;
+    for (int i = 0; i < (top + kLpWarps - 1) / kLpWarps; ++i) {
+      r = x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
+      const uint32_t at = __ballot_sync(0xffffffffu, x == r);
+      if (lane == __ffs(at) - 1) x = -CUDART_INF_F;
+    }
+    if (lane == 0) S.wm[warp] = r;
+    __syncthreads();
+    low = S.wm[0];
+#pragma unroll
+    for (int w = 1; w < kLpWarps; ++w) low = fminf(low, S.wm[w]);
+    ties = low > -CUDART_INF_F;
+  }
+  const bool has = mx > low || (ties && mx == low);
+  if (has) lp_append<kBf16>(S, low, ties, i0);
+  __syncthreads();
+  const int n = S.count;
+  if (n <= kLpCap) return lp_rank(S, top);
+  // more candidates than fit (many equal or ascending values): the largest key
+  // below the last one, `top` times
+  __syncthreads();
+  if (tid < top) S.cand[tid] = S.list[tid];
+  if (tid == 0) S.count = 0;
+  __syncthreads();
+  uint64_t last = ~0ull;
+  for (int t = 0; t < top; ++t) {
+    uint64_t best = 0;
+    if (tid < top && S.cand[tid] < last) best = S.cand[tid];
+    if (has) {
+#pragma unroll 4
+      for (int i = 0; i < C::kPer; ++i) {
+        const float x = lp_own<kBf16>(S, i);
+        const uint64_t k = lp_key(x, lp_index<kBf16>(i0, i));
+        if (x > -CUDART_INF_F && k < last && k > best) best = k;
+      }
+    }
+    best = warp_max_u64(best);
+    if (lane == 0) S.red[warp] = best;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kLpWarps; ++w) best = S.red[w] > best ? S.red[w] : best;
+    last = best;
+    if (tid == 0) S.list[t] = best;  // (0 once there are no more)
+    __syncthreads();
+  }
+  const uint64_t k = S.list[top - 1];
+  return k == 0 ? -CUDART_INF_F : lp_value(k);
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(const LpArgs a) {
+  using C = LpChunk<kBf16>;
+  __shared__ LpShared S;
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t m = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
+  const int split = blockIdx.x;
+  const char* row = reinterpret_cast<const char*>(a.logits) + m * a.ldl * (kBf16 ? 2 : 4);
+  // The row is `head` values up to a 16-byte boundary, whole vectors, and a
+  // tail. The vectors are cut into pieces; the values around them are a last
+  // step of the first piece, one per thread.
+  constexpr int kEs = kBf16 ? 2 : 4;
+  const int64_t head = min((int64_t)((16 - reinterpret_cast<uintptr_t>(row) % 16) % 16) / kEs, a.V);
+  const int64_t vecs = (a.V - head) / C::kVec, tail = head + vecs * C::kVec;
+  const uint4* body = reinterpret_cast<const uint4*>(row + head * kEs);
+  const int64_t per = ceil_div(vecs, (int64_t)a.splits);
+  const int64_t v0 = split * per, v1 = v0 + per < vecs ? v0 + per : vecs;
+  constexpr int kStep = kLpVecs * kLpThreads;  // vectors per chunk
+  const int chunks = v1 > v0 ? (int)ceil_div(v1 - v0, (int64_t)kStep) : 0;
+  const int around = split == 0 ? (int)(head + a.V - tail) : 0;
+  const int steps = chunks + (around > 0);
+  const int64_t mine = tid < head ? tid : tail + tid - head;  // this thread's value around the vectors
+  if (tid < kLpTop) S.list[tid] = 0;
+  if (tid == 0) S.count = 0;
+  __syncthreads();
+
+  float mx = -CUDART_INF_F, tau = -CUDART_INF_F;
+  float2 sum2 = make_float2(0.0f, 0.0f), tsum2 = sum2;  // tsum2 in units of log2
+  bool over = false;
+  auto index0 = [&](int step) {  // row index of the thread's value 0
+    return step < chunks ? (uint32_t)(head + (v0 + (int64_t)step * kStep + tid) * C::kVec) : (uint32_t)mine;
+  };
+  C cur;
+  auto load = [&](C& c, int step) {
+    if (step < chunks) c.load(body + v0 + (int64_t)step * kStep, v1 - v0 - (int64_t)step * kStep);
+    else c.load_one(row, mine, tid < around);
+  };
+  if (steps > 0) load(cur, 0);
+  // a given id and its logit take two trips to memory: the first now, the
+  // second after the first chunk
+  const int64_t id = a.splits == 1 && tid < a.G ? a.ids[m * a.G + tid] : -1;
+  float x_id = 0.0f;
+  for (int step = 0; step < steps; ++step) {
+    C nxt;
+    if (step + 1 < steps) load(nxt, step + 1);
+    const float cm = cur.max();
+    if (step == 0 && id >= 0 && id < a.V) x_id = lp_load<kBf16>(row, id);
+    if (cm > mx) {
+      const float c = __expf(mx - cm);  // 0 while mx = -inf, where the sums are 0 (or NaN)
+      const float d = fmaxf(mx - cm, -200.0f) * 1.44269504f;
+      tsum2 = make_float2(c * fmaf(sum2.x, d, tsum2.x), c * fmaf(sum2.y, d, tsum2.y));
+      sum2 = make_float2(c * sum2.x, c * sum2.y);
+      mx = cm;
+    }
+    // Differences in units of log2, two values per packed operation (the loop
+    // was bound by instructions: 14 a value without). One of -inf is lifted to
+    // -288, whose term is 0 in fp32 as well (0 * inf would not be); a NaN stays
+    // one, and +inf becomes one (inf - inf).
+    const float ref = mx == -CUDART_INF_F ? 0.0f : mx;
+    const float2 nref = make_float2(-ref, -ref), log2e = make_float2(1.44269504f, 1.44269504f);
+#pragma unroll
+    for (int i = 0; i < C::kPer; i += 2) {
+      float2 d = __fmul2_rn(__fadd2_rn(make_float2(cur.at(i), cur.at(i + 1)), nref), log2e);
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(d.x) : "f"(d.x), "f"(-288.0f));
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(d.y) : "f"(d.y), "f"(-288.0f));
+      float2 e;
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(d.x));
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(d.y));
+      sum2 = __fadd2_rn(sum2, e);
+      tsum2 = __ffma2_rn(e, d, tsum2);
+    }
+    if (a.top > 0) {
+      // the values around the vectors come last, the head's with lower indices
+      // than the list's: equal to tau they may still be among the best
+      const bool ties = step >= chunks;
+      const bool has = cm > tau || (ties && cm == tau && cm > -CUDART_INF_F);
+      if (has) {
+#pragma unroll
+        for (int i = 0; i < kLpVecs; ++i) S.own[i][tid] = cur.v[i];
+      }
+      // Until the list is full every chunk is ranked. From then on values above
+      // its last are collected, about `top` a chunk, and ranked now and then.
+      if (tau == -CUDART_INF_F) {
+        if (__syncthreads_or(has)) tau = lp_take<kBf16>(S, cm, tau, ties, index0(step), a.top);
+      } else {
+        if (has) lp_append<kBf16>(S, tau, ties, index0(step));
+        // ranked after 2, 4, 8, ... chunks (each time the rate of values above
+        // the last of the list halves), at the end, and when many wait
+        const bool twice = (step & (step + 1)) == 0 || step + 1 == steps;
+        if (twice || step % 4 == 3) {
+          __syncthreads();
+          const int n = S.count;
+          over |= n > kLpCap;
+          if (!over && (n > kLpCap / 4 || (n > 0 && twice))) tau = lp_rank(S, a.top);
+          else __syncthreads();
+        }
+      }
+    }
+    cur = nxt;
+  }
+  if (over) {
+    // more candidates than the buffer holds (ascending values): once more, chunk by chunk
+    __syncthreads();
+    if (tid < kLpTop) S.list[tid] = 0;
+    if (tid == 0) S.count = 0;
+    __syncthreads();
+    tau = -CUDART_INF_F;
+    for (int step = 0; step < steps; ++step) {
+      load(cur, step);
+      const float cm = cur.max();
+      const bool ties = step >= chunks, has = cm > tau || (ties && cm == tau && cm > -CUDART_INF_F);
+      if (has) {
+#pragma unroll
+        for (int i = 0; i < kLpVecs; ++i) S.own[i][tid] = cur.v[i];
+      }
+      if (__syncthreads_or(has)) tau = lp_take<kBf16>(S, cm, tau, ties, index0(step), a.top);
+    }
+  }
+  float sum = sum2.x + sum2.y, tsum = (tsum2.x + tsum2.y) * 0.693147181f;
+  lp_join_warp(mx, sum, tsum);
+  __syncthreads();
+  if (lane == 0) {
+    S.wm[warp] = mx;
+    S.wS[warp] = sum;
+    S.wT[warp] = tsum;
+  }
+  __syncthreads();
+  mx = S.wm[0];
+  sum = S.wS[0];
+  tsum = S.wT[0];
+#pragma unroll
+  for (int w = 1; w < kLpWarps; ++w) lp_join(mx, sum, tsum, S.wm[w], S.wS[w], S.wT[w]);
+  if (a.splits == 1) {
+    lp_outputs<kBf16>(a, m, row, mx, sum, tsum, S.list, tid, kLpThreads, id, x_id);
+  } else {
+    if (tid == 0) a.stats[m * a.splits + split] = make_float4(mx, sum, tsum, 0.0f);
+    if (tid < a.top) a.keys[(m * a.splits + split) * a.top + tid] = S.list[tid];
+  }
+}
+
+// The pieces of a row as one: a warp per row, a lane per piece. The pieces'
+// keys are sorted, so the largest of the lanes' heads is the next alternative.
+template <bool kBf16>
+__global__ void __launch_bounds__(32) token_logprobs_join_kernel(const LpArgs a) {
+  __shared__ uint64_t list[kLpTop], keys[kLpMaxSplits * kLpTop];
+  const int lane = threadIdx.x;
+  const int64_t m = blockIdx.x;
+  const char* row = reinterpret_cast<const char*>(a.logits) + m * a.ldl * (kBf16 ? 2 : 4);
+  // ids and logits are inputs of both kernels: gathered before the wait
+  const int64_t id = lane < a.G ? a.ids[m * a.G + lane] : -1;
+  const float x_id = id < 0 || id >= a.V ? 0.0f : lp_load<kBf16>(row, id);
+  griddep_wait();
+  const bool has = lane < a.splits;
+  float mx = -CUDART_INF_F, S = 0.0f, T = 0.0f;
+  if (has) {
+    const float4 s = a.stats[m * a.splits + lane];
+    mx = s.x;
+    S = s.y;
+    T = s.z;
+  }
+  const int all = a.splits * a.top;
+#pragma unroll 8
+  for (int i = lane; i < all; i += 32) keys[i] = a.keys[m * all + i];
+  lp_join_warp(mx, S, T);
+  __syncwarp();
+  int taken = 0;
+  uint64_t head = has && a.top > 0 ? keys[lane * a.top] : 0;
+  for (int t = 0; t < a.top; ++t) {
+    const uint64_t best = warp_max_u64(head);
+    if (lane == 0) list[t] = best;
+    if (best != 0 && head == best) {  // keys differ: one lane
+      ++taken;
+      head = taken < a.top ? keys[lane * a.top + taken] : 0;
+    }
+  }
+  __syncwarp();
+  lp_outputs<kBf16>(a, m, row, mx, S, T, list, lane, 32, id, x_id);
+}
+
+// Pieces per row: enough CTAs for four on each of 152 SMs, none much shorter
+// than a chunk of 4096 bf16 values (two of fp32). The same on every device,
+// so that the workspace is known without one.
+static int lp_splits(int64_t M, int64_t V) {
+  const int64_t want = ceil_div(608, M), most = ceil_div(V, 4096);
+  const int64_t s = want < most ? want : most;
+  return (int)(s < 1 ? 1 : s > kLpMaxSplits ? kLpMaxSplits : s);
+}
+
+struct LpWs {
+  int64_t off_keys, total;
+  LpWs(int64_t M, int64_t V, int top) {
+    const int64_t n = lp_splits(M, V) > 1 ? M * lp_splits(M, V) : 0;
+    off_keys = align_up(n * 16, 256);
+    total = align_up(off_keys + n * top * 8, 256);
+    if (total == 0) total = 256;
+  }
+};
+
+int64_t token_logprobs_ws_bytes(int64_t M, int64_t V, int top) { return LpWs(M, V, top).total; }
+
+template <bool kBf16>
+static cudaError_t launch_lp(const LpArgs& a, int64_t M, cudaStream_t st) {
+  // rows over grid.y and z (y is limited to 65535)
+  const int64_t rows_y = M < 32768 ? M : 32768;
+  for (int64_t m0 = 0; m0 < M;) {
+    const int64_t z = M - m0 >= rows_y ? (M - m0) / rows_y : 1, y = M - m0 >= rows_y ? rows_y : M - m0;
+    LpArgs b = a;
+    const int64_t rows = y * z;
+    b.logits = reinterpret_cast<const char*>(a.logits) + m0 * a.ldl * (kBf16 ? 2 : 4);
+    if (a.ids) b.ids = a.ids + m0 * a.G;
+    if (a.logprobs) b.logprobs = a.logprobs + m0 * a.G;
+    if (a.entropy) b.entropy = a.entropy + m0;
+    if (a.top_ids) b.top_ids = a.top_ids + m0 * a.top;
+    if (a.top_logprobs) b.top_logprobs = a.top_logprobs + m0 * a.top;
+    b.stats = a.stats + m0 * a.splits;
+    b.keys = a.keys + m0 * a.splits * a.top;
+    token_logprobs_kernel<kBf16>
+        <<<dim3((unsigned)a.splits, (unsigned)y, (unsigned)z), kLpThreads, 0, st>>>(b);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && a.splits > 1)
+      e = launch_kernel(token_logprobs_join_kernel<kBf16>, dim3((unsigned)rows), dim3(32), 0, st, true, b);
+    if (e != cudaSuccess) return e;
+    m0 += rows;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_token_logprobs(const void* logits, bool bf16, int64_t M, int64_t V, int64_t ldl,
                                   const int64_t* ids, int64_t G, float* logprobs, float* entropy,
                                   int top, int64_t* top_ids, float* top_logprobs, void* ws,
                                   cudaStream_t st) {
-  (void)ws;
-  if (bf16)
-    logprobs_plain_kernel<true><<<(unsigned)M, 256, 0, st>>>(logits, V, ldl, ids, (int)G, logprobs,
-                                                             entropy, top, top_ids, top_logprobs);
-  else
-    logprobs_plain_kernel<false><<<(unsigned)M, 256, 0, st>>>(logits, V, ldl, ids, (int)G, logprobs,
-                                                              entropy, top, top_ids, top_logprobs);
-  return cudaGetLastError();
-}
-
-int64_t token_logprobs_ws_bytes(int64_t M, int64_t V, int top) {
-  (void)M; (void)V; (void)top;
-  return 256;
+  const LpWs w(M, V, top);
+  LpArgs a{logits, V, ldl, ids, logprobs, entropy, top_ids, top_logprobs,
+           reinterpret_cast<float4*>(ws),
+           reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(ws) + w.off_keys),
+           (int)G, top, lp_splits(M, V)};
+  return bf16 ? launch_lp<true>(a, M, st) : launch_lp<false>(a, M, st);
 }
 
 }  // namespace qg
