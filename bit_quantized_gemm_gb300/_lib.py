@@ -5,6 +5,7 @@ CUDA kernels. PyTorch tensors provide device memory and the current stream.
 If the shared library is missing this module raises -- there is no fallback.
 """
 import ctypes
+import functools
 import os
 import re
 
@@ -305,77 +306,98 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _raw_stream(stream, device):
+    """The cudaStream_t of `stream`, or of the current stream of `device`, as a number."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None:
+        return _current_raw_stream(device)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# torch's own number of the current stream, without the Stream object around it (the calls below
+# are short next to the kernels of a decode step: 9-12 us of host time in place of 20-26)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+_BF16, _F32, _FP8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+_CODES = {_BF16: QG_BF16, _F32: QG_F32}
+
+
 def _rows(t, name, dtypes):
-    """A cuda matrix of one of `dtypes` whose rows are contiguous."""
-    if not t.is_cuda or t.dim() != 2 or t.dtype not in dtypes or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("%s must be a 2-D cuda tensor of %s with contiguous rows" %
-                         (name, " or ".join(str(d) for d in dtypes)))
-    return t
+    """(rows, columns, row stride) of a cuda matrix of one of `dtypes` whose rows are contiguous."""
+    if t.is_cuda and t.dtype in dtypes and t.dim() == 2:
+        m, n = t.shape
+        ld, step = t.stride()
+        if step == 1 or n <= 1:
+            # (of a single row torch keeps any stride)
+            return m, n, ld if m > 1 else max(n, ld)
+    raise ValueError("%s must be a 2-D cuda tensor of %s with contiguous rows" %
+                     (name, " or ".join(str(d) for d in dtypes)))
 
 
-def _ld(t):
-    """Row stride of a matrix (of a single row: its length, whatever stride torch keeps for it)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+def _fp8_scale(scale, M, K):
+    """Row stride of the scales [ceil(K/128), M] of activations [M, K]."""
+    kb, m, ld = _rows(scale, "scale", (_F32,))
+    if kb != (K + 127) // 128 or m != M:
+        raise ValueError("scale must have the shape [ceil(K/128), M]")
+    # a single block of K has one row of scales: any stride does
+    return ld if kb > 1 else (M + 3) // 4 * 4
 
 
-_FLOATS = (torch.bfloat16, torch.float32)
-_FP8 = (torch.float8_e4m3fn,)
-
-
-def _fp8_weights(w, w_scale, K, out, M, out_dtype, stream):
-    _rows(w, "w", _FP8)
-    N = w.shape[0]
-    if w.shape[1] != K:
-        raise ValueError("w has rows of %d values, the activations of %d" % (w.shape[1], K))
-    if (not w_scale.is_cuda or w_scale.dtype != torch.float32 or not w_scale.is_contiguous()
-            or tuple(w_scale.shape) != ((N + 127) // 128, (K + 127) // 128)):
+def _fp8_weights(w, w_scale, M, K, out, out_dtype, stream):
+    """(N, row stride of w, out, its row stride), checked; `out` is allocated when None."""
+    N, k, ldw = _rows(w, "w", (_FP8,))
+    if k != K:
+        raise ValueError("w has rows of %d values, the activations of %d" % (k, K))
+    if (not w_scale.is_cuda or w_scale.dtype != _F32 or not w_scale.is_contiguous()
+            or w_scale.shape != ((N + 127) // 128, (K + 127) // 128)):
         raise ValueError("w_scale must be a contiguous cuda fp32 tensor of shape [ceil(N/128), ceil(K/128)]")
     if out is None:
-        return _empty((M, N), out_dtype, w.device, stream)
-    if tuple(_rows(out, "out", _FLOATS).shape) != (M, N):
+        if out_dtype not in _CODES:
+            raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+        return N, ldw, _empty((M, N), out_dtype, w.device, stream), N
+    m, n, ldo = _rows(out, "out", _CODES)
+    if m != M or n != N:
         raise ValueError("out must have the shape (%d, %d)" % (M, N))
-    return out
+    return N, ldw, out, ldo
 
 
 def quantize_act_fp8(x, out=None, stream=None):
     """x: cuda [M, K] bf16/fp32 (rows may be strided; K % 16 == 0) -> (q float8_e4m3fn [M, K],
     scale fp32 [ceil(K/128), M], one per token and 128 values of K; its rows start on 16-byte
     boundaries). `out` may supply preallocated (q, scale)."""
-    M, K = _rows(x, "x", _FLOATS).shape
+    M, K, ldx = _rows(x, "x", _CODES)
     if out is None:
-        q = _empty((M, K), torch.float8_e4m3fn, x.device, stream)
-        scale = _empty(((K + 127) // 128, (M + 3) // 4 * 4), torch.float32, x.device, stream)[:, :M]
+        dev, lds = x.device, (M + 3) // 4 * 4
+        q = _empty((M, K), _FP8, dev, stream)
+        scale = _empty(((K + 127) // 128, lds), _F32, dev, stream)
+        if lds != M:
+            scale = scale[:, :M]
     else:
         q, scale = out
-        if _rows(q, "q", _FP8).shape != x.shape or not q.is_contiguous():
+        if _rows(q, "q", (_FP8,)) != (M, K, K):
             raise ValueError("q must be contiguous and of the shape of x")
-        if tuple(_rows(scale, "scale", (torch.float32,)).shape) != ((K + 127) // 128, M):
-            raise ValueError("scale must have the shape [ceil(K/128), M]")
-    _check(load().qg_quantize_act_fp8(_ptr(x), _dtype_code(x.dtype), M, K, _ld(x), _ptr(q),
-                                      _ptr(scale), _fp8_lds(scale), _stream(stream)))
+        lds = _fp8_scale(scale, M, K)
+    _check((_lib or load()).qg_quantize_act_fp8(x.data_ptr(), _CODES[x.dtype], M, K, ldx, q.data_ptr(),
+                                                scale.data_ptr(), lds, _raw_stream(stream, x.get_device())))
     return q, scale
-
-
-def _fp8_lds(scale):
-    # a single block of K has one row of scales: any stride does
-    return scale.stride(0) if scale.shape[0] > 1 else (scale.shape[1] + 3) // 4 * 4
 
 
 def gemm_fp8(q, scale, w, w_scale, out=None, out_dtype=torch.bfloat16, stream=None):
     """q, scale from quantize_act_fp8; w: cuda float8_e4m3fn [N, K] as stored (rows may be strided);
     w_scale: cuda fp32 [ceil(N/128), ceil(K/128)] -> out [M, N]."""
-    M, K = _rows(q, "q", _FP8).shape
-    if not q.is_contiguous():
+    M, K, ldq = _rows(q, "q", (_FP8,))
+    if ldq != K:
         raise ValueError("q must be contiguous")
-    if tuple(_rows(scale, "scale", (torch.float32,)).shape) != ((K + 127) // 128, M):
-        raise ValueError("scale must have the shape [ceil(K/128), M]")
-    out = _fp8_weights(w, w_scale, K, out, M, out_dtype, stream)
-    _check(load().qg_gemm_fp8(_ptr(q), _ptr(scale), _fp8_lds(scale), M, K, _ptr(w), _ld(w),
-                              _ptr(w_scale), w.shape[0], _ptr(out), _dtype_code(out.dtype), _ld(out),
-                              _stream(stream)))
+    lds = _fp8_scale(scale, M, K)
+    N, ldw, out, ldo = _fp8_weights(w, w_scale, M, K, out, out_dtype, stream)
+    _check((_lib or load()).qg_gemm_fp8(q.data_ptr(), scale.data_ptr(), lds, M, K, w.data_ptr(), ldw,
+                                        w_scale.data_ptr(), N, out.data_ptr(), _CODES[out.dtype], ldo,
+                                        _raw_stream(stream, q.get_device())))
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def linear_fp8_workspace_bytes(M, K):
     """Workspace bytes a linear_fp8 call of these sizes needs (0: invalid sizes)."""
     return int(load().qg_linear_fp8_workspace_bytes(M, K))
@@ -384,17 +406,20 @@ def linear_fp8_workspace_bytes(M, K):
 def linear_fp8(x, w, w_scale, out=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
     """The whole layer: x cuda [M, K] bf16/fp32 -> out [M, N] with e4m3 weights (see gemm_fp8).
     Quantize, then GEMM, through `workspace` (allocated here when not given)."""
-    M, K = _rows(x, "x", _FLOATS).shape
-    out = _fp8_weights(w, w_scale, K, out, M, out_dtype, stream)
+    M, K, ldx = _rows(x, "x", _CODES)
+    N, ldw, out, ldo = _fp8_weights(w, w_scale, M, K, out, out_dtype, stream)
     if workspace is None:
-        workspace = _empty((linear_fp8_workspace_bytes(M, K),), torch.uint8, x.device, stream)
-    _check(load().qg_linear_fp8(_ptr(x), _dtype_code(x.dtype), M, K, _ld(x), _ptr(w), _ld(w),
-                                _ptr(w_scale), w.shape[0], _ptr(out), _dtype_code(out.dtype), _ld(out),
-                                _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                _stream(stream)))
+        nbytes = linear_fp8_workspace_bytes(M, K)
+        workspace = _empty((nbytes,), torch.uint8, x.device, stream)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    _check((_lib or load()).qg_linear_fp8(x.data_ptr(), _CODES[x.dtype], M, K, ldx, w.data_ptr(), ldw,
+                                          w_scale.data_ptr(), N, out.data_ptr(), _CODES[out.dtype], ldo,
+                                          workspace.data_ptr(), nbytes, _raw_stream(stream, x.get_device())))
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def token_logprobs_workspace_bytes(M, V, top):
     """Workspace bytes a token_logprobs call of these sizes needs (0: invalid sizes)."""
     return int(load().qg_token_logprobs_workspace_bytes(M, V, top))
@@ -405,22 +430,27 @@ def token_logprobs(logits, ids, top=0, workspace=None, stream=None):
     token) -> (logprobs fp32 of ids' shape, entropy fp32 [M], top_ids int64 [M, top], top_logprobs
     fp32 [M, top]): log probabilities of the given tokens, the rows' entropies in nats and their
     `top` likeliest tokens, ties to the lowest id; -1 where a row has fewer (see include/qgemm.h)."""
-    M, V = _rows(logits, "logits", _FLOATS).shape
-    if (not ids.is_cuda or ids.dtype != torch.int64 or ids.dim() not in (1, 2) or ids.shape[0] != M
+    M, V, ldl = _rows(logits, "logits", _CODES)
+    shape = ids.shape
+    if (not ids.is_cuda or ids.dtype != torch.int64 or len(shape) not in (1, 2) or shape[0] != M
             or not ids.is_contiguous()):
         raise ValueError("ids must be a contiguous cuda int64 tensor of shape [M] or [M, G]")
-    G = ids.shape[1] if ids.dim() == 2 else 1
-    dev = logits.device
-    logprobs = _empty(ids.shape, torch.float32, dev, stream)
-    entropy = _empty((M,), torch.float32, dev, stream)
-    top_ids = _empty((M, max(top, 0)), torch.int64, dev, stream)
-    top_logprobs = _empty((M, max(top, 0)), torch.float32, dev, stream)
+    G = shape[1] if len(shape) == 2 else 1
+    dev, k = logits.device, max(top, 0)
+    logprobs = _empty(shape, _F32, dev, stream)
+    entropy = _empty((M,), _F32, dev, stream)
+    top_ids = _empty((M, k), torch.int64, dev, stream)
+    top_logprobs = _empty((M, k), _F32, dev, stream)
     if workspace is None:
-        workspace = _empty((token_logprobs_workspace_bytes(M, V, top),), torch.uint8, dev, stream)
-    _check(load().qg_token_logprobs(_ptr(logits), _dtype_code(logits.dtype), M, V, _ld(logits), _ptr(ids),
-                                    G, _ptr(logprobs), _ptr(entropy), top, _ptr(top_ids),
-                                    _ptr(top_logprobs), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream)))
+        nbytes = token_logprobs_workspace_bytes(M, V, top)
+        workspace = _empty((nbytes,), torch.uint8, dev, stream)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    _check((_lib or load()).qg_token_logprobs(logits.data_ptr(), _CODES[logits.dtype], M, V, ldl,
+                                              ids.data_ptr(), G, logprobs.data_ptr(), entropy.data_ptr(),
+                                              top, top_ids.data_ptr(), top_logprobs.data_ptr(),
+                                              workspace.data_ptr(), nbytes,
+                                              _raw_stream(stream, logits.get_device())))
     return logprobs, entropy, top_ids, top_logprobs
 
 
