@@ -190,11 +190,11 @@ struct LpChunk {
 
 struct LpShared {
   uint4 own[kLpVecs][kLpThreads];  // values of the threads that have candidates
-  uint64_t cand[kLpCap + kLpTop];  // candidates, then (to be ranked) the list so far
-  uint64_t list[kLpTop];           // the best so far, descending, 0: none
+  uint64_t cand[kLpCap];           // candidates
+  uint64_t list[2][kLpTop];        // the best so far, descending, 0: none; the other one is 0
   uint64_t red[kLpWarps];
   float wm[kLpWarps], wS[kLpWarps], wT[kLpWarps];
-  int count;                       // candidates, also those past the buffer's end
+  int count[2];                    // candidates, also those past the buffer's end
 };
 
 // value i of the thread, from S.own, and its row index (i0: that of value 0)
@@ -212,7 +212,7 @@ __device__ __forceinline__ uint32_t lp_index(uint32_t i0, int i) {
 // candidates, in no particular order: they are ranked by their keys. (Calls of
 // their own from here on: rare, and inlined they took the main loop's registers.)
 template <bool kBf16>
-__device__ __noinline__ void lp_append(LpShared& S, float low, bool ties, uint32_t i0) {
+__device__ __noinline__ void lp_append(LpShared& S, int cur, float low, bool ties, uint32_t i0) {
   using C = LpChunk<kBf16>;
 #pragma unroll 1
   for (int i = 0; i < kLpVecs; ++i) {
@@ -223,44 +223,48 @@ __device__ __noinline__ void lp_append(LpShared& S, float low, bool ties, uint32
     for (int j = 0; j < C::kVec; ++j) {
       const float x = C::value(q, j);
       if (x > low || (ties && x == low)) {
-        const int p = atomicAdd(&S.count, 1);
+        const int p = atomicAdd(&S.count[cur], 1);
         if (p < kLpCap) S.cand[p] = lp_key(x, lp_index<kBf16>(i0, i * C::kVec + j));
       }
     }
   }
 }
 
-// The candidates (no more than fit) and the list as the new list; returns its
-// last value, -inf while it is not full. Called by the whole CTA after a
-// barrier that follows the last append.
-__device__ __noinline__ float lp_rank(LpShared& S, int top) {
-  const int tid = threadIdx.x, n = S.count;
-  if (tid < top) S.cand[n + tid] = S.list[tid];
-  __syncthreads();
-  if (tid < top) S.list[tid] = 0;
-  if (tid == 0) S.count = 0;
-  __syncthreads();
+__device__ __forceinline__ float lp_last(const LpShared& S, int cur, int top) {
+  const uint64_t k = S.list[cur][top - 1];
+  return k == 0 ? -CUDART_INF_F : lp_value(k);
+}
+
+// Ranks the candidates (no more than fit) and list `cur` into list 1 - cur and
+// returns its last value, -inf while it is not full. List and count `cur` are
+// left at 0 for the round after. Called by the whole CTA after a barrier that
+// follows the last append.
+__device__ __noinline__ float lp_rank(LpShared& S, int cur, int top) {
+  const int tid = threadIdx.x, n = S.count[cur];
   // the rank of a key is the number of larger ones (keys differ, empty ones aside)
   for (int i = tid; i < n + top; i += kLpThreads) {
-    const uint64_t k = S.cand[i];
+    const uint64_t k = i < n ? S.cand[i] : S.list[cur][i - n];
     if (k == 0) continue;
     int rank = 0;
 #pragma unroll 4
-    for (int j = 0; j < n + top; ++j) rank += S.cand[j] > k;
-    if (rank < top) S.list[rank] = k;
+    for (int j = 0; j < n; ++j) rank += S.cand[j] > k;
+    for (int j = 0; j < top; ++j) rank += S.list[cur][j] > k;
+    if (rank < top) S.list[1 - cur][rank] = k;
   }
   __syncthreads();
-  const uint64_t k = S.list[top - 1];
-  return k == 0 ? -CUDART_INF_F : lp_value(k);
+  if (tid < kLpTop) S.list[cur][tid] = 0;
+  if (tid == 0) S.count[cur] = 0;
+  return lp_last(S, 1 - cur, top);
 }
 
 // Takes a chunk's values above `tau` (the last of the list's values, -inf while
 // it is not full; with `ties`, values at tau as well) into the list, whatever
-// their number, and returns the new tau. Threads whose maximum mx qualifies
-// have left their values in S.own. No candidates are pending. Called by the
+// their number: list `cur` becomes list 1 - cur, whose last value is returned.
+// Threads whose maximum mx qualifies have left their values in S.own. No candidates are pending. Called by the
 // whole CTA.
 template <bool kBf16>
-__device__ __noinline__ float lp_take(LpShared& S, float mx, float tau, bool ties, uint32_t i0, int top) {
+__device__ __noinline__ float lp_take(LpShared& S, int cur, float mx, float tau, bool ties, uint32_t i0,
+                                      int top) {
   using C = LpChunk<kBf16>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // While the list is not full, a lower bound of its last value: with r =
@@ -284,20 +288,15 @@ __device__ __noinline__ float lp_take(LpShared& S, float mx, float tau, bool tie
     ties = low > -CUDART_INF_F;
   }
   const bool has = mx > low || (ties && mx == low);
-  if (has) lp_append<kBf16>(S, low, ties, i0);
+  if (has) lp_append<kBf16>(S, cur, low, ties, i0);
   __syncthreads();
-  const int n = S.count;
-  if (n <= kLpCap) return lp_rank(S, top);
+  if (S.count[cur] <= kLpCap) return lp_rank(S, cur, top);
   // more candidates than fit (many equal or ascending values): the largest key
   // below the last one, `top` times
-  __syncthreads();
-  if (tid < top) S.cand[tid] = S.list[tid];
-  if (tid == 0) S.count = 0;
-  __syncthreads();
   uint64_t last = ~0ull;
   for (int t = 0; t < top; ++t) {
     uint64_t best = 0;
-    if (tid < top && S.cand[tid] < last) best = S.cand[tid];
+    if (tid < top && S.list[cur][tid] < last) best = S.list[cur][tid];
     if (has) {
 #pragma unroll 4
       for (int i = 0; i < C::kPer; ++i) {
@@ -312,11 +311,12 @@ __device__ __noinline__ float lp_take(LpShared& S, float mx, float tau, bool tie
 #pragma unroll
     for (int w = 0; w < kLpWarps; ++w) best = S.red[w] > best ? S.red[w] : best;
     last = best;
-    if (tid == 0) S.list[t] = best;  // (0 once there are no more)
+    if (tid == 0) S.list[1 - cur][t] = best;  // (0 once there are no more)
     __syncthreads();
   }
-  const uint64_t k = S.list[top - 1];
-  return k == 0 ? -CUDART_INF_F : lp_value(k);
+  if (tid < kLpTop) S.list[cur][tid] = 0;
+  if (tid == 0) S.count[cur] = 0;
+  return lp_last(S, 1 - cur, top);
 }
 
 template <bool kBf16>
@@ -342,8 +342,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
   const int around = split == 0 ? (int)(head + a.V - tail) : 0;
   const int steps = chunks + (around > 0);
   const int64_t mine = tid < head ? tid : tail + tid - head;  // this thread's value around the vectors
-  if (tid < kLpTop) S.list[tid] = 0;
-  if (tid == 0) S.count = 0;
+  if (tid < 2 * kLpTop) S.list[tid / kLpTop][tid % kLpTop] = 0;
+  if (tid < 2) S.count[tid] = 0;
+  int cur_list = 0;
+  bool pending = false;  // this thread has candidates that are not ranked yet
   __syncthreads();
 
   float mx = -CUDART_INF_F, tau = -CUDART_INF_F;
@@ -403,28 +405,33 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
       // Until the list is full every chunk is ranked. From then on values above
       // its last are collected, about `top` a chunk, and ranked now and then.
       if (tau == -CUDART_INF_F) {
-        if (__syncthreads_or(has)) tau = lp_take<kBf16>(S, cm, tau, ties, index0(step), a.top);
+        if (__syncthreads_or(has)) {
+          tau = lp_take<kBf16>(S, cur_list, cm, tau, ties, index0(step), a.top);
+          cur_list ^= 1;
+        }
       } else {
-        if (has) lp_append<kBf16>(S, tau, ties, index0(step));
+        if (has) lp_append<kBf16>(S, cur_list, tau, ties, index0(step));
+        pending |= has;
         // ranked after 2, 4, 8, ... chunks (each time the rate of values above
-        // the last of the list halves), at the end, and when many wait
-        const bool twice = (step & (step + 1)) == 0 || step + 1 == steps;
-        if (twice || step % 4 == 3) {
-          __syncthreads();
-          const int n = S.count;
-          over |= n > kLpCap;
-          if (!over && (n > kLpCap / 4 || (n > 0 && twice))) tau = lp_rank(S, a.top);
-          else __syncthreads();
+        // the last of the list halves) and at the end
+        if (((step & (step + 1)) == 0 || step + 1 == steps) && __syncthreads_or(pending)) {
+          over |= S.count[cur_list] > kLpCap;
+          if (!over) {
+            tau = lp_rank(S, cur_list, a.top);
+            cur_list ^= 1;
+            pending = false;
+          }
         }
       }
     }
     cur = nxt;
   }
   if (over) {
-    // more candidates than the buffer holds (ascending values): once more, chunk by chunk
+    // more candidates than the buffer holds (ascending values): once more, chunk
+    // by chunk
     __syncthreads();
-    if (tid < kLpTop) S.list[tid] = 0;
-    if (tid == 0) S.count = 0;
+    if (tid < 2 * kLpTop) S.list[tid / kLpTop][tid % kLpTop] = 0;
+    if (tid < 2) S.count[tid] = 0;
     __syncthreads();
     tau = -CUDART_INF_F;
     for (int step = 0; step < steps; ++step) {
@@ -435,7 +442,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
 #pragma unroll
         for (int i = 0; i < kLpVecs; ++i) S.own[i][tid] = cur.v[i];
       }
-      if (__syncthreads_or(has)) tau = lp_take<kBf16>(S, cm, tau, ties, index0(step), a.top);
+      if (__syncthreads_or(has)) {
+        tau = lp_take<kBf16>(S, cur_list, cm, tau, ties, index0(step), a.top);
+        cur_list ^= 1;
+      }
     }
   }
   float sum = sum2.x + sum2.y, tsum = (tsum2.x + tsum2.y) * 0.693147181f;
@@ -453,10 +463,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
 #pragma unroll
   for (int w = 1; w < kLpWarps; ++w) lp_join(mx, sum, tsum, S.wm[w], S.wS[w], S.wT[w]);
   if (a.splits == 1) {
-    lp_outputs<kBf16>(a, m, row, mx, sum, tsum, S.list, tid, kLpThreads, id, x_id);
+    lp_outputs<kBf16>(a, m, row, mx, sum, tsum, S.list[cur_list], tid, kLpThreads, id, x_id);
   } else {
     if (tid == 0) a.stats[m * a.splits + split] = make_float4(mx, sum, tsum, 0.0f);
-    if (tid < a.top) a.keys[(m * a.splits + split) * a.top + tid] = S.list[tid];
+    if (tid < a.top) a.keys[(m * a.splits + split) * a.top + tid] = S.list[cur_list][tid];
   }
 }
 
