@@ -12,7 +12,7 @@ from ._lib import (QGError, check_device_error, debug_block_sums, debug_wait_tim
                    q4k_packed_bytes, q8_0_packed_bytes, quantize_act, quantize_act_static,
                    small_m_max,
                    gemm_fp8, linear_fp8, linear_fp8_workspace_bytes, quantize_act_fp8,
-                   token_logprobs, token_logprobs_workspace_bytes)
+                   token_logprobs)
 
 __all__ = ["QGError", "check_device_error", "debug_block_sums", "debug_wait_timeout",
            "declared_symbols", "gemm_launch_count",
@@ -23,4 +23,4 @@ __all__ = ["QGError", "check_device_error", "debug_block_sums", "debug_wait_time
            "q4k_packed_bytes", "q8_0_packed_bytes", "quantize_act", "quantize_act_static",
            "small_m_max",
            "gemm_fp8", "linear_fp8", "linear_fp8_workspace_bytes", "quantize_act_fp8",
-           "token_logprobs", "token_logprobs_workspace_bytes"]
+           "token_logprobs"]

@@ -73,8 +73,7 @@ def load():
         "qg_gemm_fp8": ([P, P, I64, I64, I64, P, I64, P, I64, P, I, I64, P], I),
         "qg_linear_fp8_workspace_bytes": ([I64, I64], SZ),
         "qg_linear_fp8": ([P, I, I64, I64, I64, P, I64, P, I64, P, I, I64, P, SZ, P], I),
-        "qg_token_logprobs_workspace_bytes": ([I64, I64, I], SZ),
-        "qg_token_logprobs": ([P, I, I64, I64, I64, P, I64, P, P, I, P, P, P, SZ, P], I),
+        "qg_token_logprobs": ([P, I, I64, I64, I64, P, I64, P, P, I, P, P, P], I),
     }
     for name, (args, res) in sigs.items():
         f = getattr(L, name)
@@ -419,13 +418,7 @@ def linear_fp8(x, w, w_scale, out=None, out_dtype=torch.bfloat16, workspace=None
     return out
 
 
-@functools.lru_cache(maxsize=4096)
-def token_logprobs_workspace_bytes(M, V, top):
-    """Workspace bytes a token_logprobs call of these sizes needs (0: invalid sizes)."""
-    return int(load().qg_token_logprobs_workspace_bytes(M, V, top))
-
-
-def token_logprobs(logits, ids, top=0, workspace=None, stream=None):
+def token_logprobs(logits, ids, top=0, stream=None):
     """logits: cuda [M, V] bf16/fp32 (rows may be strided); ids: cuda int64 [M, G] or [M] (-1: no
     token) -> (logprobs fp32 of ids' shape, entropy fp32 [M], top_ids int64 [M, top], top_logprobs
     fp32 [M, top]): log probabilities of the given tokens, the rows' entropies in nats and their
@@ -441,15 +434,9 @@ def token_logprobs(logits, ids, top=0, workspace=None, stream=None):
     entropy = _empty((M,), _F32, dev, stream)
     top_ids = _empty((M, k), torch.int64, dev, stream)
     top_logprobs = _empty((M, k), _F32, dev, stream)
-    if workspace is None:
-        nbytes = token_logprobs_workspace_bytes(M, V, top)
-        workspace = _empty((nbytes,), torch.uint8, dev, stream)
-    else:
-        nbytes = workspace.numel() * workspace.element_size()
     _check((_lib or load()).qg_token_logprobs(logits.data_ptr(), _CODES[logits.dtype], M, V, ldl,
                                               ids.data_ptr(), G, logprobs.data_ptr(), entropy.data_ptr(),
                                               top, top_ids.data_ptr(), top_logprobs.data_ptr(),
-                                              workspace.data_ptr(), nbytes,
                                               _raw_stream(stream, logits.get_device())))
     return logprobs, entropy, top_ids, top_logprobs
 

@@ -51,11 +51,9 @@ cudaError_t launch_gemm_fp8(const uint8_t* q, const float* scale, int64_t lds, i
                             const uint8_t* w, int64_t ldw, const float* w_scale, int64_t N,
                             void* out, bool out_f32, int64_t ldo, uint32_t* err, bool pdl,
                             cudaStream_t st);
-int64_t token_logprobs_ws_bytes(int64_t M, int64_t V, int top);
 cudaError_t launch_token_logprobs(const void* logits, bool bf16, int64_t M, int64_t V, int64_t ldl,
                                   const int64_t* ids, int64_t G, float* logprobs, float* entropy,
-                                  int top, int64_t* top_ids, float* top_logprobs, void* ws,
-                                  cudaStream_t st);
+                                  int top, int64_t* top_ids, float* top_logprobs, cudaStream_t st);
 }  // namespace qg
 
 using namespace qg;
@@ -641,21 +639,12 @@ qg_status qg_linear_fp8(const void* x, qg_dtype x_dtype, int64_t M, int64_t K, i
                    "FP8 GEMM launch");
 }
 
-static bool logprobs_sizes_ok(int64_t M, int64_t V, int top) {
-  return M >= 1 && M <= kMaxM && V >= 1 && V <= kMaxV && top >= 0 && top <= QG_LOGPROBS_MAX_TOP;
-}
-
-size_t qg_token_logprobs_workspace_bytes(int64_t M, int64_t V, int top) {
-  return logprobs_sizes_ok(M, V, top) ? (size_t)token_logprobs_ws_bytes(M, V, top) : 0;
-}
-
 qg_status qg_token_logprobs(const void* logits, qg_dtype dtype, int64_t M, int64_t V, int64_t ldl,
                             const int64_t* ids, int64_t G, float* logprobs, float* entropy,
-                            int top, int64_t* top_ids, float* top_logprobs, void* workspace,
-                            size_t workspace_bytes, void* stream) {
+                            int top, int64_t* top_ids, float* top_logprobs, void* stream) {
   if (!logits) return fail(QG_EINVAL, "null pointer argument");
   if (dtype != QG_BF16 && dtype != QG_F32) return fail(QG_EINVAL, "dtype must be QG_BF16 or QG_F32");
-  if (!logprobs_sizes_ok(M, V, top))
+  if (M < 1 || M > kMaxM || V < 1 || V > kMaxV || top < 0 || top > QG_LOGPROBS_MAX_TOP)
     return fail(QG_EINVAL, "M=%lld, V=%lld must be in [1, 2^24] and top=%d in [0, %d]", (long long)M,
                 (long long)V, top, QG_LOGPROBS_MAX_TOP);
   if (G < 0 || G > kMaxGiven) return fail(QG_EINVAL, "G=%lld out of range [0, 2^16]", (long long)G);
@@ -667,13 +656,8 @@ qg_status qg_token_logprobs(const void* logits, qg_dtype dtype, int64_t M, int64
       (logprobs && !aligned(logprobs, 4)) || (entropy && !aligned(entropy, 4)) ||
       (top_ids && !aligned(top_ids, 8)) || (top_logprobs && !aligned(top_logprobs, 4)))
     return fail(QG_EALIGN, "every array needs the alignment of its elements");
-  const int64_t need = token_logprobs_ws_bytes(M, V, top);
-  if (!workspace || workspace_bytes < (size_t)need)
-    return fail(QG_EINVAL, "workspace of %lld bytes needed (qg_token_logprobs_workspace_bytes)",
-                (long long)need);
-  if (!aligned(workspace, 256)) return fail(QG_EALIGN, "workspace needs 256-byte alignment");
   return from_cuda(launch_token_logprobs(logits, dtype == QG_BF16, M, V, ldl, ids, G, logprobs,
-                                         entropy, top, top_ids, top_logprobs, workspace,
+                                         entropy, top, top_ids, top_logprobs,
                                          reinterpret_cast<cudaStream_t>(stream)),
                    "log-probability launch");
 }

@@ -21,8 +21,13 @@
 // inverted index) and only looks at values above the last of them: the first
 // chunk, where a threshold comes from the warps' maxima, is ranked at once, and
 // from then on the few values that pass (about `top` for each doubling of the
-// length) are collected without a barrier and ranked now and then. A second
-// kernel joins the pieces.
+// length) are collected without a barrier and ranked after 2, 4, 8, ... chunks.
+// The pieces of a row are a cluster of CTAs, whose first one joins them.
+//
+// Measured (GB300, bf16, from a CUDA graph): 4096 x 131072 without alternatives
+// 171 us, 6.3 TB/s of 6.69 measured for a copy; with 1, 5, 32 alternatives 196,
+// 218, 303 us (the ranks, during which a CTA reads nothing, and the candidates);
+// 2048 x 131072 fp32, 5 alternatives 179 us; 1 x 131072 4.1 us, with 20 12.6 us.
 #include <math_constants.h>
 
 #include "qg_common.cuh"
@@ -33,9 +38,9 @@ namespace qg {
 // bf16, no alternatives: 167 us, 175 with 256 threads, 209 with 512).
 constexpr int kLpThreads = 128, kLpWarps = kLpThreads / 32, kLpCtas = 8;
 constexpr int kLpVecs = 4;                   // 16-byte loads per thread and chunk
-constexpr int kLpCap = 512;                 // candidates of a chunk that are ranked at once
+constexpr int kLpCap = 512;                  // candidates that are ranked at once
 constexpr int kLpTop = QG_LOGPROBS_MAX_TOP;
-constexpr int kLpMaxSplits = 32;             // a lane each in the joining warp
+constexpr int kLpMaxSplits = 16;             // CTAs of a cluster
 static_assert(kLpTop <= 32 && kLpTop % kLpWarps == 0, "a lane per alternative");
 
 struct LpArgs {
@@ -46,8 +51,6 @@ struct LpArgs {
   float* entropy;
   int64_t* top_ids;
   float* top_logprobs;
-  float4* stats;      // [M][splits] m, S, T
-  uint64_t* keys;     // [M][splits][top], descending, 0: none
   int G, top, splits;
 };
 
@@ -195,6 +198,8 @@ struct LpShared {
   uint64_t red[kLpWarps];
   float wm[kLpWarps], wS[kLpWarps], wT[kLpWarps];
   int count[2];                    // candidates, also those past the buffer's end
+  uint64_t final_list[kLpTop];     // what the row's first CTA reads of a piece
+  float stats[3];
 };
 
 // value i of the thread, from S.own, and its row index (i0: that of value 0)
@@ -323,7 +328,6 @@ template <bool kBf16>
 __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(const LpArgs a) {
   using C = LpChunk<kBf16>;
   __shared__ LpShared S;
-  griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t m = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
   const int split = blockIdx.x;
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
   if (steps > 0) load(cur, 0);
   // a given id and its logit take two trips to memory: the first now, the
   // second after the first chunk
-  const int64_t id = a.splits == 1 && tid < a.G ? a.ids[m * a.G + tid] : -1;
+  const int64_t id = split == 0 && tid < a.G ? a.ids[m * a.G + tid] : -1;
   float x_id = 0.0f;
   for (int step = 0; step < steps; ++step) {
     C nxt;
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
         for (int i = 0; i < kLpVecs; ++i) S.own[i][tid] = cur.v[i];
       }
       // Until the list is full every chunk is ranked. From then on values above
-      // its last are collected, about `top` a chunk, and ranked now and then.
+      // its last are collected.
       if (tau == -CUDART_INF_F) {
         if (__syncthreads_or(has)) {
           tau = lp_take<kBf16>(S, cur_list, cm, tau, ties, index0(step), a.top);
@@ -464,108 +468,103 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
   for (int w = 1; w < kLpWarps; ++w) lp_join(mx, sum, tsum, S.wm[w], S.wS[w], S.wT[w]);
   if (a.splits == 1) {
     lp_outputs<kBf16>(a, m, row, mx, sum, tsum, S.list[cur_list], tid, kLpThreads, id, x_id);
-  } else {
-    if (tid == 0) a.stats[m * a.splits + split] = make_float4(mx, sum, tsum, 0.0f);
-    if (tid < a.top) a.keys[(m * a.splits + split) * a.top + tid] = S.list[cur_list][tid];
+    return;
   }
-}
-
-// The pieces of a row as one: a warp per row, a lane per piece. The pieces'
-// keys are sorted, so the largest of the lanes' heads is the next alternative.
-template <bool kBf16>
-__global__ void __launch_bounds__(32) token_logprobs_join_kernel(const LpArgs a) {
-  __shared__ uint64_t list[kLpTop], keys[kLpMaxSplits * kLpTop];
-  const int lane = threadIdx.x;
-  const int64_t m = blockIdx.x;
-  const char* row = reinterpret_cast<const char*>(a.logits) + m * a.ldl * (kBf16 ? 2 : 4);
-  // ids and logits are inputs of both kernels: gathered before the wait
-  const int64_t id = lane < a.G ? a.ids[m * a.G + lane] : -1;
-  const float x_id = id < 0 || id >= a.V ? 0.0f : lp_load<kBf16>(row, id);
-  griddep_wait();
-  const bool has = lane < a.splits;
-  float mx = -CUDART_INF_F, S = 0.0f, T = 0.0f;
-  if (has) {
-    const float4 s = a.stats[m * a.splits + lane];
-    mx = s.x;
-    S = s.y;
-    T = s.z;
+  // The pieces of a row are a cluster: the first CTA joins them, a lane per
+  // piece. Their keys are sorted, so the largest of the lanes' heads is the next
+  // alternative.
+  if (tid < a.top) S.final_list[tid] = S.list[cur_list][tid];
+  if (tid == 0) {
+    S.stats[0] = mx;
+    S.stats[1] = sum;
+    S.stats[2] = tsum;
   }
-  const int all = a.splits * a.top;
-#pragma unroll 8
-  for (int i = lane; i < all; i += 32) keys[i] = a.keys[m * all + i];
-  lp_join_warp(mx, S, T);
-  __syncwarp();
-  int taken = 0;
-  uint64_t head = has && a.top > 0 ? keys[lane * a.top] : 0;
-  for (int t = 0; t < a.top; ++t) {
-    const uint64_t best = warp_max_u64(head);
-    if (lane == 0) list[t] = best;
-    if (best != 0 && head == best) {  // keys differ: one lane
-      ++taken;
-      head = taken < a.top ? keys[lane * a.top + taken] : 0;
+  cluster_sync();
+  if (split == 0) {
+    for (int i = tid; i < a.splits * a.top; i += kLpThreads)
+      S.cand[i] = ld_cluster_u64(map_to_cta(&S.final_list[i % a.top], i / a.top));
+    __syncthreads();
+    if (warp == 0) {
+      const bool has = lane < a.splits;
+      const uint32_t st = map_to_cta(S.stats, has ? lane : 0);
+      mx = has ? ld_cluster_f32(st) : -CUDART_INF_F;
+      sum = has ? ld_cluster_f32(st + 4) : 0.0f;
+      tsum = has ? ld_cluster_f32(st + 8) : 0.0f;
+      lp_join_warp(mx, sum, tsum);
+      int taken = 0;
+      uint64_t head = has && a.top > 0 ? S.cand[lane * a.top] : 0;
+      for (int t = 0; t < a.top; ++t) {
+        const uint64_t best = warp_max_u64(head);
+        if (lane == 0) S.final_list[t] = best;
+        if (best != 0 && head == best) {  // keys differ: one lane
+          ++taken;
+          head = taken < a.top ? S.cand[lane * a.top + taken] : 0;
+        }
+      }
+      __syncwarp();
+      lp_outputs<kBf16>(a, m, row, mx, sum, tsum, S.final_list, lane, 32, id, x_id);
     }
   }
-  __syncwarp();
-  lp_outputs<kBf16>(a, m, row, mx, S, T, list, lane, 32, id, x_id);
+  cluster_sync();  // a piece's shared memory outlives its reading
 }
 
-// Pieces per row: enough CTAs for four on each of 152 SMs, none much shorter
-// than a chunk of 4096 bf16 values (two of fp32). The same on every device,
-// so that the workspace is known without one.
+// Pieces per row, a power of two: doubled while there are fewer than 3.75 CTAs
+// an SM (100 x 131072 bf16, top 5: 18.3 us, 27.8 up to 1.25 an SM; 300 x 50001:
+// 21.9 us, 29.6 up to 4), none much shorter than a chunk of 4096 bf16 values
+// (two of fp32).
 static int lp_splits(int64_t M, int64_t V) {
-  const int64_t want = ceil_div(608, M), most = ceil_div(V, 4096);
-  const int64_t s = want < most ? want : most;
-  return (int)(s < 1 ? 1 : s > kLpMaxSplits ? kLpMaxSplits : s);
+  int s = 1;
+  while (s < kLpMaxSplits && M * s * 4 < 15 * (int64_t)num_sms() && V > 4096 * (int64_t)s) s *= 2;
+  return s;
 }
-
-struct LpWs {
-  int64_t off_keys, total;
-  LpWs(int64_t M, int64_t V, int top) {
-    const int64_t n = lp_splits(M, V) > 1 ? M * lp_splits(M, V) : 0;
-    off_keys = align_up(n * 16, 256);
-    total = align_up(off_keys + n * top * 8, 256);
-    if (total == 0) total = 256;
-  }
-};
-
-int64_t token_logprobs_ws_bytes(int64_t M, int64_t V, int top) { return LpWs(M, V, top).total; }
 
 template <bool kBf16>
 static cudaError_t launch_lp(const LpArgs& a, int64_t M, cudaStream_t st) {
+  auto kern = token_logprobs_kernel<kBf16>;
+  if (a.splits > 8) {  // clusters of more than eight CTAs have to be asked for
+    static std::atomic<uint64_t> attr_set{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+    if (!bit || !(attr_set.load(std::memory_order_acquire) & bit)) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      attr_set.fetch_or(bit, std::memory_order_release);
+    }
+  }
   // rows over grid.y and z (y is limited to 65535)
   const int64_t rows_y = M < 32768 ? M : 32768;
   for (int64_t m0 = 0; m0 < M;) {
     const int64_t z = M - m0 >= rows_y ? (M - m0) / rows_y : 1, y = M - m0 >= rows_y ? rows_y : M - m0;
     LpArgs b = a;
-    const int64_t rows = y * z;
     b.logits = reinterpret_cast<const char*>(a.logits) + m0 * a.ldl * (kBf16 ? 2 : 4);
     if (a.ids) b.ids = a.ids + m0 * a.G;
     if (a.logprobs) b.logprobs = a.logprobs + m0 * a.G;
     if (a.entropy) b.entropy = a.entropy + m0;
     if (a.top_ids) b.top_ids = a.top_ids + m0 * a.top;
     if (a.top_logprobs) b.top_logprobs = a.top_logprobs + m0 * a.top;
-    b.stats = a.stats + m0 * a.splits;
-    b.keys = a.keys + m0 * a.splits * a.top;
-    token_logprobs_kernel<kBf16>
-        <<<dim3((unsigned)a.splits, (unsigned)y, (unsigned)z), kLpThreads, 0, st>>>(b);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && a.splits > 1)
-      e = launch_kernel(token_logprobs_join_kernel<kBf16>, dim3((unsigned)rows), dim3(32), 0, st, true, b);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.splits, (unsigned)y, (unsigned)z);
+    cfg.blockDim = dim3(kLpThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)a.splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.splits > 1 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, b);
     if (e != cudaSuccess) return e;
-    m0 += rows;
+    m0 += y * z;
   }
   return cudaSuccess;
 }
 
 cudaError_t launch_token_logprobs(const void* logits, bool bf16, int64_t M, int64_t V, int64_t ldl,
                                   const int64_t* ids, int64_t G, float* logprobs, float* entropy,
-                                  int top, int64_t* top_ids, float* top_logprobs, void* ws,
-                                  cudaStream_t st) {
-  const LpWs w(M, V, top);
-  LpArgs a{logits, V, ldl, ids, logprobs, entropy, top_ids, top_logprobs,
-           reinterpret_cast<float4*>(ws),
-           reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(ws) + w.off_keys),
-           (int)G, top, lp_splits(M, V)};
+                                  int top, int64_t* top_ids, float* top_logprobs, cudaStream_t st) {
+  const LpArgs a{logits, V, ldl, ids, logprobs, entropy, top_ids, top_logprobs, (int)G, top, lp_splits(M, V)};
   return bf16 ? launch_lp<true>(a, M, st) : launch_lp<false>(a, M, st);
 }
 

@@ -352,16 +352,12 @@ qg_status qg_linear_fp8(const void* x, qg_dtype x_dtype, int64_t M, int64_t K, i
 /*   entropy  [M] fp32, or NULL.                                              */
 /*   top_ids  [M][top] int64, top_logprobs [M][top] fp32, 0 <= top <=         */
 /*            QG_LOGPROBS_MAX_TOP; both may be NULL when top is 0.            */
-/*   workspace  at least qg_token_logprobs_workspace_bytes(M, V, top) bytes,  */
-/*            256-byte aligned (0 bytes: the sizes are invalid).              */
 /* 1 <= M <= 2^24, 1 <= V <= 2^24, 0 <= G <= 2^16.                            */
 /* ------------------------------------------------------------------------ */
 #define QG_LOGPROBS_MAX_TOP 32
-size_t qg_token_logprobs_workspace_bytes(int64_t M, int64_t V, int top);
 qg_status qg_token_logprobs(const void* logits, qg_dtype dtype, int64_t M, int64_t V, int64_t ldl,
                             const int64_t* ids, int64_t G, float* logprobs, float* entropy,
-                            int top, int64_t* top_ids, float* top_logprobs, void* workspace,
-                            size_t workspace_bytes, void* stream);
+                            int top, int64_t* top_ids, float* top_logprobs, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Test support: the exact per-block integer sums as the chosen kernel sees   */

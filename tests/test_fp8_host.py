@@ -81,25 +81,16 @@ def test_linear_workspace(L):
     (dict(x=0), EINVAL), (dict(dt=5), EINVAL), (dict(M=0), EINVAL), (dict(V=0), EINVAL),
     (dict(V=2**24 + 1, ldl=2**25), EINVAL), (dict(ldl=99), EINVAL), (dict(G=-1), EINVAL),
     (dict(G=2**16 + 1), EINVAL), (dict(ids=0), EINVAL), (dict(lp=0), EINVAL), (dict(top=33), EINVAL),
-    (dict(top=-1), EINVAL), (dict(ti=0), EINVAL), (dict(tl=0), EINVAL), (dict(work=0), EINVAL),
-    (dict(nbytes=-1), EINVAL), (dict(x=FAKE + 1), EALIGN), (dict(ids=FAKE + 4), EALIGN),
-    (dict(ent=FAKE + 2), EALIGN), (dict(ti=FAKE + 4), EALIGN), (dict(work=FAKE + 16), EALIGN),
+    (dict(top=-1), EINVAL), (dict(ti=0), EINVAL), (dict(tl=0), EINVAL),
+    (dict(x=FAKE + 1), EALIGN), (dict(ids=FAKE + 4), EALIGN),
+    (dict(ent=FAKE + 2), EALIGN), (dict(ti=FAKE + 4), EALIGN),
 ])
 def test_logprobs_refusals(L, kw, status):
-    a = dict(x=FAKE, dt=0, M=4, V=100, ldl=100, ids=FAKE, G=2, lp=FAKE, ent=FAKE, top=5, ti=FAKE, tl=FAKE,
-             work=FAKE, nbytes=0)
+    a = dict(x=FAKE, dt=0, M=4, V=100, ldl=100, ids=FAKE, G=2, lp=FAKE, ent=FAKE, top=5, ti=FAKE, tl=FAKE)
     a.update(kw)
-    need = L.qg_token_logprobs_workspace_bytes(4, 100, 5)
-    assert need > 0
     assert L.qg_token_logprobs(P(a["x"]), a["dt"], a["M"], a["V"], a["ldl"], P(a["ids"]), a["G"], P(a["lp"]),
-                               P(a["ent"]), a["top"], P(a["ti"]), P(a["tl"]), P(a["work"]),
-                               need + a["nbytes"], None) == status
+                               P(a["ent"]), a["top"], P(a["ti"]), P(a["tl"]), None) == status
     assert L.qg_last_error().decode()
-
-
-def test_logprobs_workspace_of_invalid_sizes(L):
-    for M, V, top in [(0, 10, 0), (1, 0, 0), (1, 10, 33), (1, 10, -1), (1, 2**24 + 1, 0)]:
-        assert L.qg_token_logprobs_workspace_bytes(M, V, top) == 0
 
 
 def test_binding_refuses_tensors_it_cannot_use():
