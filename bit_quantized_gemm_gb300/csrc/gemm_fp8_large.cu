@@ -594,8 +594,8 @@ cudaError_t launch_gemm_fp8(const uint8_t* q, const float* scale, int64_t lds, i
                             const uint8_t* w, int64_t ldw, const float* w_scale, int64_t N,
                             void* out, bool out_f32, int64_t ldo, uint32_t* err, bool pdl,
                             cudaStream_t st) {
-  // up to 64 tokens stream the weights (64 x 5120 x 17408: 19.4 us, 19.3 here; 64 x
-  // 17408 x 5120: 37.2 us, 41.9 here)
+  // up to 64 tokens stream the weights (64 x 5120 x 17408: 18.7 us, 19.3 here; 64 x
+  // 17408 x 5120: 26.6 us, 41.9 here)
   if (M <= 64)
     return launch_gemm_fp8_small(q, scale, lds, M, K, w, ldw, w_scale, N, out, out_f32, ldo, err,
                                  pdl, st);

@@ -5,16 +5,31 @@
 //
 // Bound by reading the weights once: N*K bytes. So the weights are the MMA's
 // long operand (R rows in tensor-memory lanes) and the tokens its short one
-// (BM columns), and every CTA streams its R rows along K through a TMA ring
-// as deep as shared memory allows. Each block of 128 accumulates from zero in
-// its own tensor-memory buffer (BM columns), and the epilogue warps apply the
-// chain while the next blocks' MMAs run: a thread owns one weight row and up
-// to 32 tokens, the token scales come through the ring with the operands, the
-// weight scale is one number per tile and block.
-// The chain of an output is not split over CTAs, so its bits do not depend on
-// the batch or the tile.
+// (BM columns), and every CTA streams the rows of its tiles along K through a
+// TMA ring as deep as shared memory allows; the ring runs on from tile to tile.
+// Each block of 128 accumulates from zero in its own tensor-memory buffer (BM
+// columns), and the epilogue warps apply the chain while the next blocks' MMAs
+// run. The chain of an output is not split over CTAs, so its bits do not depend
+// on the batch or the tile.
 //
-// Warps: 0 TMA producer, 1 MMA issuer, then the epilogue (4 per 32 tokens).
+// The epilogue reads tensor memory as 16-lane fragments: a thread has 2 (R = 64)
+// or 4 weight rows and a quarter of the tokens, so that all lanes of a 64-row
+// tile have work, and a token's scale is read from shared memory once for those
+// rows (17408 -> 5120, 64 tokens: 31 us; 37 with one row and 32 tokens a thread).
+// The scales come through the ring with the operands, the weight scale is one
+// number per tile and block.
+//
+// An MMA of this size takes 56 cycles from one issuing thread; each block of a
+// stage has an issuing warp of its own (17408 -> 5120, 1 token: 20.5 us with one
+// warp, 19.2 with two, 17.9 with four).
+//
+// Measured (from a CUDA graph): 16 tokens, 4096 -> 131072: 80.8 us, 6.69 TB/s,
+// what a copy reaches; 64 tokens 85.6 us; 5120 -> 17408: 16.8 us, 18.7 with 64
+// tokens, of which about 4 are a launch's fixed share; 17408 -> 5120: 17.7 us and
+// 26.6 (80 tiles, each 136 blocks after one another: 163 cycles of MMAs a block,
+// 200 to 340 with the handshakes and the loads).
+//
+// Warps: 0 TMA producer, 1..G MMA issuers, then the epilogue (4 per 32 tokens).
 #include <cuda.h>
 
 #include "qg_common.cuh"
@@ -38,26 +53,28 @@ constexpr int kFp8SmallMaxStages = 16;
 
 // G blocks of K share a ring stage, a group of tensor-memory buffers and their
 // barriers: a barrier wait costs 100-200 cycles beside running MMAs, more than
-// the MMAs of one block of few tokens.
+// the MMAs of one block of few tokens. (Of 128 rows and more than 16 tokens, a
+// stage of four would leave a ring of two: 32 tokens, 5120 -> 17408 19.6 us, 17.2
+// with stages of two.)
 template <int R, int BM>
 struct Fp8SmallCfg {
-  static constexpr int G = BM <= 32 ? 4 : 2;
+  static constexpr int G = R == 128 && BM > 16 ? 2 : 4;
   static constexpr uint32_t kW = R * 128, kQ = BM * 128, kS = BM * 4;
   static constexpr uint32_t kStage = G * (kW + kQ + kS);
-  // groups of buffers: 256 columns, so that two CTAs can share an SM
-  static constexpr int kGroups = 256 / (G * BM);
-  static constexpr uint32_t kCols = kGroups * G * BM;
+  // groups of buffers: four, or what fits (the CTA has the SM's 512 columns)
+  static constexpr uint32_t kCols = 4 * G * BM < 512 ? 4 * G * BM : 512;
+  static constexpr int kGroups = kCols / (G * BM);
   // epilogue warps: four (a quarter of the lanes each) per 32 columns
-  static constexpr int kCpt = BM < 32 ? BM : 32;  // columns per thread
-  static constexpr int kEpi = 4 * (BM / kCpt);
-  static constexpr int kThreads = 64 + 32 * kEpi;
-  static_assert(kGroups >= 2 && (kCols & (kCols - 1)) == 0, "tensor memory");
+  static constexpr int kCpt = BM < 32 ? BM : 32;  // columns per warp
+  static constexpr int kEpi = 4 * (BM / kCpt), kEpi0 = 1 + G;
+  static constexpr int kThreads = 32 * (kEpi0 + kEpi);
+  static_assert(kGroups >= 2 && kGroups <= 4, "tensor memory");
 };
 
 struct Fp8SmallBars {
   uint64_t full[kFp8SmallMaxStages], empty[kFp8SmallMaxStages];
   uint64_t tfull[4], tempty[4];
-  uint64_t mdrain;
+  uint64_t mdrain[4];  // [issuer]
   uint32_t tmem_base, tmem_busy;
 };
 
@@ -78,18 +95,19 @@ __global__ void __launch_bounds__(Fp8SmallCfg<R, BM>::kThreads)
   uint8_t* sq = sw + stages * G * C::kW;         // token tiles [stage][G]
   uint8_t* ss = sq + stages * G * C::kQ;         // token scales [stage][G][BM]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n0 = blockIdx.x * R, m0 = blockIdx.y * BM;
+  const int tiles = (a.N + R - 1) / R, step = gridDim.x;
+  const int total = (tiles - (int)blockIdx.x + step - 1) / step * NS;  // stages of this CTA's tiles
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
       mbar_init(&S.full[i], 1);
-      mbar_init(&S.empty[i], 1 + C::kEpi);  // the MMAs' commit and the epilogue warps (scales)
+      mbar_init(&S.empty[i], G + C::kEpi);  // the issuers' commits and the epilogue warps (scales)
     }
     for (int i = 0; i < C::kGroups; ++i) {
-      mbar_init(&S.tfull[i], 1);
+      mbar_init(&S.tfull[i], G);
       mbar_init(&S.tempty[i], C::kEpi);
     }
-    mbar_init(&S.mdrain, 1);
+    for (int i = 0; i < G; ++i) mbar_init(&S.mdrain[i], 1);
     S.tmem_busy = 0;
     fence_barrier_init();
   }
@@ -108,7 +126,7 @@ __global__ void __launch_bounds__(Fp8SmallCfg<R, BM>::kThreads)
   const uint32_t tmem = S.tmem_base;
 
   if (warp == 0) {
-    auto load_w = [&](int i, int s) {
+    auto load_w = [&](int n0, int i, int s) {
       mbar_arrive_expect_tx(&S.full[s], C::kStage);
 #pragma unroll
       for (int g = 0; g < G; ++g)
@@ -117,34 +135,37 @@ __global__ void __launch_bounds__(Fp8SmallCfg<R, BM>::kThreads)
     auto load_q = [&](int i, int s) {
 #pragma unroll
       for (int g = 0; g < G; ++g)
-        tma_load_2d(sq + (s * G + g) * C::kQ, &tmQ, &S.full[s], (i * G + g) * 128, m0);
-      tma_load_2d(ss + s * G * C::kS, &tmS, &S.full[s], m0, i * G);
+        tma_load_2d(sq + (s * G + g) * C::kQ, &tmQ, &S.full[s], (i * G + g) * 128, 0);
+      tma_load_2d(ss + s * G * C::kS, &tmS, &S.full[s], 0, i * G);
+    };
+    int n0 = blockIdx.x * R, i = 0;  // tile and stage of K
+    auto next = [&] {
+      if (++i == NS) { i = 0; n0 += step * R; }
     };
     // the first round of the ring: as a programmatic dependent of the
     // quantize kernel, the weights are requested before the wait for its grid
-    const int P = min(NS, stages);
-    for (int i = 0; i < P; ++i)
+    const int P = min(total, stages);
+    for (int l = 0; l < P; ++l, next())
       if (elect_one()) {
-        load_w(i, i);
-        if (!a.pdl) load_q(i, i);
+        load_w(n0, i, l);
+        if (!a.pdl) load_q(i, l);
       }
     if (a.pdl) {
       griddep_wait();
-      for (int i = 0; i < P; ++i)
-        if (elect_one()) load_q(i, i);
+      for (int l = 0; l < P; ++l)
+        if (elect_one()) load_q(l % NS, l);
     }
     bool ok = true;
     int s = 0;
     uint32_t phase = 0;
     int last = P;  // loads issued
-    for (int i = P; i < NS; ++i) {
+    for (; last < total; ++last, next()) {
       ok = mbar_wait_warp(&S.empty[s], phase, a.err);
       if (!ok) break;
       if (elect_one()) {
-        load_w(i, s);
+        load_w(n0, i, s);
         load_q(i, s);
       }
-      ++last;
       if (++s == stages) { s = 0; phase ^= 1; }
     }
     // every load has landed and (unless a wait gave up) every stage has been
@@ -153,25 +174,24 @@ __global__ void __launch_bounds__(Fp8SmallCfg<R, BM>::kThreads)
       mbar_wait_warp(&S.full[i % stages], (uint32_t)(i / stages) & 1u, a.err);
       if (ok) mbar_wait_warp(&S.empty[i % stages], (uint32_t)(i / stages) & 1u, a.err);
     }
-  } else if (warp == 1) {
+  } else if (warp <= G) {
+    // one block of every stage
     constexpr uint32_t idesc = idesc_e4m3_f32(R, BM);
+    const int g = warp - 1;
     int s = 0, t = 0;
     uint32_t phase = 0, tphase = 1;
     bool ok = true;
-    for (int i = 0; i < NS; ++i) {
+    for (int i = 0; i < total; ++i) {
       ok = mbar_wait_warp2(&S.full[s], phase, &S.tempty[t], tphase, a.err);
       if (!ok) break;
       tc_fence_after();
+      const uint32_t wa = smem_u32(sw + (s * G + g) * C::kW);
+      const uint32_t qa = smem_u32(sq + (s * G + g) * C::kQ);
       if (elect_one()) {
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const uint32_t wa = smem_u32(sw + (s * G + g) * C::kW);
-          const uint32_t qa = smem_u32(sq + (s * G + g) * C::kQ);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_e4m3_ss(tmem + (t * G + g) * BM, smem_desc_sw128(wa + k * 32),
-                        smem_desc_sw128(qa + k * 32), idesc, k);
-        }
+        for (int k = 0; k < 4; ++k)
+          mma_e4m3_ss(tmem + (t * G + g) * BM, smem_desc_sw128(wa + k * 32),
+                      smem_desc_sw128(qa + k * 32), idesc, k);
         mma_commit(&S.tfull[t]);
         mma_commit(&S.empty[s]);
       }
@@ -180,86 +200,101 @@ __global__ void __launch_bounds__(Fp8SmallCfg<R, BM>::kThreads)
       if (++t == C::kGroups) { t = 0; tphase ^= 1; }
     }
     if (!ok) {
-      if (elect_one()) mma_commit(&S.mdrain);
+      if (elect_one()) mma_commit(&S.mdrain[g]);
       __syncwarp();
-      if (!mbar_wait_warp(&S.mdrain, 0, a.err)) atomicExch(&S.tmem_busy, 1u);
+      if (!mbar_wait_warp(&S.mdrain[g], 0, a.err)) atomicExch(&S.tmem_busy, 1u);
     }
   } else {
-    const int quarter = warp & 3, c0 = ((warp - 2) >> 2) * C::kCpt;  // lanes and columns of this warp
+    const int quarter = warp & 3, c0 = ((warp - C::kEpi0) >> 2) * C::kCpt;  // lanes and columns of this warp
     constexpr int kCpt = C::kCpt;
-    // M = 128: row i in lane i; M = 64: rows 16w.. in the first lanes of quarter w
-    const int n = n0 + quarter * (R / 4) + lane;
-    const bool nvalid = lane < R / 4 && n < a.N;
+    constexpr int H = R / 64;  // 16-lane halves of the quarter in use
+    // R = 128: row i in lane i; R = 64: rows 16w.. in the first lanes of quarter w
+    const int row = quarter * (R / 4) + (lane >> 2);
     // the weight scales of 32 blocks, one per lane, the next 32 on their way
     // (a tile lies inside one block of rows)
-    const float* wsp = a.w_scale + (int64_t)(n0 >> 7) * KB;
-    float w_cur = lane < KB ? __ldg(wsp + lane) : 0.0f;
-    float w_nxt = 32 + lane < KB ? ldg_f32_pinned(wsp + 32 + lane) : 0.0f;
+    auto scales = [&](int tile) { return a.w_scale + (int64_t)(tile * R >> 7) * KB; };
+    float w_first = lane < KB ? __ldg(scales(blockIdx.x) + lane) : 0.0f;  // a tile's first
     if (a.pdl) griddep_wait();  // the output may be what an earlier kernel still reads
-    float acc[kCpt];
-#pragma unroll
-    for (int j = 0; j < kCpt; ++j) acc[j] = 0.0f;
     int s = 0, t = 0;
     uint32_t phase = 0, tphase = 0;
     bool ok = true;
-    for (int i = 0; i < NS; ++i) {
-      ok = mbar_wait_warp2(&S.full[s], phase, &S.tfull[t], tphase, a.err);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + t * G * BM + c0;
-      const float* sc = reinterpret_cast<const float*>(ss + s * G * C::kS) + c0;
+    for (int tile = blockIdx.x; tile < tiles && ok; tile += step) {
+      const float* wsp = scales(tile);
+      float w_cur = w_first;
+      float w_nxt = 32 + lane < KB ? ldg_f32_pinned(wsp + 32 + lane) : 0.0f;
+      if (tile + step < tiles && lane < KB) w_first = ldg_f32_pinned(scales(tile + step) + lane);
+      float acc[H][kCpt / 2];
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int b = i * G + g;
-        const float wsc = __shfl_sync(0xffffffffu, w_cur, b & 31);
-        if ((b & 31) == 31) {
-          w_cur = w_nxt;
-          w_nxt = b + 33 + lane < KB ? ldg_f32_pinned(wsp + b + 33 + lane) : 0.0f;
-        }
-        const float2 w2 = make_float2(wsc, wsc);
-        uint32_t v[kCpt];
-        tmem_ld(taddr + g * BM, v);
-        float2 f[kCpt / 2];
+      for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int j = 0; j < kCpt; j += 4) {
-          const float4 f4 = *reinterpret_cast<const float4*>(sc + g * BM + j);
-          f[j / 2] = __fmul2_rn(make_float2(f4.x, f4.y), w2);
-          f[j / 2 + 1] = __fmul2_rn(make_float2(f4.z, f4.w), w2);
-        }
-        tmem_wait_ld();
+        for (int j = 0; j < kCpt / 2; ++j) acc[h][j] = 0.0f;
+      for (int i = 0; i < NS; ++i) {
+        ok = mbar_wait_warp2(&S.full[s], phase, &S.tfull[t], tphase, a.err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + t * G * BM + c0;
+        const float* sc = reinterpret_cast<const float*>(ss + s * G * C::kS) + c0 + 2 * (lane & 3);
 #pragma unroll
-        for (int j = 0; j < kCpt; ++j) asm volatile("" : "+r"(v[j]));
-        if (g + 1 == G) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&S.tempty[t]);
-            mbar_arrive(&S.empty[s]);  // this warp has read the stage's scales, too
+        for (int g = 0; g < G; ++g) {
+          const int b = i * G + g;
+          uint32_t v[H][kCpt / 2];
+#pragma unroll
+          for (int h = 0; h < H; ++h) tmem_ld_frag(taddr + (h << 20) + g * BM, v[h]);
+          const float wsc = __shfl_sync(0xffffffffu, w_cur, b & 31);
+          if ((b & 31) == 31) {
+            w_cur = w_nxt;
+            w_nxt = b + 33 + lane < KB ? ldg_f32_pinned(wsp + b + 33 + lane) : 0.0f;
           }
-        }
-        if (b >= KB) continue;  // past K
+          const float2 w2 = make_float2(wsc, wsc);
+          float2 f[kCpt / 8];
 #pragma unroll
-        for (int j = 0; j < kCpt; j += 2) {
-          const float2 r = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
-                                      f[j / 2], make_float2(acc[j], acc[j + 1]));
-          acc[j] = r.x;
-          acc[j + 1] = r.y;
-        }
-      }
-      if (++s == stages) { s = 0; phase ^= 1; }
-      if (++t == C::kGroups) { t = 0; tphase ^= 1; }
-    }
-    if (ok && nvalid) {
-      const int64_t o = (int64_t)(m0 + c0) * a.ldo + n;
-      const int mc = a.M - m0 - c0;
+          for (int j = 0; j < kCpt / 8; ++j)
+            f[j] = __fmul2_rn(*reinterpret_cast<const float2*>(sc + g * BM + 8 * j), w2);
+          tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < kCpt; ++j) {
-        if (j >= mc) continue;
-        if (a.out_f32)
-          reinterpret_cast<float*>(a.out)[o + j * a.ldo] = acc[j];
-        else
-          reinterpret_cast<uint16_t*>(a.out)[o + j * a.ldo] = f32_to_bf16_rne(acc[j]);
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int j = 0; j < kCpt / 2; ++j) asm volatile("" : "+r"(v[h][j]));
+          if (g + 1 == G) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&S.tempty[t]);
+              mbar_arrive(&S.empty[s]);  // this warp has read the stage's scales, too
+            }
+          }
+          if (b >= KB) continue;  // past K
+#pragma unroll
+          for (int j = 0; j < kCpt / 8; ++j)
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+              for (int u = 0; u < 4; u += 2) {
+                float* ac = acc[h] + 4 * j + u;
+                const float2 r = __ffma2_rn(make_float2(__uint_as_float(v[h][4 * j + u]),
+                                                        __uint_as_float(v[h][4 * j + u + 1])),
+                                            f[j], make_float2(ac[0], ac[1]));
+                ac[0] = r.x;
+                ac[1] = r.y;
+              }
+        }
+        if (++s == stages) { s = 0; phase ^= 1; }
+        if (++t == C::kGroups) { t = 0; tphase ^= 1; }
       }
+      if (!ok) break;
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int j = 0; j < kCpt / 2; ++j) {
+          const int m = c0 + 8 * (j >> 2) + 2 * (lane & 3) + (j & 1);
+          const int n = tile * R + row + 16 * h + 8 * (j >> 1 & 1);
+          if (m >= a.M || n >= a.N) continue;
+          const int64_t o = (int64_t)m * a.ldo + n;
+          if (a.out_f32)
+            reinterpret_cast<float*>(a.out)[o] = acc[h][j];
+          else
+            reinterpret_cast<uint16_t*>(a.out)[o] = f32_to_bf16_rne(acc[h][j]);
+        }
     }
   }
   tc_fence_before();
@@ -280,14 +315,11 @@ static cudaError_t launch_small(const CUtensorMap& tw, const uint8_t* q, const f
       !make_tmap_2d(&ts, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, scale, align_up(a.M, 4), a.KB, lds * 4, BM,
                     C::G, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorNotSupported;
-  const dim3 grid((unsigned)ceil_div(a.N, R), (unsigned)ceil_div(a.M, BM));
-  // one CTA per SM takes the whole shared memory for its ring; two share it
-  const int64_t ctas = (int64_t)grid.x * grid.y;
-  const int budget = (ctas <= num_sms() ? 224 : 110) * 1024 - 1024;
-  int stages = budget / (int)C::kStage;
+  // one CTA per SM, with the whole shared memory for its ring
+  const int64_t tiles = ceil_div(a.N, R);
+  const dim3 grid((unsigned)(tiles < num_sms() ? tiles : num_sms()));
+  int stages = 223 * 1024 / (int)C::kStage;
   stages = stages > kFp8SmallMaxStages ? kFp8SmallMaxStages : stages;
-  const int ns = (int)ceil_div(a.KB, C::G);
-  stages = stages > ns ? ns : stages;
   a.stages = stages;
   const size_t smem = (size_t)stages * C::kStage + 1024;
   auto kern = gemm_fp8_small_kernel<R, BM>;
@@ -302,8 +334,10 @@ cudaError_t launch_gemm_fp8_small(const uint8_t* q, const float* scale, int64_t 
                                   int64_t N, void* out, bool out_f32, int64_t ldo, uint32_t* err,
                                   bool pdl, cudaStream_t st) {
   const int bm = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-  // 128-row tiles read the tokens half as often; 64-row tiles fill the SMs
-  const int r = ceil_div(N, 128) * ceil_div(M, bm) * 4 >= 3 * num_sms() ? 128 : 64;
+  // 64-row tiles while all of them run at once, else 128-row tiles, which read
+  // the tokens half as often (16 tokens: 17408 -> 5120, 80 tiles 17.7 us, 24.4 as 40
+  // of 128; 5120 -> 10000, 157 tiles 13.8 us, 12.6 as 79)
+  const int r = ceil_div(N, 64) <= num_sms() ? 64 : 128;
   CUtensorMap tw;
   if (!make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, K, N, ldw, 128, r,
                     CU_TENSOR_MAP_SWIZZLE_128B))

@@ -27,7 +27,7 @@
 // Measured (GB300, bf16, from a CUDA graph): 4096 x 131072 without alternatives
 // 171 us, 6.3 TB/s of 6.69 measured for a copy; with 1, 5, 32 alternatives 196,
 // 218, 303 us (the ranks, during which a CTA reads nothing, and the candidates);
-// 2048 x 131072 fp32, 5 alternatives 179 us; 1 x 131072 4.1 us, with 20 12.6 us.
+// 2048 x 131072 fp32, 5 alternatives 178 us; 1 x 131072 4.1 us, with 20 12.7 us.
 #include <math_constants.h>
 
 #include "qg_common.cuh"
