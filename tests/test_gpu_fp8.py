@@ -163,6 +163,20 @@ def test_gemm_layer_sizes(m, k, n):
     check_product(qg.gemm_fp8(q, s, w, ws), q, s, w, ws)
 
 
+@pytest.mark.parametrize("m,k,n", [(1, 16, 40000), (9, 400, 30001), (16, 2576, 25003), (32, 144, 48000), (64, 656, 20001)])
+def test_gemm_more_tiles_than_sms(m, k, n):
+    # few tokens and many weight rows: a CTA takes several tiles after one another
+    x = activations(m, 200, k)
+    w, ws = weights(n, n, k)
+    q, s = qg.quantize_act_fp8(x)
+    all_rows = qg.gemm_fp8(q, s, w, ws, out_dtype=torch.float32)
+    out = qg.linear_fp8(x[:m], w, ws, out_dtype=torch.float32)
+    q, s = qg.quantize_act_fp8(x[:m])
+    check_product(out, q, s, w, ws)
+    assert torch.equal(out, all_rows[:m])
+    assert torch.equal(qg.gemm_fp8(q, s, w, ws, out_dtype=torch.float32), out)
+
+
 @pytest.mark.parametrize("m", [1, 5, 64, 130, 600])
 def test_gemm_strides(m):
     # weight rows inside a wider buffer, output rows inside a wider one whose rest stays as it was
