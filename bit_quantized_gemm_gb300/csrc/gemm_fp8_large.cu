@@ -286,7 +286,12 @@ __global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
     // scale warp: s * ws of each block for this CTA's 128 tokens and the (at
     // most two) blocks of weight rows of the tile, so that the epilogue, whose
     // loop bounds the kernel, reads one number per block. Of the weight scales
-    // a lane holds one of 32 blocks, and the next 32 are on their way.
+    // a lane holds one of 32 blocks, and the next 32 are on their way. The
+    // products are formed before the wait for their buffer; with two buffers an
+    // issuer, both blocks of a stage go through one round of waits (single waits,
+    // products after them: 4096 x 5120 x 4864 in pair tiles of 128 columns 95 us,
+    // 83 here).
+    constexpr int U = kSlots == 1 ? 1 : G;
     const int tiles_here = first < tiles ? (tiles - first + step - 1) / step : 0;
     bool ok = true;
     int s = 0;
@@ -312,33 +317,49 @@ __global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
         if (ti + 1 < tiles_here)
           w_first[r] = lane < KB ? ldg_f32_pinned(w_row(tile + step, r) + lane) : 0.0f;
       }
-#pragma unroll (2 * kSlots)
-      for (int b = 0; b < KB; ++b) {
-        const int own = b & 1, buf = own * kSlots + (b >> 1 & (kSlots - 1));
-        const uint32_t par = (used >> buf) & 1u;
-        ok = own ? mbar_wait_warp(&sempty[buf], par, a.err)
-                 : mbar_wait_warp2(&sfull[s], phase, &sempty[buf], par, a.err);
+#pragma unroll (2 * kSlots / U)
+      for (int b = 0; b < KB; b += U) {
+        const int own = U == 1 ? b & 1 : 0, t = b >> 1 & (kSlots - 1);
+        const int buf = own * kSlots + t, buf1 = buf + kSlots;
+        const bool two = U == 2 && b + 1 < KB, last_of_stage = U == 2 || own || b + 1 == KB;
+        if (!own) ok = mbar_wait_warp(&sfull[s], phase, a.err);
         if (!ok) break;
-        const float4 v = *reinterpret_cast<const float4*>(ss + s * C::kScaleBytes + own * 512 + lane * 16);
-        float* f = sf + buf * (C::kScaleRows * 128) + lane * 4;
+        float4 p[U][C::kScaleRows];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float4 v =
+              *reinterpret_cast<const float4*>(ss + s * C::kScaleBytes + (own + u) * 512 + lane * 16);
+#pragma unroll
+          for (int r = 0; r < C::kScaleRows; ++r) {
+            const float w = __shfl_sync(0xffffffffu, w_cur[r], (b + u) & 31);
+            p[u][r] = make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
+            // (done before the wait below)
+            asm volatile("" : "+f"(p[u][r].x), "+f"(p[u][r].y), "+f"(p[u][r].z), "+f"(p[u][r].w));
+          }
+        }
+        const int mine = two && (lane & 1) ? buf1 : buf;
+        ok = mbar_wait_warp(&sempty[mine], (used >> mine) & 1u, a.err);
+        if (!ok) break;
+        float* f = sf + lane * 4;
 #pragma unroll
         for (int r = 0; r < C::kScaleRows; ++r) {
-          const float w = __shfl_sync(0xffffffffu, w_cur[r], b & 31);
-          *reinterpret_cast<float4*>(f + r * 128) = make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
+          *reinterpret_cast<float4*>(f + (buf * C::kScaleRows + r) * 128) = p[0][r];
+          if (two) *reinterpret_cast<float4*>(f + (buf1 * C::kScaleRows + r) * 128) = p[U - 1][r];
         }
         __syncwarp();
-        const bool last_of_stage = own || b + 1 == KB;
         if (lane == 0) {
           mbar_arrive(&tfull[buf]);
+          if (two) mbar_arrive(&tfull[buf1]);
           if (last_of_stage) mbar_arrive(&empty[s]);  // its scales are read
         }
         if (last_of_stage && ++s == C::kStages) { s = 0; phase ^= 1; }
         used ^= 1u << buf;
-        if ((b & 31) == 31) {
+        if (two) used ^= 1u << buf1;
+        if (((b + U) & 31) == 0) {
 #pragma unroll
           for (int r = 0; r < C::kScaleRows; ++r) {
             w_cur[r] = w_nxt[r];
-            w_nxt[r] = b + 33 + lane < KB ? ldg_f32_pinned(wp[r] + b + 33 + lane) : 0.0f;
+            w_nxt[r] = b + U + 32 + lane < KB ? ldg_f32_pinned(wp[r] + b + U + 32 + lane) : 0.0f;
           }
         }
       }
@@ -470,14 +491,17 @@ __global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
           }
         } else {
           __syncwarp();
+          // 32 columns of a row at a time, or 16 of two rows
+          constexpr int kRows = 32 / C::kRound;
           const int rows = min(32, a.M - mrow0), cols = min(C::kRound, a.N - nc0 - c0);
-          const int byte = lane * C::kEsize;
+          const int col = lane % C::kRound, byte = col * C::kEsize;
 #pragma unroll 4
-          for (int r = 0; r < rows; ++r) {
+          for (int r0 = 0; r0 < rows; r0 += kRows) {
+            const int r = r0 + lane / C::kRound;
             const uint8_t* p =
                 stage + r * C::kRowBytes + (((byte >> 4) ^ ((r >> 1) & 3)) << 4) + (byte & 15);
-            const int64_t o = (int64_t)(mrow0 + r) * a.ldo + nc0 + c0 + lane;
-            if (lane >= cols) continue;
+            const int64_t o = (int64_t)(mrow0 + r) * a.ldo + nc0 + c0 + col;
+            if (r >= rows || col >= cols) continue;
             if constexpr (kF32)
               reinterpret_cast<float*>(a.out)[o] = *reinterpret_cast<const float*>(p);
             else
@@ -571,7 +595,7 @@ static cudaError_t launch_large_any(const uint8_t* q, int64_t K, const uint8_t* 
     int w;
     double step;
   };
-  static const Choice kChoices[] = {{true, 256, 472}, {true, 128, 280}, {false, 128, 292}, {false, 64, 240}};
+  static const Choice kChoices[] = {{true, 256, 481}, {true, 128, 252}, {false, 128, 276}, {false, 64, 236}};
   const int sms = num_sms();
   int best = 0;
   double best_t = 1e300;
