@@ -219,7 +219,8 @@ __device__ __forceinline__ uint32_t lp_index(uint32_t i0, int i) {
 template <bool kBf16>
 __device__ __noinline__ void lp_append(LpShared& S, int cur, float low, bool ties, uint32_t i0) {
   using C = LpChunk<kBf16>;
-#pragma unroll 1
+  uint32_t hits = 0;  // bit per value: one atomic per thread, not one per value
+#pragma unroll
   for (int i = 0; i < kLpVecs; ++i) {
     const uint4 q = S.own[i][threadIdx.x];
     const float vm = C::max_of(q);
@@ -227,11 +228,13 @@ __device__ __noinline__ void lp_append(LpShared& S, int cur, float low, bool tie
 #pragma unroll
     for (int j = 0; j < C::kVec; ++j) {
       const float x = C::value(q, j);
-      if (x > low || (ties && x == low)) {
-        const int p = atomicAdd(&S.count[cur], 1);
-        if (p < kLpCap) S.cand[p] = lp_key(x, lp_index<kBf16>(i0, i * C::kVec + j));
-      }
+      if (x > low || (ties && x == low)) hits |= 1u << (i * C::kVec + j);
     }
+  }
+  int p = atomicAdd(&S.count[cur], __popc(hits));
+  for (; hits != 0; hits &= hits - 1, ++p) {
+    const int i = __ffs(hits) - 1;
+    if (p < kLpCap) S.cand[p] = lp_key(lp_own<kBf16>(S, i), lp_index<kBf16>(i0, i));
   }
 }
 
@@ -253,6 +256,7 @@ __device__ __noinline__ float lp_rank(LpShared& S, int cur, int top) {
     int rank = 0;
 #pragma unroll 4
     for (int j = 0; j < n; ++j) rank += S.cand[j] > k;
+#pragma unroll 4
     for (int j = 0; j < top; ++j) rank += S.list[cur][j] > k;
     if (rank < top) S.list[1 - cur][rank] = k;
   }
@@ -277,15 +281,15 @@ __device__ __noinline__ float lp_take(LpShared& S, int cur, float mx, float tau,
   // thread maximum has at least `top` values at or above it.
   float low = tau;
   if (tau == -CUDART_INF_F) {
-    float x = mx, r = -CUDART_INF_F;
+    // (as ordered integers, for the warp's maximum in one instruction)
+    uint32_t x = mx == mx ? (uint32_t)(lp_key(mx, 0) >> 32) : 0u, r = 0;
     for (int i = 0; i < (top + kLpWarps - 1) / kLpWarps; ++i) {
-      r = x;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
+      r = __reduce_max_sync(0xffffffffu, x);
       const uint32_t at = __ballot_sync(0xffffffffu, x == r);
-      if (lane == __ffs(at) - 1) x = -CUDART_INF_F;
+      if (lane == __ffs(at) - 1) x = 0;
     }
-    if (lane == 0) S.wm[warp] = r;
+    const float rv = r <= 0x007FFFFFu ? -CUDART_INF_F : lp_value((uint64_t)r << 32);
+    if (lane == 0) S.wm[warp] = rv;
     __syncthreads();
     low = S.wm[0];
 #pragma unroll
@@ -470,9 +474,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
     lp_outputs<kBf16>(a, m, row, mx, sum, tsum, S.list[cur_list], tid, kLpThreads, id, x_id);
     return;
   }
-  // The pieces of a row are a cluster: the first CTA joins them, a lane per
-  // piece. Their keys are sorted, so the largest of the lanes' heads is the next
-  // alternative.
+  // The pieces of a row are a cluster: the first CTA joins them. Their lists are
+  // sorted: the k-th largest of their r-th keys has k * r >= top keys at or above
+  // it, and with r about sqrt(top) not many more. Those are ranked.
   if (tid < a.top) S.final_list[tid] = S.list[cur_list][tid];
   if (tid == 0) {
     S.stats[0] = mx;
@@ -481,29 +485,52 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
   }
   cluster_sync();
   if (split == 0) {
-    for (int i = tid; i < a.splits * a.top; i += kLpThreads)
-      S.cand[i] = ld_cluster_u64(map_to_cta(&S.final_list[i % a.top], i / a.top));
-    __syncthreads();
-    if (warp == 0) {
-      const bool has = lane < a.splits;
-      const uint32_t st = map_to_cta(S.stats, has ? lane : 0);
-      mx = has ? ld_cluster_f32(st) : -CUDART_INF_F;
-      sum = has ? ld_cluster_f32(st + 4) : 0.0f;
-      tsum = has ? ld_cluster_f32(st + 8) : 0.0f;
-      lp_join_warp(mx, sum, tsum);
-      int taken = 0;
-      uint64_t head = has && a.top > 0 ? S.cand[lane * a.top] : 0;
-      for (int t = 0; t < a.top; ++t) {
-        const uint64_t best = warp_max_u64(head);
-        if (lane == 0) S.final_list[t] = best;
-        if (best != 0 && head == best) {  // keys differ: one lane
-          ++taken;
-          head = taken < a.top ? S.cand[lane * a.top + taken] : 0;
-        }
-      }
-      __syncwarp();
-      lp_outputs<kBf16>(a, m, row, mx, sum, tsum, S.final_list, lane, 32, id, x_id);
+    constexpr int kKeys = kLpMaxSplits * kLpTop / kLpThreads;
+    const int shift = 31 - __clz(a.splits), n = a.splits * a.top;
+    uint64_t k[kKeys];
+#pragma unroll
+    for (int u = 0; u < kKeys; ++u) {
+      const int i = tid + u * kLpThreads;  // key i >> shift of a piece
+      k[u] = i < n ? ld_cluster_u64(map_to_cta(&S.final_list[i >> shift], i & (a.splits - 1))) : 0;
     }
+    const bool has = lane < a.splits;
+    const uint32_t st = map_to_cta(S.stats, has ? lane : 0);
+    mx = has ? ld_cluster_f32(st) : -CUDART_INF_F;
+    sum = has ? ld_cluster_f32(st + 4) : 0.0f;
+    tsum = has ? ld_cluster_f32(st + 8) : 0.0f;
+    lp_join_warp(mx, sum, tsum);
+    if (a.top > 0) {
+      if (tid < kLpTop) S.list[1][tid] = 0;
+      if (tid == 0) S.count[0] = 0;
+      int r = 1;
+      while (r * r < a.top || r * a.splits < a.top) ++r;
+      const int kth = (a.top + r - 1) / r;
+#pragma unroll
+      for (int u = 0; u < kKeys; ++u) {
+        const int i = tid + u * kLpThreads;
+        if (i < n && i >> shift == r - 1) S.list[0][i & (a.splits - 1)] = k[u];
+      }
+      __syncthreads();
+      const uint64_t own = has ? S.list[0][lane] : 0;
+      int above = 0;
+      for (int j = 0; j < a.splits; ++j) above += S.list[0][j] > own;
+      const uint32_t at = __ballot_sync(0xffffffffu, own != 0 && above == kth - 1);
+      const uint64_t low = at ? S.list[0][__ffs(at) - 1] : 0;
+#pragma unroll
+      for (int u = 0; u < kKeys; ++u)
+        if (k[u] != 0 && k[u] >= low) S.cand[atomicAdd(&S.count[0], 1)] = k[u];
+      __syncthreads();
+      const int c = S.count[0];
+      for (int i = tid; i < c; i += kLpThreads) {
+        const uint64_t key = S.cand[i];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < c; ++j) rank += S.cand[j] > key;
+        if (rank < a.top) S.list[1][rank] = key;
+      }
+      __syncthreads();
+    }
+    lp_outputs<kBf16>(a, m, row, mx, sum, tsum, S.list[1], tid, kLpThreads, id, x_id);
   }
   cluster_sync();  // a piece's shared memory outlives its reading
 }
