@@ -11,11 +11,19 @@
 //
 // A lane owns 16 consecutive values (K is a multiple of 16), eight lanes a
 // block, so the block's maximum takes three shuffles and q leaves in one
-// 16-byte store per lane. HBM-bound: 2 (bf16) or 4 (fp32) bytes read and 1
-// written per value.
+// 16-byte store per lane. HBM-bound for fp32 (4 bytes read and 1 written per
+// value: 4096 x 17408 54 us, 6.6 TB/s); for bf16 (2 read) the instructions are
+// as near a bound (issue slots 79 % used at 8192 x 17408, 75 us, 5.7 TB/s).
 #include "qg_common.cuh"
 
 namespace qg {
+
+// maximum that keeps a NaN (fmaxf drops it)
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 // 16 consecutive values as they lie in memory (bf16 ones are unpacked where
 // they are used: a unit in flight is 8 registers then, not 16)
@@ -41,14 +49,24 @@ struct Raw16 {
     }
     return __uint_as_float(j == 0 ? q.x : j == 1 ? q.y : j == 2 ? q.z : q.w);
   }
+  __device__ __forceinline__ float absmax() const {  // NaN if there is one
+    if (kBf16) {  // without their signs, the bits are in the order of the values
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        m = __vmaxu2(m, w[i].x & 0x7FFF7FFFu);
+        m = __vmaxu2(m, w[i].y & 0x7FFF7FFFu);
+        m = __vmaxu2(m, w[i].z & 0x7FFF7FFFu);
+        m = __vmaxu2(m, w[i].w & 0x7FFF7FFFu);
+      }
+      return __uint_as_float(max(m << 16, m & 0xFFFF0000u));
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = max_nan(m, fabsf(at(j)));
+    return m;
+  }
 };
-
-// maximum that keeps a NaN (fmaxf drops it)
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 
 // e4m3 of four values (round to nearest even, saturating; NaN stays NaN)
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -115,9 +133,7 @@ __global__ void __launch_bounds__(128, kBf16 ? 12 : 8) quantize_act_fp8_kernel(
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
     const int k = u * 512 + lane * 16;
-    float amax = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) amax = max_nan(amax, fabsf(v[i].at(j)));
+    float amax = v[i].absmax();
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if (unit0 + i < units && k < K) {
@@ -156,7 +172,7 @@ static void launch_q8(const void* x, int64_t M, int64_t K, int64_t ldx, uint8_t*
 cudaError_t launch_quantize_act_fp8(const void* x, bool bf16, int64_t M, int64_t K, int64_t ldx,
                                     uint8_t* q, float* scale, int64_t lds, cudaStream_t st) {
   // Two units a warp where bf16 rows fill the SMs several times over (their
-  // units are 1 KB): 8192 x 17408 76 us, 85 with one (5.6 and 5.1 TB/s); 2048 x
+  // units are 1 KB): 8192 x 17408 75 us, 85 with one (5.7 and 5.0 TB/s); 2048 x
   // 2560 5.9 us, 5.7 with one. fp32 rows: 4096 x 17408 61 us, 53 with one.
   if (!bf16)
     launch_q8<false, 1>(x, M, K, ldx, q, scale, lds, st);
