@@ -25,9 +25,10 @@
 // The pieces of a row are a cluster of CTAs, whose first one joins them.
 //
 // Measured (GB300, bf16, from a CUDA graph): 4096 x 131072 without alternatives
-// 171 us, 6.3 TB/s of 6.69 measured for a copy; with 1, 5, 32 alternatives 196,
-// 218, 303 us (the ranks, during which a CTA reads nothing, and the candidates);
-// 2048 x 131072 fp32, 5 alternatives 178 us; 1 x 131072 4.1 us, with 20 12.7 us.
+// 163 us, 6.6 TB/s (a copy: 6.69); with 1, 5, 32 alternatives 180, 200, 278 us:
+// bound by issued instructions there (73 % of the slots; 8.9 a value without
+// alternatives, 11.5 with five). 2048 x 131072 fp32, 5 alternatives 169 us; 1 x
+// 131072 4.4 us, with 20 11 us.
 #include <math_constants.h>
 
 #include "qg_common.cuh"
@@ -35,7 +36,7 @@
 namespace qg {
 
 // Small CTAs, eight on an SM: one's barriers hide behind the others (4096 x 131072
-// bf16, no alternatives: 167 us, 175 with 256 threads, 209 with 512).
+// bf16, no alternatives, when it took 167 us: 175 with 256 threads, 209 with 512).
 constexpr int kLpThreads = 128, kLpWarps = kLpThreads / 32, kLpCtas = 8;
 constexpr int kLpVecs = 4;                   // 16-byte loads per thread and chunk
 constexpr int kLpCap = 512;                  // candidates that are ranked at once
@@ -151,7 +152,7 @@ struct LpChunk {
   }
   static constexpr uint32_t kNone = kBf16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
   // the thread's vectors of a chunk of n (whole: n = 4 * 128)
-  __device__ __forceinline__ void load(const uint4* chunk, int64_t n) {
+  __device__ __forceinline__ void load(const uint4* chunk, int n) {
     if (n >= kLpVecs * kLpThreads) {
 #pragma unroll
       for (int i = 0; i < kLpVecs; ++i) v[i] = __ldcs(chunk + i * kLpThreads + threadIdx.x);
@@ -269,8 +270,8 @@ __device__ __noinline__ float lp_rank(LpShared& S, int cur, int top) {
 // Takes a chunk's values above `tau` (the last of the list's values, -inf while
 // it is not full; with `ties`, values at tau as well) into the list, whatever
 // their number: list `cur` becomes list 1 - cur, whose last value is returned.
-// Threads whose maximum mx qualifies have left their values in S.own. No candidates are pending. Called by the
-// whole CTA.
+// Threads whose maximum mx qualifies have left their values in S.own. No
+// candidates are pending. Called by the whole CTA.
 template <bool kBf16>
 __device__ __noinline__ float lp_take(LpShared& S, int cur, float mx, float tau, bool ties, uint32_t i0,
                                       int top) {
@@ -364,17 +365,23 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
   };
   C cur;
   auto load = [&](C& c, int step) {
-    if (step < chunks) c.load(body + v0 + (int64_t)step * kStep, v1 - v0 - (int64_t)step * kStep);
+    if (step < chunks) c.load(body + v0 + (int64_t)step * kStep, (int)(v1 - v0 - (int64_t)step * kStep));
     else c.load_one(row, mine, tid < around);
   };
   if (steps > 0) load(cur, 0);
+  const uint4* next = body + v0;  // chunk on its way, and the vectors from there on
+  int left = (int)(v1 - v0);
   // a given id and its logit take two trips to memory: the first now, the
   // second after the first chunk
   const int64_t id = split == 0 && tid < a.G ? a.ids[m * a.G + tid] : -1;
   float x_id = 0.0f;
+  int rank_at = 0;  // the next step whose candidates are ranked
   for (int step = 0; step < steps; ++step) {
     C nxt;
-    if (step + 1 < steps) load(nxt, step + 1);
+    next += kStep;
+    left -= kStep;
+    if (left > 0) nxt.load(next, left);
+    else if (step + 1 < steps) nxt.load_one(row, mine, tid < around);
     const float cm = cur.max();
     if (step == 0 && id >= 0 && id < a.V) x_id = lp_load<kBf16>(row, id);
     if (cm > mx) {
@@ -402,33 +409,43 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
       tsum2 = __ffma2_rn(e, d, tsum2);
     }
     if (a.top > 0) {
-      // the values around the vectors come last, the head's with lower indices
-      // than the list's: equal to tau they may still be among the best
-      const bool ties = step >= chunks;
-      const bool has = cm > tau || (ties && cm == tau && cm > -CUDART_INF_F);
-      if (has) {
-#pragma unroll
-        for (int i = 0; i < kLpVecs; ++i) S.own[i][tid] = cur.v[i];
-      }
       // Until the list is full every chunk is ranked. From then on values above
-      // its last are collected.
-      if (tau == -CUDART_INF_F) {
-        if (__syncthreads_or(has)) {
-          tau = lp_take<kBf16>(S, cur_list, cm, tau, ties, index0(step), a.top);
-          cur_list ^= 1;
+      // its last are collected, and ranked after 2, 4, 8, ... chunks (each time
+      // the rate of such values halves) and at the end.
+      if (step != rank_at && step + 1 != steps) {
+        if (cm > tau) {
+#pragma unroll
+          for (int i = 0; i < kLpVecs; ++i) S.own[i][tid] = cur.v[i];
+          lp_append<kBf16>(S, cur_list, tau, false, index0(step));
+          pending = true;
         }
       } else {
-        if (has) lp_append<kBf16>(S, cur_list, tau, ties, index0(step));
-        pending |= has;
-        // ranked after 2, 4, 8, ... chunks (each time the rate of values above
-        // the last of the list halves) and at the end
-        if (((step & (step + 1)) == 0 || step + 1 == steps) && __syncthreads_or(pending)) {
-          over |= S.count[cur_list] > kLpCap;
-          if (!over) {
-            tau = lp_rank(S, cur_list, a.top);
+        // the values around the vectors come last, the head's with lower indices
+        // than the list's: equal to tau they may still be among the best
+        const bool ties = step >= chunks;
+        const bool has = cm > tau || (ties && cm == tau && cm > -CUDART_INF_F);
+        if (has) {
+#pragma unroll
+          for (int i = 0; i < kLpVecs; ++i) S.own[i][tid] = cur.v[i];
+        }
+        if (tau == -CUDART_INF_F) {
+          if (__syncthreads_or(has)) {
+            tau = lp_take<kBf16>(S, cur_list, cm, tau, ties, index0(step), a.top);
             cur_list ^= 1;
-            pending = false;
           }
+          rank_at = tau == -CUDART_INF_F ? step + 1 : step | (step + 1);
+        } else {
+          if (has) lp_append<kBf16>(S, cur_list, tau, ties, index0(step));
+          pending |= has;
+          if (__syncthreads_or(pending)) {
+            over |= S.count[cur_list] > kLpCap;
+            if (!over) {
+              tau = lp_rank(S, cur_list, a.top);
+              cur_list ^= 1;
+              pending = false;
+            }
+          }
+          rank_at = 2 * step + 1;
         }
       }
     }
@@ -536,8 +553,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
 }
 
 // Pieces per row, a power of two: doubled while there are fewer than 3.75 CTAs
-// an SM (100 x 131072 bf16, top 5: 18.3 us, 27.8 up to 1.25 an SM; 300 x 50001:
-// 21.9 us, 29.6 up to 4), none much shorter than a chunk of 4096 bf16 values
+// an SM (100 x 131072 bf16, top 5: 18.0 us, 27.8 up to 1.25 an SM; 300 x 50001:
+// 20.6 us, 29.6 up to 4), none much shorter than a chunk of 4096 bf16 values
 // (two of fp32).
 static int lp_splits(int64_t M, int64_t V) {
   int s = 1;
