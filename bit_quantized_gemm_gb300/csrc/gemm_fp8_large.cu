@@ -11,7 +11,7 @@
 // that a thread owns one token and a span of columns inside one block of 128
 // weight rows: s * ws is one number per thread and block, the chain one FMA per
 // output and block (256 cycles of the FMA pipe for a block of 512 MMA cycles).
-// Measured at 8192 x 5120 x 17408: 545 us, 2.69 PFLOP/s, about 890 cycles per
+// Measured at 8192 x 5120 x 17408: 558 us, 2.62 PFLOP/s, about 910 cycles per
 // block; without the epilogue's FMAs 457 us, without its loads and FMAs 446,
 // without the operand loads too 399 (the MMAs alone: 310 at 1.93 GHz).
 //
