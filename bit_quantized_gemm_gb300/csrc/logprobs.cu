@@ -27,7 +27,7 @@
 // Measured (GB300, bf16, from a CUDA graph): 4096 x 131072 without alternatives
 // 163 us, 6.6 TB/s (a copy: 6.69); with 1, 5, 32 alternatives 180, 200, 278 us:
 // bound by issued instructions there (73 % of the slots; 8.9 a value without
-// alternatives, 11.5 with five). 2048 x 131072 fp32, 5 alternatives 169 us; 1 x
+// alternatives, 10.7 with five). 2048 x 131072 fp32, 5 alternatives 169 us; 1 x
 // 131072 4.4 us, with 20 11 us.
 #include <math_constants.h>
 
