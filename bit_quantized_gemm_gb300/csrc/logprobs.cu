@@ -25,7 +25,7 @@
 // The pieces of a row are a cluster of CTAs, whose first one joins them.
 //
 // Measured (GB300, bf16, from a CUDA graph): 4096 x 131072 without alternatives
-// 163 us, 6.6 TB/s (a copy: 6.69); with 1, 5, 32 alternatives 180, 200, 278 us:
+// 161 us, 6.7 TB/s (a copy: 6.69); with 1, 5, 32 alternatives 180, 199, 278 us:
 // bound by issued instructions there (73 % of the slots; 8.9 a value without
 // alternatives, 10.7 with five). 2048 x 131072 fp32, 5 alternatives 169 us; 1 x
 // 131072 4.4 us, with 20 11 us.
@@ -98,25 +98,29 @@ __device__ __forceinline__ float lp_load(const void* row, int64_t i) {
   return reinterpret_cast<const float*>(row)[i];
 }
 
-// One row's outputs from its statistics and its keys (descending, 0: none).
+// One row's outputs from its statistics and its keys (descending, 0: none), by
+// the whole CTA: the given tokens, the entropy and the alternatives by warps of
+// their own (each part is short and waits mostly for its own instructions).
 // id0, x0: the thread's first given id and its logit, loaded ahead.
 template <bool kBf16>
 __device__ __forceinline__ void lp_outputs(const LpArgs& a, int64_t m, const void* row, float mx, float S,
-                                           float T, const uint64_t* keys, int tid, int threads,
-                                           int64_t id0, float x0) {
+                                           float T, const uint64_t* keys, int64_t id0, float x0) {
+  const int tid = threadIdx.x;
   const bool empty = mx == -CUDART_INF_F && S == 0.0f, bad = !(S == S);
   const float shift = empty ? 0.0f : mx, lse = empty ? 0.0f : logf(S);
   auto logp = [&](float x) {
     if (bad) return CUDART_NAN_F;
     return x == -CUDART_INF_F ? x : (x - shift) - lse;
   };
-  if (tid == 0 && a.entropy) a.entropy[m] = bad ? CUDART_NAN_F : empty ? 0.0f : lse - T / S;
-  for (int g = tid; g < a.G; g += threads) {
+  if (tid == kLpThreads - 33 && a.entropy)
+    a.entropy[m] = bad ? CUDART_NAN_F : empty ? 0.0f : lse - T / S;
+  for (int g = tid; g < a.G; g += kLpThreads) {
     const int64_t id = g == tid ? id0 : a.ids[m * a.G + g];
     const float x = g == tid || id < 0 || id >= a.V ? x0 : lp_load<kBf16>(row, id);
     a.logprobs[m * a.G + g] = id < 0 ? 0.0f : id >= a.V ? CUDART_NAN_F : logp(x);
   }
-  for (int t = tid; t < a.top; t += threads) {
+  const int t = tid - (kLpThreads - 32);  // the last warp
+  if (t >= 0 && t < a.top) {
     const uint64_t k = keys[t];
     const bool none = bad || k == 0;
     a.top_ids[m * a.top + t] = none ? -1 : (int64_t)(uint32_t)~(uint32_t)k;
@@ -488,7 +492,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
 #pragma unroll
   for (int w = 1; w < kLpWarps; ++w) lp_join(mx, sum, tsum, S.wm[w], S.wS[w], S.wT[w]);
   if (a.splits == 1) {
-    lp_outputs<kBf16>(a, m, row, mx, sum, tsum, S.list[cur_list], tid, kLpThreads, id, x_id);
+    lp_outputs<kBf16>(a, m, row, mx, sum, tsum, S.list[cur_list], id, x_id);
     return;
   }
   // The pieces of a row are a cluster: the first CTA joins them. Their lists are
@@ -501,20 +505,23 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
     S.stats[2] = tsum;
   }
   cluster_sync();
+  constexpr int kKeys = kLpMaxSplits * kLpTop / kLpThreads;
+  const int shift = 31 - __clz(a.splits), n = a.splits * a.top;
+  uint64_t k[kKeys];
+  const bool has = lane < a.splits;
   if (split == 0) {
-    constexpr int kKeys = kLpMaxSplits * kLpTop / kLpThreads;
-    const int shift = 31 - __clz(a.splits), n = a.splits * a.top;
-    uint64_t k[kKeys];
 #pragma unroll
     for (int u = 0; u < kKeys; ++u) {
       const int i = tid + u * kLpThreads;  // key i >> shift of a piece
       k[u] = i < n ? ld_cluster_u64(map_to_cta(&S.final_list[i >> shift], i & (a.splits - 1))) : 0;
     }
-    const bool has = lane < a.splits;
     const uint32_t st = map_to_cta(S.stats, has ? lane : 0);
     mx = has ? ld_cluster_f32(st) : -CUDART_INF_F;
     sum = has ? ld_cluster_f32(st + 4) : 0.0f;
     tsum = has ? ld_cluster_f32(st + 8) : 0.0f;
+  }
+  cluster_arrive();  // a piece's shared memory outlives its reading, no more
+  if (split == 0) {
     lp_join_warp(mx, sum, tsum);
     if (a.top > 0) {
       if (tid < kLpTop) S.list[1][tid] = 0;
@@ -547,9 +554,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
       }
       __syncthreads();
     }
-    lp_outputs<kBf16>(a, m, row, mx, sum, tsum, S.list[1], tid, kLpThreads, id, x_id);
+    lp_outputs<kBf16>(a, m, row, mx, sum, tsum, S.list[1], id, x_id);
   }
-  cluster_sync();  // a piece's shared memory outlives its reading
+  cluster_wait();
 }
 
 // Pieces per row, a power of two: doubled while there are fewer than 3.75 CTAs
