@@ -559,13 +559,13 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
   cluster_wait();
 }
 
-// Pieces per row, a power of two: doubled while there are fewer than 3.75 CTAs
-// an SM (100 x 131072 bf16, top 5: 18.0 us, 27.8 up to 1.25 an SM; 300 x 50001:
-// 20.6 us, 29.6 up to 4), none much shorter than a chunk of 4096 bf16 values
-// (two of fp32).
+// Pieces per row, a power of two: doubled while there are fewer than 3.25 CTAs
+// an SM (200 x 131072 bf16, top 5: 24.3 us, 27.8 up to 2 an SM; 64 x 131072, top
+// 20: 18.2 us, 20.4 up to 3.75), none much shorter than a chunk of 4096 bf16
+// values (two of fp32).
 static int lp_splits(int64_t M, int64_t V) {
   int s = 1;
-  while (s < kLpMaxSplits && M * s * 4 < 15 * (int64_t)num_sms() && V > 4096 * (int64_t)s) s *= 2;
+  while (s < kLpMaxSplits && M * s * 4 < 13 * (int64_t)num_sms() && V > 4096 * (int64_t)s) s *= 2;
   return s;
 }
 
