@@ -297,12 +297,15 @@ def linear_w4a8_mxfp4(x, packed, N, out=None, out_dtype=torch.bfloat16, scale_ou
                    fn=load().qg_linear_w4a8_mxfp4)
 
 
-def _empty(shape, dtype, device, stream):
-    """Memory for work on `stream`: taken from that stream's pool, so that its reuse follows that work."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+def _empty(shape, dtype, device, stream, ld=None):
+    """Memory for work on `stream`: taken from that stream's pool, so that its reuse follows that work.
+    `ld`: distance of a matrix's rows (a view of a wider tensor costs several us of host time)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _empty(shape, dtype, device, None, ld)
+    if ld is not None:
+        return torch.empty_strided(shape, (ld, 1), dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _raw_stream(stream, device):
@@ -369,9 +372,7 @@ def quantize_act_fp8(x, out=None, stream=None):
     if out is None:
         dev, lds = x.device, (M + 3) // 4 * 4
         q = _empty((M, K), _FP8, dev, stream)
-        scale = _empty(((K + 127) // 128, lds), _F32, dev, stream)
-        if lds != M:  # (a slice takes 5 us, this 1)
-            scale = scale.as_strided((scale.shape[0], M), (lds, 1))
+        scale = _empty(((K + 127) // 128, M), _F32, dev, stream, lds)
     else:
         q, scale = out
         if _rows(q, "q", (_FP8,)) != (M, K, K):

@@ -545,7 +545,7 @@ static cudaError_t launch_large(const uint8_t* q, int64_t K, const uint8_t* w, i
                     CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, K, a.N, ldw, 128, C::kWRows,
                     CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&ts, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.scale, align_up(a.M, 4), a.KB, a.lds * 4, 128,
+      !make_tmap_2d(&ts, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.scale, a.M, a.KB, a.lds * 4, 128,
                     C::G, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorNotSupported;
   memset(&to, 0, sizeof(to));

@@ -312,7 +312,7 @@ static cudaError_t launch_small(const CUtensorMap& tw, const uint8_t* q, const f
   CUtensorMap tq, ts;
   if (!make_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, a.M, K, 128, BM,
                     CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&ts, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, scale, align_up(a.M, 4), a.KB, lds * 4, BM,
+      !make_tmap_2d(&ts, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, scale, a.M, a.KB, lds * 4, BM,
                     C::G, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorNotSupported;
   // one CTA per SM, with the whole shared memory for its ring
