@@ -13,7 +13,7 @@
 // block, so the block's maximum takes three shuffles and q leaves in one
 // 16-byte store per lane. HBM-bound for fp32 (4 bytes read and 1 written per
 // value: 4096 x 17408 54 us, 6.6 TB/s); for bf16 (2 read) the instructions are
-// as near a bound (issue slots 79 % used at 8192 x 17408, 75 us, 5.7 TB/s).
+// as near a bound (issue slots 81 % used at 8192 x 17408, 75 us, 5.7 TB/s).
 #include "qg_common.cuh"
 
 namespace qg {

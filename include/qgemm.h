@@ -312,7 +312,8 @@ qg_status qg_linear_w8a8_q8_0_noalloc(const void* x, qg_dtype x_dtype, int64_t M
 /*          ldx*elem_size % 16 == 0.                                          */
 /*   q      [M][K] e4m3 out, 16-byte aligned.                                 */
 /*   scale  [ceil(K/128)][lds] fp32 out: s[b][m] at scale[b*lds + m];         */
-/*          16-byte aligned, lds >= M a multiple of 4. Columns M.. are left.  */
+/*          16-byte aligned, lds >= M a multiple of 4. Columns M.. are left,  */
+/*          and the last row may end at M.                                    */
 qg_status qg_quantize_act_fp8(const void* x, qg_dtype x_dtype, int64_t M, int64_t K, int64_t ldx,
                               uint8_t* q, float* scale, int64_t lds, void* stream);
 /*   q, scale, lds  as written by qg_quantize_act_fp8.                        */
