@@ -183,6 +183,10 @@ __global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
         ok = mbar_wait_warp(&empty[s], phase, a.err);
         if (!ok) break;
         if (elect_one()) {
+          // the scale warp reads the slot's scales through the generic proxy
+          // (ld.shared); the load below rewrites them through the async proxy,
+          // ordered after those reads only by this fence
+          fence_proxy_async_smem();
           const int blocks = min(G, KB - G * i);
           // both CTAs' bytes complete on the leader's barrier
           if (rank == 0)

@@ -163,6 +163,10 @@ __global__ void __launch_bounds__(Fp8SmallCfg<R, BM>::kThreads)
       ok = mbar_wait_warp(&S.empty[s], phase, a.err);
       if (!ok) break;
       if (elect_one()) {
+        // the epilogue warps read the slot's scales through the generic proxy
+        // (ld.shared); the loads below rewrite them through the async proxy,
+        // ordered after those reads only by this fence
+        fence_proxy_async_smem();
         load_w(n0, i, s);
         load_q(i, s);
       }
