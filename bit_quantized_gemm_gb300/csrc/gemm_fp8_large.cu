@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
         const int mine = two && (lane & 1) ? buf1 : buf;
         ok = mbar_wait_warp(&sempty[mine], (used >> mine) & 1u, a.err);
         if (!ok) break;
+        __syncwarp();  // each lane has seen one of the two buffers released
         float* f = sf + lane * 4;
 #pragma unroll
         for (int r = 0; r < C::kScaleRows; ++r) {
@@ -433,6 +434,7 @@ __global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
           } else {
             tc_fence_before();
             ready = __all_sync(0xffffffffu, ready);
+            __syncwarp();  // (a vote orders no memory: the lanes' reads of f)
             if (lane == 0) {
               if constexpr (kPair) mbar_arrive_cluster(tempty_leader + here * 8);
               else mbar_arrive(&tempty[here]);

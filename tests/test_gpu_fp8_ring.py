@@ -6,7 +6,7 @@ shows as another block's scale.
 Every value is exact, so that nothing but the right scale passes: operands are
 whole numbers of at most 2, scales powers of two (a token's from 1 to 8, another
 one from block to block; a weight block's 1 or 2), so that a block's sum is at
-most 512, an output at most 512 * 16 * 136 < 2^24 and every step of the chain is
+most 512, an output at most 512 * 16 * 512 < 2^24 and every step of the chain is
 a whole number in fp32.
 """
 import pytest
@@ -51,6 +51,8 @@ def exact_case(m, k, n):
     # more: single CTAs and pairs, short tails of K, several tiles a CTA
     (65, 17408, 5120), (128, 17408, 5120), (512, 17408, 5120), (777, 2576, 5003), (1024, 9744, 2560),
     (2048, 2560, 9728), (4096, 4240, 4864),
+    # the longest chains: products of scales pass through two to four buffers 512 times
+    (200, 65536, 1500), (2000, 65536, 2500), (600, 65424, 5000),
 ])
 def test_scales_of_many_rounds(m, k, n):
     q, s, w, ws, want = exact_case(m, k, n)
