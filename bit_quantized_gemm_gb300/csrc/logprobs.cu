@@ -5,7 +5,9 @@
 //   log p[i] = x[i] - m - log S,   H = -sum p log p = log S - T / S
 // (both terms of H are >= 0: nothing cancels). The alternatives are the first
 // `top` values in the order (value descending, index ascending). Statistics
-// are held in fp32 relative to a running maximum.
+// are held in fp32 relative to a running maximum: a thread adds up the terms of a
+// chunk, the sums of up to 32 chunks, and these in a compensated sum, so that log S
+// is off by no more than 2e-5 at any V (one chain of 4096 terms: 1.2e-4).
 //
 // Rows without a distribution: -inf everywhere (a mask that leaves nothing)
 // gives log p = -inf, H = 0 and no alternatives (index -1, -inf); a row with a
@@ -41,6 +43,7 @@ constexpr int kLpThreads = 128, kLpWarps = kLpThreads / 32, kLpCtas = 8;
 constexpr int kLpVecs = 4;                   // 16-byte loads per thread and chunk
 constexpr int kLpCap = 512;                  // candidates that are ranked at once
 constexpr int kLpTop = QG_LOGPROBS_MAX_TOP;
+constexpr int kLpFold = 32;                  // chunks whose sums are added in plain fp32
 constexpr int kLpMaxSplits = 16;             // CTAs of a cluster
 static_assert(kLpTop <= 32 && kLpTop % kLpWarps == 0, "a lane per alternative");
 
@@ -90,6 +93,41 @@ __device__ __forceinline__ void lp_join_warp(float& m, float& S, float& T) {
                 T2 = __shfl_xor_sync(0xffffffffu, T, o);
     lp_join(m, S, T, m2, S2, T2);
   }
+}
+
+// a + b with the rounding error of the sum added to `lost`
+__device__ __forceinline__ float add_exact(float a, float b, float& lost) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  lost += __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+  return s;
+}
+
+// Adds the sums of kLpFold chunks (relative to m, the thread's maximum so far) to
+// the thread's sums. These follow the maximum only once it is one above their
+// reference, so that many small rises do not scale them, and round them, many
+// times: the factors shrink what the earlier ones rounded. (Shared memory and a
+// call of its own: rare, and the loop has no register to spare.)
+__device__ __noinline__ void lp_fold(float (*fold)[kLpThreads], float m, float S, float T) {
+  if (S == 0.0f) return;  // only -inf so far
+  float* f = &fold[0][threadIdx.x];
+  float ref = f[0], s = f[kLpThreads], s_lost = f[2 * kLpThreads], t = f[3 * kLpThreads], t_lost = f[4 * kLpThreads];
+  if (!(m <= ref + 1.0f)) {
+    const float c = __expf(ref - m), d = fmaxf(ref - m, -200.0f);  // c = 0 at first
+    t = c * fmaf(s, d, t);
+    t_lost = c * fmaf(s_lost, d, t_lost);
+    s *= c;
+    s_lost *= c;
+    ref = m;
+  } else {
+    const float d = m - ref, c = __expf(d);
+    T = c * fmaf(S, d, T);
+    S *= c;
+  }
+  f[0] = ref;
+  f[kLpThreads] = add_exact(s, S, s_lost);
+  f[2 * kLpThreads] = s_lost;
+  f[3 * kLpThreads] = add_exact(t, T, t_lost);
+  f[4 * kLpThreads] = t_lost;
 }
 
 template <bool kBf16>
@@ -203,6 +241,9 @@ struct LpShared {
   uint64_t red[kLpWarps];
   float wm[kLpWarps], wS[kLpWarps], wT[kLpWarps];
   int count[2];                    // candidates, also those past the buffer's end
+  // a thread's sums of whole groups of chunks: their reference, then S and T, each
+  // with what its roundings lost
+  float fold[5][kLpThreads];
   uint64_t final_list[kLpTop];     // what the row's first CTA reads of a piece
   float stats[3];
 };
@@ -357,12 +398,17 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
   const int64_t mine = tid < head ? tid : tail + tid - head;  // this thread's value around the vectors
   if (tid < 2 * kLpTop) S.list[tid / kLpTop][tid % kLpTop] = 0;
   if (tid < 2) S.count[tid] = 0;
+  if (chunks > kLpFold) {
+    S.fold[0][tid] = -CUDART_INF_F;
+#pragma unroll
+    for (int i = 1; i < 5; ++i) S.fold[i][tid] = 0.0f;
+  }
   int cur_list = 0;
   bool pending = false;  // this thread has candidates that are not ranked yet
   __syncthreads();
 
   float mx = -CUDART_INF_F, tau = -CUDART_INF_F;
-  float2 sum2 = make_float2(0.0f, 0.0f), tsum2 = sum2;  // tsum2 in units of log2
+  float sum = 0.0f, tsum = 0.0f;  // tsum in units of log2
   bool over = false;
   auto index0 = [&](int step) {  // row index of the thread's value 0
     return step < chunks ? (uint32_t)(head + (v0 + (int64_t)step * kStep + tid) * C::kVec) : (uint32_t)mine;
@@ -391,8 +437,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
     if (cm > mx) {
       const float c = __expf(mx - cm);  // 0 while mx = -inf, where the sums are 0 (or NaN)
       const float d = fmaxf(mx - cm, -200.0f) * 1.44269504f;
-      tsum2 = make_float2(c * fmaf(sum2.x, d, tsum2.x), c * fmaf(sum2.y, d, tsum2.y));
-      sum2 = make_float2(c * sum2.x, c * sum2.y);
+      tsum = c * fmaf(sum, d, tsum);
+      sum = c * sum;
       mx = cm;
     }
     // Differences in units of log2, two values per packed operation (the loop
@@ -401,6 +447,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
     // one, and +inf becomes one (inf - inf).
     const float ref = mx == -CUDART_INF_F ? 0.0f : mx;
     const float2 nref = make_float2(-ref, -ref), log2e = make_float2(1.44269504f, 1.44269504f);
+    float2 sum2, tsum2;  // of this chunk (its first terms start them: no more additions than in one chain)
 #pragma unroll
     for (int i = 0; i < C::kPer; i += 2) {
       float2 d = __fmul2_rn(__fadd2_rn(make_float2(cur.at(i), cur.at(i + 1)), nref), log2e);
@@ -409,9 +456,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
       float2 e;
       asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(d.x));
       asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(d.y));
-      sum2 = __fadd2_rn(sum2, e);
-      tsum2 = __ffma2_rn(e, d, tsum2);
+      sum2 = i == 0 ? e : __fadd2_rn(sum2, e);
+      tsum2 = i == 0 ? __fmul2_rn(e, d) : __ffma2_rn(e, d, tsum2);
     }
+    sum += sum2.x + sum2.y;
+    tsum += tsum2.x + tsum2.y;
     if (a.top > 0) {
       // Until the list is full every chunk is ranked. From then on values above
       // its last are collected, and ranked after 2, 4, 8, ... chunks (each time
@@ -454,6 +503,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
       }
     }
     cur = nxt;
+    if (step % kLpFold == kLpFold - 1 && step + 1 < chunks) {
+      lp_fold(S.fold, mx, sum, tsum * 0.693147181f);
+      sum = tsum = 0.0f;
+    }
   }
   if (over) {
     // more candidates than the buffer holds (ascending values): once more, chunk
@@ -477,7 +530,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
       }
     }
   }
-  float sum = sum2.x + sum2.y, tsum = (tsum2.x + tsum2.y) * 0.693147181f;
+  tsum *= 0.693147181f;
+  if (chunks > kLpFold)
+    lp_join(mx, sum, tsum, S.fold[0][tid], S.fold[1][tid] + S.fold[2][tid], S.fold[3][tid] + S.fold[4][tid]);
   lp_join_warp(mx, sum, tsum);
   __syncthreads();
   if (lane == 0) {

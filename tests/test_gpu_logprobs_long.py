@@ -1,0 +1,100 @@
+"""GPU tests of token_logprobs on long rows against the definition in 64 bits.
+
+Tolerances. A thread adds up to 16 terms of a chunk and the sums of up to 32
+chunks; these are scaled at most 32 times to a higher maximum (the exponential
+2^-22, the product 2^-24 each time, relative) before they go into a compensated
+sum. A term e^d, d = x - m, is off by 2^-22 and by its rounded argument, 2 |d|
+2^-24. The compensated sum, the scalings of it (each follows a rise of the maximum
+by one or more, so that all of them weigh less than 1 / (1 - 1/e) of one) and the
+tree of threads, warps and pieces add no more than 32 roundings. For |d| <= 24,
+below which terms weigh nothing beside these, S and T are off by
+    (16 + 32 + 32 * 5 + 4 + 48 + 32) 2^-24 < 2e-5
+of their sums of magnitudes. So log S is off by 2e-5, x - m - log S by two more
+roundings, and H = log S - T / S by 2e-5 (1 + 2 |T / S|).
+"""
+import math
+
+import pytest
+import torch
+
+import bit_quantized_gemm_gb300 as qg
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+INF = math.inf
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from bit_quantized_gemm_gb300 import build
+    build.build()
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    yield
+    qg.check_device_error()
+    torch.cuda.empty_cache()
+
+
+def near(got, want, tol, what):
+    got = got.double()
+    assert torch.equal(got.isnan(), want.isnan()), what
+    sure = want.isfinite()
+    assert torch.equal(got[~sure & ~want.isnan()], want[~sure & ~want.isnan()]), what
+    assert bool(((got - want).abs() <= tol)[sure].all()), \
+        "%s: off by %.3g" % (what, float(((got - want).abs() - tol)[sure].max()))
+
+
+def check(x, ids, top, got=None, rows_at_once=32):
+    """The definition in 64 bits, some rows at a time; `got`: the outputs to compare (computed when None)."""
+    given, entropy, order, vals = got if got is not None else qg.token_logprobs(x, ids, top=top)
+    for r in range(0, x.shape[0], rows_at_once):
+        part, pid = x[r:r + rows_at_once].double(), ids[r:r + rows_at_once]
+        m, v = part.shape
+        bad = ~(part < INF).all(dim=1, keepdim=True)
+        empty = (part == -INF).all(dim=1, keepdim=True)
+        zero = torch.zeros((), dtype=torch.float64, device=DEV)
+        peak = torch.where(bad | empty, zero, part.amax(dim=1, keepdim=True))
+        d = part - peak
+        e = torch.exp(d)
+        total = torch.where(empty, zero + 1, e.sum(dim=1, keepdim=True))
+        t_over_s = torch.where(e > 0, e * d, zero).sum(dim=1, keepdim=True) / total
+        lp = torch.where(bad, zero + math.nan, d - total.log())
+        want = torch.gather(lp, 1, pid.clamp(0, v - 1))
+        want = torch.where(pid < 0, zero, torch.where(pid >= v, zero + math.nan, want))
+        near(given[r:r + rows_at_once], want, 2e-5 + 2 * 2.0 ** -24 * want.abs(), "given")
+        want = torch.where(bad, zero + math.nan, torch.where(empty, zero, total.log() - t_over_s))[:, 0]
+        near(entropy[r:r + rows_at_once], want, 2e-5 * (1 + 2 * t_over_s[:, 0].abs()), "entropy")
+        if top:
+            best = torch.sort(part, dim=1, descending=True, stable=True).indices[:, :top]
+            want = torch.gather(lp, 1, best)
+            best = torch.where((want == -INF) | want.isnan(), -1, best)
+            assert torch.equal(order[r:r + rows_at_once], best), "top ids"
+            near(vals[r:r + rows_at_once], want, 2e-5 + 2 * 2.0 ** -24 * want.abs(), "top")
+
+
+def some_ids(m, v, count):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(m + v)
+    return torch.randint(0, v, (m, count), generator=g, device=DEV)
+
+
+# Peaks where a thread starts and a constant background below them: every step of its sum rounds
+# the same way, which random logits never show. (Chains of 4096 such terms are off by 1e-4 and more.)
+@pytest.mark.parametrize("below", [9.14, 11.0, 12.61])
+@pytest.mark.parametrize("m,v,pieces,dtype", [
+    (1, 1 << 24, 16, torch.float32), (1, 1 << 24, 16, torch.bfloat16),
+    (512, 1 << 20, 1, torch.bfloat16), (512, 1 << 20, 1, torch.float32),
+])
+def test_peaks_above_a_constant_background(m, v, pieces, dtype, below):
+    x = torch.full((m, v), -below, device=DEV).to(dtype)
+    x.view(m, pieces, v // pieces)[:, :, :4096] = 0.0
+    check(x, some_ids(m, v, 2), 0, rows_at_once=4)
+
+
+# A maximum that rises in every chunk, by little and by much: the sums so far are scaled each time.
+@pytest.mark.parametrize("rise", [1e-3, 0.3, 4.0, 40.0, 1e4])
+@pytest.mark.parametrize("m,v", [(1, 1 << 24), (500, 262143)])
+def test_rising_maximum(m, v, rise):
+    x = (torch.arange(v, device=DEV, dtype=torch.float64) * (rise / v)).float()[None].repeat(m, 1)
+    check(x, some_ids(m, v, 2), 0, rows_at_once=4)
