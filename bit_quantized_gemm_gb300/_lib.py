@@ -320,45 +320,58 @@ def _raw_stream(stream, device):
 # torch's own number of the current stream, without the Stream object around it (the calls below
 # are short next to the kernels of a decode step: 9-12 us of host time in place of 20-26)
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# (the same without its check that CUDA has been initialised: a cuda tensor is at hand)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 _BF16, _F32, _FP8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 _CODES = {_BF16: QG_BF16, _F32: QG_F32}
 
 
-def _rows(t, name, dtypes):
-    """(rows, columns, row stride) of a cuda matrix of one of `dtypes` whose rows are contiguous."""
-    if t.is_cuda and t.dtype in dtypes and t.dim() == 2:
+def _device(first, stream):
+    """Index of a call's device, that of its first tensor; `stream` has to be one of its streams. (The
+    library launches on the current device: where that is another one, a call enters itself again.)"""
+    dev = first.get_device()
+    if stream is not None and stream.device_index != dev:
+        raise ValueError("the stream must belong to the tensors' device")
+    return dev
+
+
+def _rows(t, name, dtypes, dev=None):
+    """(rows, columns, row stride) of a cuda matrix of one of `dtypes` whose rows are contiguous, on
+    device `dev` if one is given."""
+    if (t.is_cuda if dev is None else t.get_device() == dev) and t.dtype in dtypes and t.dim() == 2:
         m, n = t.shape
         ld, step = t.stride()
         if step == 1 or n <= 1:
             # (of a single row torch keeps any stride)
             return m, n, ld if m > 1 else max(n, ld)
-    raise ValueError("%s must be a 2-D cuda tensor of %s with contiguous rows" %
-                     (name, " or ".join(str(d) for d in dtypes)))
+    raise ValueError("%s must be a 2-D cuda tensor of %s with contiguous rows%s" %
+                     (name, " or ".join(str(d) for d in dtypes),
+                      "" if dev is None else ", on device %d like the others of its call" % dev))
 
 
-def _fp8_scale(scale, M, K):
+def _fp8_scale(scale, M, K, dev):
     """Row stride of the scales [ceil(K/128), M] of activations [M, K]."""
-    kb, m, ld = _rows(scale, "scale", (_F32,))
+    kb, m, ld = _rows(scale, "scale", (_F32,), dev)
     if kb != (K + 127) // 128 or m != M:
         raise ValueError("scale must have the shape [ceil(K/128), M]")
     # a single block of K has one row of scales: any stride does
     return ld if kb > 1 else (M + 3) // 4 * 4
 
 
-def _fp8_weights(w, w_scale, M, K, out, out_dtype, stream):
+def _fp8_weights(w, w_scale, M, K, out, out_dtype, stream, dev):
     """(N, row stride of w, out, its row stride), checked; `out` is allocated when None."""
-    N, k, ldw = _rows(w, "w", (_FP8,))
+    N, k, ldw = _rows(w, "w", (_FP8,), dev)
     if k != K:
         raise ValueError("w has rows of %d values, the activations of %d" % (k, K))
-    if (not w_scale.is_cuda or w_scale.dtype != _F32 or not w_scale.is_contiguous()
+    if (w_scale.get_device() != dev or w_scale.dtype != _F32 or not w_scale.is_contiguous()
             or w_scale.shape != ((N + 127) // 128, (K + 127) // 128)):
-        raise ValueError("w_scale must be a contiguous cuda fp32 tensor of shape [ceil(N/128), ceil(K/128)]")
+        raise ValueError("w_scale must be a contiguous fp32 tensor of shape [ceil(N/128), ceil(K/128)] on w's device")
     if out is None:
         if out_dtype not in _CODES:
             raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
         return N, ldw, _empty((M, N), out_dtype, w.device, stream), N
-    m, n, ldo = _rows(out, "out", _CODES)
+    m, n, ldo = _rows(out, "out", _CODES, dev)
     if m != M or n != N:
         raise ValueError("out must have the shape (%d, %d)" % (M, N))
     return N, ldw, out, ldo
@@ -369,17 +382,21 @@ def quantize_act_fp8(x, out=None, stream=None):
     scale fp32 [ceil(K/128), M], one per token and 128 values of K; its rows start on 16-byte
     boundaries). `out` may supply preallocated (q, scale)."""
     M, K, ldx = _rows(x, "x", _CODES)
+    dev = _device(x, stream)
     if out is None:
-        dev, lds = x.device, (M + 3) // 4 * 4
-        q = _empty((M, K), _FP8, dev, stream)
-        scale = _empty(((K + 127) // 128, M), _F32, dev, stream, lds)
+        lds = (M + 3) // 4 * 4
+        q = _empty((M, K), _FP8, x.device, stream)
+        scale = _empty(((K + 127) // 128, M), _F32, x.device, stream, lds)
     else:
         q, scale = out
-        if _rows(q, "q", (_FP8,)) != (M, K, K):
+        if _rows(q, "q", (_FP8,), dev) != (M, K, K):
             raise ValueError("q must be contiguous and of the shape of x")
-        lds = _fp8_scale(scale, M, K)
+        lds = _fp8_scale(scale, M, K, dev)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return quantize_act_fp8(x, (q, scale), stream)
     _check((_lib or load()).qg_quantize_act_fp8(x.data_ptr(), _CODES[x.dtype], M, K, ldx, q.data_ptr(),
-                                                scale.data_ptr(), lds, _raw_stream(stream, x.get_device())))
+                                                scale.data_ptr(), lds, _raw_stream(stream, dev)))
     return q, scale
 
 
@@ -389,11 +406,15 @@ def gemm_fp8(q, scale, w, w_scale, out=None, out_dtype=torch.bfloat16, stream=No
     M, K, ldq = _rows(q, "q", (_FP8,))
     if ldq != K:
         raise ValueError("q must be contiguous")
-    lds = _fp8_scale(scale, M, K)
-    N, ldw, out, ldo = _fp8_weights(w, w_scale, M, K, out, out_dtype, stream)
+    dev = _device(q, stream)
+    lds = _fp8_scale(scale, M, K, dev)
+    N, ldw, out, ldo = _fp8_weights(w, w_scale, M, K, out, out_dtype, stream, dev)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return gemm_fp8(q, scale, w, w_scale, out, stream=stream)
     _check((_lib or load()).qg_gemm_fp8(q.data_ptr(), scale.data_ptr(), lds, M, K, w.data_ptr(), ldw,
                                         w_scale.data_ptr(), N, out.data_ptr(), _CODES[out.dtype], ldo,
-                                        _raw_stream(stream, q.get_device())))
+                                        _raw_stream(stream, dev)))
     return out
 
 
@@ -407,15 +428,21 @@ def linear_fp8(x, w, w_scale, out=None, out_dtype=torch.bfloat16, workspace=None
     """The whole layer: x cuda [M, K] bf16/fp32 -> out [M, N] with e4m3 weights (see gemm_fp8).
     Quantize, then GEMM, through `workspace` (allocated here when not given)."""
     M, K, ldx = _rows(x, "x", _CODES)
-    N, ldw, out, ldo = _fp8_weights(w, w_scale, M, K, out, out_dtype, stream)
+    dev = _device(x, stream)
+    N, ldw, out, ldo = _fp8_weights(w, w_scale, M, K, out, out_dtype, stream, dev)
     if workspace is None:
         nbytes = linear_fp8_workspace_bytes(M, K)
         workspace = _empty((nbytes,), torch.uint8, x.device, stream)
     else:
+        if workspace.get_device() != dev:
+            raise ValueError("workspace must be on x's device")
         nbytes = workspace.numel() * workspace.element_size()
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return linear_fp8(x, w, w_scale, out, workspace=workspace, stream=stream)
     _check((_lib or load()).qg_linear_fp8(x.data_ptr(), _CODES[x.dtype], M, K, ldx, w.data_ptr(), ldw,
                                           w_scale.data_ptr(), N, out.data_ptr(), _CODES[out.dtype], ldo,
-                                          workspace.data_ptr(), nbytes, _raw_stream(stream, x.get_device())))
+                                          workspace.data_ptr(), nbytes, _raw_stream(stream, dev)))
     return out
 
 
@@ -426,19 +453,23 @@ def token_logprobs(logits, ids, top=0, stream=None):
     `top` likeliest tokens, ties to the lowest id; -1 where a row has fewer (see include/qgemm.h)."""
     M, V, ldl = _rows(logits, "logits", _CODES)
     shape = ids.shape
-    if (not ids.is_cuda or ids.dtype != torch.int64 or len(shape) not in (1, 2) or shape[0] != M
+    dev = _device(logits, stream)
+    if (ids.get_device() != dev or ids.dtype != torch.int64 or len(shape) not in (1, 2) or shape[0] != M
             or not ids.is_contiguous()):
-        raise ValueError("ids must be a contiguous cuda int64 tensor of shape [M] or [M, G]")
+        raise ValueError("ids must be a contiguous int64 tensor of shape [M] or [M, G] on the logits' device")
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return token_logprobs(logits, ids, top, stream)
     G = shape[1] if len(shape) == 2 else 1
-    dev, k = logits.device, max(top, 0)
-    logprobs = _empty(shape, _F32, dev, stream)
-    entropy = _empty((M,), _F32, dev, stream)
-    top_ids = _empty((M, k), torch.int64, dev, stream)
-    top_logprobs = _empty((M, k), _F32, dev, stream)
+    where, k = logits.device, max(top, 0)
+    logprobs = _empty(shape, _F32, where, stream)
+    entropy = _empty((M,), _F32, where, stream)
+    top_ids = _empty((M, k), torch.int64, where, stream)
+    top_logprobs = _empty((M, k), _F32, where, stream)
     _check((_lib or load()).qg_token_logprobs(logits.data_ptr(), _CODES[logits.dtype], M, V, ldl,
                                               ids.data_ptr(), G, logprobs.data_ptr(), entropy.data_ptr(),
                                               top, top_ids.data_ptr(), top_logprobs.data_ptr(),
-                                              _raw_stream(stream, logits.get_device())))
+                                              _raw_stream(stream, dev)))
     return logprobs, entropy, top_ids, top_logprobs
 
 
