@@ -434,8 +434,8 @@ def linear_fp8(x, w, w_scale, out=None, out_dtype=torch.bfloat16, workspace=None
         nbytes = linear_fp8_workspace_bytes(M, K)
         workspace = _empty((nbytes,), torch.uint8, x.device, stream)
     else:
-        if workspace.get_device() != dev:
-            raise ValueError("workspace must be on x's device")
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on x's device")
         nbytes = workspace.numel() * workspace.element_size()
     if dev != _current_device():
         with torch.cuda.device(dev):

@@ -155,3 +155,13 @@ def test_a_workspace_of_host_memory_is_refused(library):
     with pytest.raises(ValueError):
         linear(a)
     assert not library.calls
+
+
+@pytest.mark.parametrize("shape,stride", [((1 << 20,), (0,)), ((1 << 10, 1 << 10), (1 << 11, 1)), ((1 << 20,), (2,))])
+def test_a_workspace_that_is_not_one_piece_is_refused(library, shape, stride):
+    # its element count says nothing of the memory from its first element on
+    a = arguments()
+    a["workspace"] = Tensor(shape, torch.uint8, stride=stride)
+    with pytest.raises(ValueError):
+        linear(a)
+    assert not library.calls
