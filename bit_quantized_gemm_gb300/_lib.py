@@ -343,8 +343,8 @@ def _rows(t, name, dtypes, dev=None):
         m, n = t.shape
         ld, step = t.stride()
         if step == 1 or n <= 1:
-            # (of a single row torch keeps any stride)
-            return m, n, ld if m > 1 else max(n, ld)
+            # (the distance of a single row to the next says nothing)
+            return m, n, ld if m > 1 else n
     raise ValueError("%s must be a 2-D cuda tensor of %s with contiguous rows%s" %
                      (name, " or ".join(str(d) for d in dtypes),
                       "" if dev is None else ", on device %d like the others of its call" % dev))
