@@ -450,7 +450,8 @@ def token_logprobs(logits, ids, top=0, stream=None):
     """logits: cuda [M, V] bf16/fp32 (rows may be strided); ids: cuda int64 [M, G] or [M] (-1: no
     token) -> (logprobs fp32 of ids' shape, entropy fp32 [M], top_ids int64 [M, top], top_logprobs
     fp32 [M, top]): log probabilities of the given tokens, the rows' entropies in nats and their
-    `top` likeliest tokens, ties to the lowest id; -1 where a row has fewer (see include/qgemm.h)."""
+    `top` likeliest tokens, ties to the lowest id; -1 where a row has fewer (see include/qgemm.h).
+    The last bits of the floats depend on the number of rows and on where a row lies."""
     M, V, ldl = _rows(logits, "logits", _CODES)
     shape = ids.shape
     dev = _device(logits, stream)

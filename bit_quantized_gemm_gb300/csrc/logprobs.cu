@@ -8,6 +8,8 @@
 // are held in fp32 relative to a running maximum: a thread adds up the terms of a
 // chunk, the sums of up to 32 chunks, and these in a compensated sum, so that log S
 // is off by no more than 2e-5 at any V (one chain of 4096 terms: 1.2e-4).
+// The order of a row's sums depends on its pieces, so on the number of rows, and on
+// its address modulo 16: so do its last bits. The alternatives' order is exact.
 //
 // Rows without a distribution: -inf everywhere (a mask that leaves nothing)
 // gives log p = -inf, H = 0 and no alternatives (index -1, -inf); a row with a

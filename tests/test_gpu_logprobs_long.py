@@ -98,3 +98,35 @@ def test_peaks_above_a_constant_background(m, v, pieces, dtype, below):
 def test_rising_maximum(m, v, rise):
     x = (torch.arange(v, device=DEV, dtype=torch.float64) * (rise / v)).float()[None].repeat(m, 1)
     check(x, some_ids(m, v, 2), 0, rows_at_once=4)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("v,pitch", [(40003, 40003), (131072, 131072), (131072, 131077)])
+def test_rows_in_other_batches_and_places(v, pitch, dtype):
+    # a row alone, in small and large batches (16 pieces down to one) and at other addresses: the
+    # alternatives are the same, the floats within twice the error of one call
+    g = torch.Generator(device=DEV)
+    g.manual_seed(v)
+    most = 520
+    x = torch.randn(most, pitch, generator=g, device=DEV).mul_(2.5).to(dtype)[:, :v]
+    x[3, ::7] = x[3, 0]                     # ties
+    x[4] = -INF
+    x[4, v // 2] = 1.0
+    ids = some_ids(most, v, 2)
+    whole = qg.token_logprobs(x, ids, top=20)
+    for r0, m in [(0, 1), (3, 1), (4, 2), (1, 7), (0, 16), (2, 40), (5, 62), (30, 100), (100, 200), (17, 500)]:
+        part = qg.token_logprobs(x[r0:r0 + m], ids[r0:r0 + m].contiguous(), top=20)
+        assert torch.equal(part[2], whole[2][r0:r0 + m])
+        for a, b, t in [(part[0], whole[0], 0), (part[1], whole[1], 2), (part[3], whole[3], 0)]:
+            b = b[r0:r0 + m].double()
+            # (|T / S| is at most the entropy's own size: both of its terms are positive)
+            near(a, b, 4e-5 * (1 + t * b.abs()) + 4 * 2.0 ** -24 * b.abs(), "batch of %d from %d" % (m, r0))
+    moved = torch.empty(70 * pitch + 8, dtype=dtype, device=DEV)
+    for shift in range(1, 8):
+        place = moved[shift:shift + 70 * pitch].view(70, pitch)[:, :v]
+        place.copy_(x[:70])
+        part = qg.token_logprobs(place, ids[:70].contiguous(), top=20)
+        assert torch.equal(part[2], whole[2][:70])
+        for a, b, t in [(part[0], whole[0], 0), (part[1], whole[1], 2), (part[3], whole[3], 0)]:
+            b = b[:70].double()
+            near(a, b, 4e-5 * (1 + t * b.abs()) + 4 * 2.0 ** -24 * b.abs(), "at an address + %d" % shift)
