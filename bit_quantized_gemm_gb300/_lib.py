@@ -62,6 +62,8 @@ def load():
         "qg_linear_workspace_bytes": ([I, I64, I64], SZ),
         "qg_debug_prefill_plan_q8_0": ([I64, I64, I, P, P, P], I),
         "qg_debug_prefill_tile_q4k": ([I64, I64, I, P, P], I),
+        "qg_debug_gemm_fp8_tile": ([I64, I64, I, P, P], I),
+        "qg_debug_logprobs_pieces": ([I64, I64, I, P], I),
         "qg_linear_w8a8_q8_0": ([P, I, I64, I64, I64, P, I64, P, I, I64, P, P, SZ, P], I),
         "qg_linear_w4a8_q4k": ([P, I, I64, I64, I64, P, I64, P, I, I64, P, P, SZ, P], I),
         "qg_linear_w8a8_q8_0_noalloc": ([P, I, I64, I64, I64, P, I64, P, I, I64, P, P], I),
@@ -495,6 +497,20 @@ def linear_w8a8_q8_0_noalloc(x, packed, N, out=None, out_dtype=torch.bfloat16, s
         _ptr(x), _dtype_code(x.dtype), M, K, x.stride(0), _ptr(packed), N, _ptr(out),
         _dtype_code(out.dtype), out.stride(0), _ptr(scale_out), _stream(stream)))
     return out
+
+
+def gemm_fp8_tile(M, N, sms):
+    """Test support (host-only): (tokens, weight rows) of gemm_fp8's tile for M x N on `sms` SMs."""
+    tokens, rows = ctypes.c_int(), ctypes.c_int()
+    _check(load().qg_debug_gemm_fp8_tile(M, N, sms, ctypes.byref(tokens), ctypes.byref(rows)))
+    return tokens.value, rows.value
+
+
+def logprobs_pieces(M, V, sms):
+    """Test support (host-only): the pieces token_logprobs cuts a row of V into, for M rows on `sms` SMs."""
+    pieces = ctypes.c_int()
+    _check(load().qg_debug_logprobs_pieces(M, V, sms, ctypes.byref(pieces)))
+    return pieces.value
 
 
 def prefill_tile_q4k(M, N, sms):

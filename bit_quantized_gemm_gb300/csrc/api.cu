@@ -54,6 +54,8 @@ cudaError_t launch_gemm_fp8(const uint8_t* q, const float* scale, int64_t lds, i
 cudaError_t launch_token_logprobs(const void* logits, bool bf16, int64_t M, int64_t V, int64_t ldl,
                                   const int64_t* ids, int64_t G, float* logprobs, float* entropy,
                                   int top, int64_t* top_ids, float* top_logprobs, cudaStream_t st);
+void fp8_tile(int64_t M, int64_t N, int sms, int* tokens, int* rows);
+int lp_splits(int64_t M, int64_t V, int sms);
 }  // namespace qg
 
 using namespace qg;
@@ -339,6 +341,24 @@ qg_status qg_debug_prefill_tile_q4k(int64_t M, int64_t N, int sms, int* kind, in
     return fail(QG_EINVAL, "M, N out of range [1, 2^24]");
   if (sms < 1 || sms > 4096) return fail(QG_EINVAL, "sms=%d out of range [1, 4096]", sms);
   *tokens = prefill_tile_q4k(M, N, sms, kind);
+  return QG_OK;
+}
+
+qg_status qg_debug_gemm_fp8_tile(int64_t M, int64_t N, int sms, int* tokens, int* rows) {
+  if (!tokens || !rows) return fail(QG_EINVAL, "null pointer argument");
+  if (M < 1 || M > kMaxM || N < 1 || N > kMaxN)
+    return fail(QG_EINVAL, "M, N out of range [1, 2^24]");
+  if (sms < 1 || sms > 4096) return fail(QG_EINVAL, "sms=%d out of range [1, 4096]", sms);
+  fp8_tile(M, N, sms, tokens, rows);
+  return QG_OK;
+}
+
+qg_status qg_debug_logprobs_pieces(int64_t M, int64_t V, int sms, int* pieces) {
+  if (!pieces) return fail(QG_EINVAL, "null pointer argument");
+  if (M < 1 || M > kMaxM || V < 1 || V > kMaxV)
+    return fail(QG_EINVAL, "M, V out of range [1, 2^24]");
+  if (sms < 1 || sms > 4096) return fail(QG_EINVAL, "sms=%d out of range [1, 4096]", sms);
+  *pieces = lp_splits(M, V, sms);
   return QG_OK;
 }
 

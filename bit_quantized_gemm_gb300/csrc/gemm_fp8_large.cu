@@ -44,6 +44,11 @@ cudaError_t launch_gemm_fp8_small(const uint8_t* q, const float* scale, int64_t 
                                   int64_t K, const uint8_t* w, int64_t ldw, const float* w_scale,
                                   int64_t N, void* out, bool out_f32, int64_t ldo, uint32_t* err,
                                   bool pdl, cudaStream_t st);
+void fp8_small_tile(int64_t M, int64_t N, int sms, int* tokens, int* rows);
+
+// up to 64 tokens stream the weights (64 x 5120 x 17408: 18.7 us, 19.3 here; 64 x
+// 17408 x 5120: 26.6 us, 41.9 here)
+constexpr int64_t kFp8SmallM = 64;
 
 struct Fp8LargeArgs {
   const float* scale;    // [KB][lds]
@@ -591,28 +596,41 @@ static cudaError_t launch_large(const uint8_t* q, int64_t K, const uint8_t* w, i
   return cudaLaunchKernelEx(&cfg, kern, tq, tw, ts, to, a);
 }
 
-template <bool kF32>
-static cudaError_t launch_large_any(const uint8_t* q, int64_t K, const uint8_t* w, int64_t ldw,
-                                    const Fp8LargeArgs& a, cudaStream_t st) {
-  // the tile of the smallest estimated time: waves x ns per block of K
-  // (measured with forced choices at 8192 x 5120 x 17408)
-  struct Choice {
-    bool pair;
-    int w;
-    double step;
-  };
-  static const Choice kChoices[] = {{true, 256, 481}, {true, 128, 252}, {false, 128, 276}, {false, 64, 236}};
-  const int sms = num_sms();
-  int best = 0;
+// The tiles, and their ns per block of K (measured with forced choices at
+// 8192 x 5120 x 17408)
+struct Fp8LargeChoice {
+  bool pair;
+  int w;
+  double step;
+};
+static const Fp8LargeChoice kChoices[] = {{true, 256, 481}, {true, 128, 252}, {false, 128, 276}, {false, 64, 236}};
+
+// the tile of the smallest estimated time: waves x ns per block
+static int fp8_large_choice(int64_t M, int64_t N, int sms) {
+  int best = 3;
   double best_t = 1e300;
   for (int i = 0; i < 4; ++i) {
-    const Choice& c = kChoices[i];
+    const Fp8LargeChoice& c = kChoices[i];
     const int ctas = c.pair ? 2 : 1;
-    const int64_t tiles = ceil_div(a.M, 128 * ctas) * ceil_div(a.N, c.w);
+    if (sms < ctas) continue;
+    const int64_t tiles = ceil_div(M, 128 * ctas) * ceil_div(N, c.w);
     const double t = (double)ceil_div(tiles, sms / ctas) * c.step;
     if (t < best_t) { best_t = t; best = i; }
   }
-  switch (best) {
+  return best;
+}
+
+void fp8_tile(int64_t M, int64_t N, int sms, int* tokens, int* rows) {
+  if (M <= kFp8SmallM) return fp8_small_tile(M, N, sms, tokens, rows);
+  const Fp8LargeChoice& c = kChoices[fp8_large_choice(M, N, sms)];
+  *tokens = c.pair ? 256 : 128;
+  *rows = c.w;
+}
+
+template <bool kF32>
+static cudaError_t launch_large_any(const uint8_t* q, int64_t K, const uint8_t* w, int64_t ldw,
+                                    const Fp8LargeArgs& a, cudaStream_t st) {
+  switch (fp8_large_choice(a.M, a.N, num_sms())) {
     case 0: return launch_large<true, 256, kF32>(q, K, w, ldw, a, st);
     case 1: return launch_large<true, 128, kF32>(q, K, w, ldw, a, st);
     case 2: return launch_large<false, 128, kF32>(q, K, w, ldw, a, st);
@@ -624,9 +642,7 @@ cudaError_t launch_gemm_fp8(const uint8_t* q, const float* scale, int64_t lds, i
                             const uint8_t* w, int64_t ldw, const float* w_scale, int64_t N,
                             void* out, bool out_f32, int64_t ldo, uint32_t* err, bool pdl,
                             cudaStream_t st) {
-  // up to 64 tokens stream the weights (64 x 5120 x 17408: 18.7 us, 19.3 here; 64 x
-  // 17408 x 5120: 26.6 us, 41.9 here)
-  if (M <= 64)
+  if (M <= kFp8SmallM)
     return launch_gemm_fp8_small(q, scale, lds, M, K, w, ldw, w_scale, N, out, out_f32, ldo, err,
                                  pdl, st);
   Fp8LargeArgs a{scale, w_scale, out, lds, ldo, (int)M, (int)N, (int)ceil_div(K, 128),

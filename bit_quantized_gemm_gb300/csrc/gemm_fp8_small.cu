@@ -333,15 +333,20 @@ static cudaError_t launch_small(const CUtensorMap& tw, const uint8_t* q, const f
   return launch_kernel(kern, grid, dim3(C::kThreads), smem, st, pdl, tw, tq, ts, a);
 }
 
+// Tile of up to 64 tokens. 64-row tiles while all of them run at once, else 128-row
+// tiles, which read the tokens half as often (16 tokens: 17408 -> 5120, 80 tiles 17.7
+// us, 24.4 as 40 of 128; 5120 -> 10000, 157 tiles 13.8 us, 12.6 as 79)
+void fp8_small_tile(int64_t M, int64_t N, int sms, int* tokens, int* rows) {
+  *tokens = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  *rows = ceil_div(N, 64) <= sms ? 64 : 128;
+}
+
 cudaError_t launch_gemm_fp8_small(const uint8_t* q, const float* scale, int64_t lds, int64_t M,
                                   int64_t K, const uint8_t* w, int64_t ldw, const float* w_scale,
                                   int64_t N, void* out, bool out_f32, int64_t ldo, uint32_t* err,
                                   bool pdl, cudaStream_t st) {
-  const int bm = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-  // 64-row tiles while all of them run at once, else 128-row tiles, which read
-  // the tokens half as often (16 tokens: 17408 -> 5120, 80 tiles 17.7 us, 24.4 as 40
-  // of 128; 5120 -> 10000, 157 tiles 13.8 us, 12.6 as 79)
-  const int r = ceil_div(N, 64) <= num_sms() ? 64 : 128;
+  int bm, r;
+  fp8_small_tile(M, N, num_sms(), &bm, &r);
   CUtensorMap tw;
   if (!make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, K, N, ldw, 128, r,
                     CU_TENSOR_MAP_SWIZZLE_128B))

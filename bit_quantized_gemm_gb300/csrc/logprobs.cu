@@ -620,9 +620,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
 // an SM (200 x 131072 bf16, top 5: 24.3 us, 27.8 up to 2 an SM; 64 x 131072, top
 // 20: 18.2 us, 20.4 up to 3.75), none much shorter than a chunk of 4096 bf16
 // values (two of fp32).
-static int lp_splits(int64_t M, int64_t V) {
+int lp_splits(int64_t M, int64_t V, int sms) {
   int s = 1;
-  while (s < kLpMaxSplits && M * s * 4 < 13 * (int64_t)num_sms() && V > 4096 * (int64_t)s) s *= 2;
+  while (s < kLpMaxSplits && M * s * 4 < 13 * (int64_t)sms && V > 4096 * (int64_t)s) s *= 2;
   return s;
 }
 
@@ -672,7 +672,7 @@ static cudaError_t launch_lp(const LpArgs& a, int64_t M, cudaStream_t st) {
 cudaError_t launch_token_logprobs(const void* logits, bool bf16, int64_t M, int64_t V, int64_t ldl,
                                   const int64_t* ids, int64_t G, float* logprobs, float* entropy,
                                   int top, int64_t* top_ids, float* top_logprobs, cudaStream_t st) {
-  const LpArgs a{logits, V, ldl, ids, logprobs, entropy, top_ids, top_logprobs, (int)G, top, lp_splits(M, V)};
+  const LpArgs a{logits, V, ldl, ids, logprobs, entropy, top_ids, top_logprobs, (int)G, top, lp_splits(M, V, num_sms())};
   return bf16 ? launch_lp<true>(a, M, st) : launch_lp<false>(a, M, st);
 }
 

@@ -399,6 +399,15 @@ qg_status qg_debug_prefill_plan_q8_0(int64_t M, int64_t N, int sms, int64_t* row
  * the result. */
 qg_status qg_debug_prefill_tile_q4k(int64_t M, int64_t N, int sms, int* kind, int* tokens);
 
+/* Test support: the tile of qg_gemm_fp8 for M x N on a GPU of `sms` SMs: *tokens
+ * (16, 32 or 64 in the kernel of up to 64 tokens, 128 of a CTA or 256 of a pair
+ * above) x *rows weight rows. Host-only. The tile never changes a bit. */
+qg_status qg_debug_gemm_fp8_tile(int64_t M, int64_t N, int sms, int* tokens, int* rows);
+
+/* Test support: the pieces that qg_token_logprobs cuts a row into, for M rows of
+ * V values on a GPU of `sms` SMs. Host-only. */
+qg_status qg_debug_logprobs_pieces(int64_t M, int64_t V, int sms, int* pieces);
+
 /* Test support for failure detection: launches one bounded wait on a
  * barrier that nothing completes; after `polls` polls (1 .. 2^20) it records
  * a timeout in the device error word and returns, leaving the context usable.

@@ -13,6 +13,7 @@ import pytest
 import torch
 
 import bit_quantized_gemm_gb300 as qg
+from bit_quantized_gemm_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +77,23 @@ def test_layer_calls_in_a_row(m, k, n):
     out = [qg.linear_fp8(x, w, ws, workspace=work) for _ in range(5)]
     for y in out:
         assert torch.equal(y, two)
+
+
+# Every tile of the kernel above 64 tokens, with more tiles than CTAs (or pairs) at once: rows that
+# leave by TMA and by element stores, an odd last block of K, more than 32 blocks (the weight scales of
+# the next 32 follow), more than 2048 tokens (a second group of the tile order), a short last token tile.
+@pytest.mark.parametrize("m,k,n,tile", [
+    (25600, 272, 64, (128, 64)), (20001, 656, 40, (128, 64)), (4890, 4208, 398, (128, 64)),
+    (777, 2576, 5003, (128, 128)), (300, 4208, 17408, (128, 128)), (5390, 4240, 775, (128, 128)),
+    (5390, 400, 776, (128, 128)),
+    (700, 656, 9000, (256, 128)), (4970, 4208, 778, (256, 128)), (4970, 272, 776, (256, 128)),
+    (2048, 4208, 9728, (256, 256)), (5783, 4240, 1164, (256, 256)), (5783, 400, 1163, (256, 256)),
+])
+def test_every_tile(m, k, n, tile):
+    sms = torch.cuda.get_device_properties(DEV).multi_processor_count
+    if sms == 152:
+        assert _lib.gemm_fp8_tile(m, n, sms) == tile
+    q, s, w, ws, want = exact_case(m, k, n)
+    for dtype in (torch.float32, torch.bfloat16):
+        for _ in range(2):
+            assert torch.equal(qg.gemm_fp8(q, s, w, ws, out_dtype=dtype), want.to(dtype))

@@ -18,6 +18,7 @@ import pytest
 import torch
 
 import bit_quantized_gemm_gb300 as qg
+from bit_quantized_gemm_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +131,51 @@ def test_rows_in_other_batches_and_places(v, pitch, dtype):
         for a, b, t in [(part[0], whole[0], 0), (part[1], whole[1], 2), (part[3], whole[3], 0)]:
             b = b[:70].double()
             near(a, b, 4e-5 * (1 + t * b.abs()) + 4 * 2.0 ** -24 * b.abs(), "at an address + %d" % shift)
+
+
+# One CTA over a whole long row: 32 to 128 chunks, candidates that are ranked after up to 64 of them,
+# more candidates than their buffer holds (ascending rows), and the values around the aligned part of a
+# row, which come last but may have the lowest indices.
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("v,pitch", [(131072, 131072), (200003, 200003), (262143, 262151)])
+def test_whole_rows(v, pitch, dtype):
+    m = 512
+    sms = torch.cuda.get_device_properties(DEV).multi_processor_count
+    if sms == 152:
+        assert _lib.logprobs_pieces(m, v, sms) == 1
+    g = torch.Generator(device=DEV)
+    g.manual_seed(pitch)
+    x = torch.randn(m, pitch, generator=g, device=DEV).mul_(2.5)[:, :v]
+    up = torch.arange(v, device=DEV).float() / v
+    x[0:6] = up                                     # ascending, with runs of equal values in bf16
+    x[6:12] = -up
+    x[12:18] = 0.0                                  # all equal
+    x[18:24] = (torch.arange(v, device=DEV) % 3).float()
+    for r in range(24, 48):                         # the largest in the unaligned ends, ties among them
+        x[r, :8] = 30.0
+        x[r, v - 8:] = 30.0
+        x[r, v // 2] = 30.0 + r % 2
+    x[48:56, 1:] = 5.0                              # a first value that ties with all the rest, or not
+    x[48:56, 0] = torch.tensor([5.0, 6.0, 4.0, 5.0, -INF, 5.0, 6.0, 5.0], device=DEV)
+    x[56:64] = -INF                                 # nothing, one value, a few
+    x[57, v - 1] = 2.0
+    x[58, 0] = 2.0
+    x[59, ::v // 20] = 1.0
+    x[60, 5000:5040] = 3.0
+    x[64:72, ::2] = -INF
+    x[72, v // 3] = math.nan
+    x[73, v - 1] = INF
+    x[74:80, : v - 3000] = -INF                     # only the last chunks have any
+    x[80:86] = up * up * 40.0                       # a maximum that rises to the end
+    x[86:90] = torch.finfo(dtype).min
+    x[87, 77] = 0.0
+    x = x.to(dtype)
+    if pitch != v:
+        room = torch.zeros(m, pitch, dtype=dtype, device=DEV)
+        room[:, :v] = x
+        x = room[:, :v]
+    ids = some_ids(m, v, 3)
+    ids[::5, 1] = -1
+    ids[::7, 2] = v
+    for top in (0, 1, 5, 32):
+        check(x, ids, top)
