@@ -616,13 +616,15 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_kernel(con
   cluster_wait();
 }
 
-// Pieces per row, a power of two: doubled while there are fewer than 3.25 CTAs
-// an SM (200 x 131072 bf16, top 5: 24.3 us, 27.8 up to 2 an SM; 64 x 131072, top
-// 20: 18.2 us, 20.4 up to 3.75), none much shorter than a chunk of 4096 bf16
-// values (two of fp32).
+// Pieces per row, a power of two, none much shorter than a chunk of 4096 bf16 values
+// (two of fp32). Doubled while there are fewer than 3.25 CTAs an SM (131072 bf16, top
+// 5: 200 rows 24.2 us in 4 pieces, 27.1 in 2; 246 rows 27.0 in 4, 29.1 in 2; 247 to
+// 493 rows 29.2 to 39.5 in 2, 36.4 to 42.8 whole), but to 16, where a row's join is the
+// longest, only below 2 (31 rows 11.4 us, 12.6 in 8; 40 rows 12.5 and 13.1; 42 rows
+// 13.8 and 13.3; 61 rows 16.4 and 14.4).
 int lp_splits(int64_t M, int64_t V, int sms) {
   int s = 1;
-  while (s < kLpMaxSplits && M * s * 4 < 13 * (int64_t)sms && V > 4096 * (int64_t)s) s *= 2;
+  while (s < kLpMaxSplits && M * s * 4 < (s < 8 ? 13 : 8) * (int64_t)sms && V > 4096 * (int64_t)s) s *= 2;
   return s;
 }
 

@@ -28,12 +28,14 @@ def test_tiles_follow_the_tokens(sms):
 def test_pieces():
     for v in (1, 100, 4096, 4097, 32768, 131072, 1 << 24):
         last = 16
-        for m in (1, 2, 16, 61, 62, 200, 493, 494, 4096, 1 << 24):
+        for m in (1, 2, 16, 37, 38, 61, 62, 200, 493, 494, 4096, 1 << 24):
             pieces = _lib.logprobs_pieces(m, v, 152)
             assert pieces in (1, 2, 4, 8, 16) and pieces <= last
             assert pieces == 1 or v > 4096 * (pieces // 2)
             last = pieces
-    assert _lib.logprobs_pieces(1, 131072, 152) == 16 and _lib.logprobs_pieces(494, 1 << 24, 152) == 1
+    # 16 pieces were slower than 8 from about 42 rows on (61 rows of 131072: 16.4 and 14.4 us)
+    assert [_lib.logprobs_pieces(m, 131072, 152) for m in (1, 31, 37, 42, 61, 64)] == [16, 16, 16, 8, 8, 8]
+    assert _lib.logprobs_pieces(494, 1 << 24, 152) == 1
 
 
 def test_refusals():
