@@ -11,9 +11,13 @@
 // that a thread owns one token and a span of columns inside one block of 128
 // weight rows: s * ws is one number per thread and block, the chain one FMA per
 // output and block (256 cycles of the FMA pipe for a block of 512 MMA cycles).
-// Measured at 8192 x 5120 x 17408: 558 us, 2.62 PFLOP/s, about 910 cycles per
-// block; without the epilogue's FMAs 457 us, without its loads and FMAs 446,
-// without the operand loads too 399 (the MMAs alone: 310 at 1.93 GHz).
+// Measured at 8192 x 5120 x 17408: 550-556 us from a graph, 2.6 PFLOP/s. In loops of
+// two seconds, with the SM clock sampled (median): 588 us at 1916 MHz, the power
+// limit, 971 cycles a block; without the epilogue's FMAs 551 us at 1980, 940 cycles;
+// without its loads too 547, 940; without the operand loads too 504 at 2070, 899. So
+// what bounds it is neither the epilogue's work nor the clock: with nothing left but
+// MMAs (512 cycles) and barriers a block still takes 900. What is left is the way of
+// a buffer from the commit over the epilogue and the scale warp back to its issuer.
 //
 // A tile is 128 tokens x W columns for one CTA, or 256 x W for a pair of CTAs
 // of one cluster (kPair): each CTA of the pair loads its own 128 tokens and
@@ -25,7 +29,8 @@
 // while the tensor core is busy, so one issuer's barrier waits have to overlap
 // the other's MMAs; one issuer 692 us); 3 scales; 4..11 epilogue: warp w reads
 // lanes 32*(w%4).. and half (w-4)/4 of the columns. Sixteen epilogue warps were
-// no faster (570 us), nor were half blocks of 128 columns in four buffers (599).
+// no faster (570 us), nor were half blocks of 128 columns in four buffers (599; both
+// when this form took 545 to 560).
 // Outputs are staged per warp in shared memory (32 rows of 64 bytes, swizzled)
 // and leave by TMA, or by coalesced element stores where the row length or the
 // pitch is not a multiple of 16 bytes.
@@ -46,8 +51,8 @@ cudaError_t launch_gemm_fp8_small(const uint8_t* q, const float* scale, int64_t 
                                   bool pdl, cudaStream_t st);
 void fp8_small_tile(int64_t M, int64_t N, int sms, int* tokens, int* rows);
 
-// up to 64 tokens stream the weights (64 x 5120 x 17408: 18.7 us, 19.3 here; 64 x
-// 17408 x 5120: 26.6 us, 41.9 here)
+// up to 64 tokens stream the weights (64 x 5120 x 17408: 18.4 us, 19.0 here; 64 x
+// 17408 x 5120: 26.1 us, 35.5 here; 40 x 4096 x 131072: 84.0, 88.8)
 constexpr int64_t kFp8SmallM = 64;
 
 struct Fp8LargeArgs {

@@ -23,8 +23,8 @@
 // stage has an issuing warp of its own (17408 -> 5120, 1 token: 20.5 us with one
 // warp, 19.2 with two, 17.9 with four).
 //
-// Measured (from a CUDA graph): 16 tokens, 4096 -> 131072: 80.8 us, 6.69 TB/s,
-// what a copy reaches; 64 tokens 85.6 us; 5120 -> 17408: 16.8 us, 18.7 with 64
+// Measured (from a CUDA graph): 16 tokens, 4096 -> 131072: 82.5 us, 6.56 TB/s of the
+// 6.69 that a copy reaches; 64 tokens 87 us; 5120 -> 17408: 16.8 us, 18.4-19.1 with 64
 // tokens, of which about 4 are a launch's fixed share; 17408 -> 5120: 17.7 us and
 // 26.6 (80 tiles, each 136 blocks after one another: 163 cycles of MMAs a block,
 // 200 to 340 with the handshakes and the loads).

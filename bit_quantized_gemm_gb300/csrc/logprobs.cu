@@ -29,10 +29,10 @@
 // The pieces of a row are a cluster of CTAs, whose first one joins them.
 //
 // Measured (GB300, bf16, from a CUDA graph): 4096 x 131072 without alternatives
-// 161 us, 6.7 TB/s (a copy: 6.69); with 1, 5, 32 alternatives 180, 199, 278 us:
-// bound by issued instructions there (73 % of the slots; 8.9 a value without
-// alternatives, 10.7 with five). 2048 x 131072 fp32, 5 alternatives 169 us; 1 x
-// 131072 4.4 us, with 20 11 us.
+// 164-168 us, 6.4-6.5 TB/s (a copy: 6.69); with 1, 5, 20, 32 alternatives 182, 200,
+// 243, 275 us: bound by issued instructions there (73 % of the slots; 8.7 a value
+// without alternatives, 10.9 with five). 2048 x 131072 fp32, 5 alternatives 169 us; 1 x
+// 131072 4.2 us, with 5 8.7, with 20 10.3.
 #include <math_constants.h>
 
 #include "qg_common.cuh"
