@@ -12,7 +12,8 @@ from ._lib import (QGError, check_device_error, debug_block_sums, debug_wait_tim
                    q4k_packed_bytes, q8_0_packed_bytes, quantize_act, quantize_act_static,
                    small_m_max,
                    gemm_fp8, linear_fp8, linear_fp8_workspace_bytes, quantize_act_fp8,
-                   token_logprobs)
+                   token_logprobs, rmsnorm_quantize_act, rmsnorm_quantize_act_fp8,
+                   silu_mul_quantize_act_fp8, gemm_fp8_grouped, add_lora, add_lora_workspace_bytes)
 
 __all__ = ["QGError", "check_device_error", "debug_block_sums", "debug_wait_timeout",
            "declared_symbols", "gemm_launch_count",
@@ -23,4 +24,5 @@ __all__ = ["QGError", "check_device_error", "debug_block_sums", "debug_wait_time
            "q4k_packed_bytes", "q8_0_packed_bytes", "quantize_act", "quantize_act_static",
            "small_m_max",
            "gemm_fp8", "linear_fp8", "linear_fp8_workspace_bytes", "quantize_act_fp8",
-           "token_logprobs"]
+           "token_logprobs", "rmsnorm_quantize_act", "rmsnorm_quantize_act_fp8",
+           "silu_mul_quantize_act_fp8", "gemm_fp8_grouped", "add_lora", "add_lora_workspace_bytes"]

@@ -38,7 +38,7 @@ def load():
         raise RuntimeError("libqgemm.so is not built: run `python -m bit_quantized_gemm_gb300.build` "
                            "(or __graft_entry__.build()); there is no CPU fallback")
     L = ctypes.CDLL(SO_PATH)
-    P, I64, I, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+    P, I64, I, SZ, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
     sigs = {
         "qg_status_string": ([I], ctypes.c_char_p),
         "qg_last_error": ([], ctypes.c_char_p),
@@ -76,6 +76,12 @@ def load():
         "qg_linear_fp8_workspace_bytes": ([I64, I64], SZ),
         "qg_linear_fp8": ([P, I, I64, I64, I64, P, I64, P, I64, P, I, I64, P, SZ, P], I),
         "qg_token_logprobs": ([P, I, I64, I64, I64, P, I64, P, P, I, P, P, P], I),
+        "qg_rmsnorm_quantize_act_fp8": ([P, P, I, I64, I64, I64, I64, P, I, F, P, I64, P, P, I64, P], I),
+        "qg_rmsnorm_quantize_act": ([P, P, I, I64, I64, I64, I64, P, I, F, P, I64, P, P, P, P, P], I),
+        "qg_silu_mul_quantize_act_fp8": ([P, I, I64, I64, I64, P, P, I64, P], I),
+        "qg_gemm_fp8_grouped": ([P, P, I64, I64, I64, P, I64, P, I64, I64, P, I64, P, I, I64, P], I),
+        "qg_add_lora_workspace_bytes": ([I64, I64], SZ),
+        "qg_add_lora": ([P, I, I64, P, I, I64, I64, I64, P, P, I64, I64, I64, P, P, P, I64, P, SZ, P], I),
     }
     for name, (args, res) in sigs.items():
         f = getattr(L, name)
@@ -474,6 +480,227 @@ def token_logprobs(logits, ids, top=0, stream=None):
                                               top, top_ids.data_ptr(), top_logprobs.data_ptr(),
                                               _raw_stream(stream, dev)))
     return logprobs, entropy, top_ids, top_logprobs
+
+
+def _norm_inputs(x, weight, residual):
+    """(M, K, row stride of x, of residual, device), checked."""
+    M, K, ldx = _rows(x, "x", _CODES)
+    dev = x.get_device()
+    if (weight.get_device() != dev or weight.dtype not in _CODES or weight.shape != (K,)
+            or not weight.is_contiguous()):
+        raise ValueError("weight must be a contiguous bf16 or fp32 tensor of shape [K] on x's device")
+    if residual is None:
+        return M, K, ldx, 0, dev
+    m, k, ldr = _rows(residual, "residual", (x.dtype,), dev)
+    if m != M or k != K:
+        raise ValueError("residual must have the shape of x")
+    return M, K, ldx, ldr, dev
+
+
+def _norm_sum(total, x, M, K, stream, dev):
+    """(sum, its row stride): checked, allocated when None."""
+    if total is None:
+        return _empty((M, K), x.dtype, x.device, stream), K
+    m, k, ld = _rows(total, "sum", (x.dtype,), dev)
+    if m != M or k != K:
+        raise ValueError("sum must have the shape of x")
+    return total, ld
+
+
+def _ptr_or_none(t):
+    return None if t is None else t.data_ptr()
+
+
+def rmsnorm_quantize_act_fp8(x, weight, eps=1e-6, residual=None, out=None, stream=None):
+    """Norm of the rows of x (cuda [M, K] bf16/fp32, rows may be strided; K % 16 == 0), or of
+    x + residual, times weight (bf16/fp32 [K]), quantized as by quantize_act_fp8 -> (q float8_e4m3fn
+    [M, K], scale fp32 [ceil(K/128), M], x + residual in x's dtype or None). `out` may supply
+    preallocated (q, scale, sum); sum may be residual or x itself."""
+    M, K, ldx, ldr, dev = _norm_inputs(x, weight, residual)
+    _device(x, stream)
+    if out is None:
+        lds = (M + 3) // 4 * 4
+        q = _empty((M, K), _FP8, x.device, stream)
+        scale = _empty(((K + 127) // 128, M), _F32, x.device, stream, lds)
+        total = None
+    else:
+        q, scale, total = out
+        if _rows(q, "q", (_FP8,), dev) != (M, K, K):
+            raise ValueError("q must be contiguous and of the shape of x")
+        lds = _fp8_scale(scale, M, K, dev)
+    total, ldsum = (None, 0) if residual is None else _norm_sum(total, x, M, K, stream, dev)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return rmsnorm_quantize_act_fp8(x, weight, eps, residual, (q, scale, total), stream)
+    _check((_lib or load()).qg_rmsnorm_quantize_act_fp8(
+        x.data_ptr(), _ptr_or_none(residual), _CODES[x.dtype], M, K, ldx, ldr, weight.data_ptr(),
+        _CODES[weight.dtype], eps, _ptr_or_none(total), ldsum, q.data_ptr(), scale.data_ptr(), lds,
+        _raw_stream(stream, dev)))
+    return q, scale, total
+
+
+def rmsnorm_quantize_act(x, weight, eps=1e-6, residual=None, block_sums=False, q16=False, out=None,
+                         stream=None, int8=True):
+    """As rmsnorm_quantize_act_fp8, quantized as by quantize_act (K % 32 == 0) -> (q int8 [M, K] or
+    None, scale fp32 [M], block_sums int32 [M, K/32] or None, q16 fp16 [M, K] or None, x + residual
+    or None). `out` may supply preallocated (q, scale, block_sums, q16, sum)."""
+    M, K, ldx, ldr, dev = _norm_inputs(x, weight, residual)
+    _device(x, stream)
+    total = None
+    if out is None:
+        where = x.device
+        q = _empty((M, K), torch.int8, where, stream) if int8 else None
+        scale = _empty((M,), _F32, where, stream)
+        bs = _empty((M, K // 32), torch.int32, where, stream) if block_sums else None
+        h = _empty((M, K), torch.float16, where, stream) if q16 else None
+    else:
+        q, scale, bs, h, total = out
+        for t, name, dtype, shape in ((q, "q", torch.int8, (M, K)), (scale, "scale", _F32, (M,)),
+                                      (bs, "block_sums", torch.int32, (M, K // 32)),
+                                      (h, "q16", torch.float16, (M, K))):
+            if t is not None and (t.get_device() != dev or t.dtype != dtype or t.shape != shape
+                                  or not t.is_contiguous()):
+                raise ValueError("%s must be a contiguous %s tensor of shape %s on x's device" %
+                                 (name, dtype, shape))
+    total, ldsum = (None, 0) if residual is None else _norm_sum(total, x, M, K, stream, dev)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return rmsnorm_quantize_act(x, weight, eps, residual, out=(q, scale, bs, h, total), stream=stream)
+    _check((_lib or load()).qg_rmsnorm_quantize_act(
+        x.data_ptr(), _ptr_or_none(residual), _CODES[x.dtype], M, K, ldx, ldr, weight.data_ptr(),
+        _CODES[weight.dtype], eps, _ptr_or_none(total), ldsum, _ptr_or_none(q), _ptr_or_none(scale),
+        _ptr_or_none(bs), _ptr_or_none(h), _raw_stream(stream, dev)))
+    return q, scale, bs, h, total
+
+
+def silu_mul_quantize_act_fp8(x, out=None, stream=None):
+    """x: cuda [M, 2K] bf16/fp32 (rows may be strided; K % 16 == 0), K gates and K values up a row ->
+    silu(gate) * up quantized as by quantize_act_fp8: (q float8_e4m3fn [M, K], scale fp32
+    [ceil(K/128), M]). `out` may supply preallocated (q, scale)."""
+    M, K2, ldx = _rows(x, "x", _CODES)
+    if K2 % 2:
+        raise ValueError("x must have an even number of columns: gates, then values")
+    K = K2 // 2
+    dev = _device(x, stream)
+    if out is None:
+        lds = (M + 3) // 4 * 4
+        q = _empty((M, K), _FP8, x.device, stream)
+        scale = _empty(((K + 127) // 128, M), _F32, x.device, stream, lds)
+    else:
+        q, scale = out
+        if _rows(q, "q", (_FP8,), dev) != (M, K, K):
+            raise ValueError("q must be contiguous and of half the columns of x")
+        lds = _fp8_scale(scale, M, K, dev)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return silu_mul_quantize_act_fp8(x, (q, scale), stream)
+    _check((_lib or load()).qg_silu_mul_quantize_act_fp8(x.data_ptr(), _CODES[x.dtype], M, K, ldx,
+                                                         q.data_ptr(), scale.data_ptr(), lds,
+                                                         _raw_stream(stream, dev)))
+    return q, scale
+
+
+def _matrices(t, name, dtype, dev):
+    """(matrices, rows, columns, row stride, matrix stride) of a cuda tensor whose rows are contiguous."""
+    if t.get_device() == dev and t.dtype == dtype and t.dim() == 3:
+        e, n, k = t.shape
+        lde, ld, step = t.stride()
+        if step == 1 or k <= 1:
+            # (the distance of a single row or matrix to the next says nothing)
+            return e, n, k, ld if n > 1 else k, lde
+    raise ValueError("%s must be a 3-D cuda tensor of %s with contiguous rows, on device %d like the others "
+                     "of its call" % (name, dtype, dev))
+
+
+def gemm_fp8_grouped(q, scale, offsets, w, w_scale, out=None, out_dtype=torch.bfloat16, stream=None):
+    """gemm_fp8 with the weights of each row's expert: q, scale from quantize_act_fp8 (or one of its
+    siblings), rows sorted by expert; offsets: cuda int64 [E+1], expert e owns rows offsets[e] up to
+    offsets[e+1] (read on the device: no synchronisation); w: cuda float8_e4m3fn [E, N, K] (rows and
+    experts may be strided); w_scale: cuda fp32 [E, ceil(N/128), ceil(K/128)] -> out [M, N]. Rows of
+    no expert are left as they were (undefined in an `out` allocated here)."""
+    M, K, ldq = _rows(q, "q", (_FP8,))
+    if ldq != K:
+        raise ValueError("q must be contiguous")
+    dev = _device(q, stream)
+    lds = _fp8_scale(scale, M, K, dev)
+    E, N, k, ldw, lde = _matrices(w, "w", _FP8, dev)
+    if k != K:
+        raise ValueError("w has rows of %d values, the activations of %d" % (k, K))
+    if (offsets.get_device() != dev or offsets.dtype != torch.int64 or offsets.shape != (E + 1,)
+            or not offsets.is_contiguous()):
+        raise ValueError("offsets must be a contiguous int64 tensor of shape [E + 1] on q's device")
+    if (w_scale.get_device() != dev or w_scale.dtype != _F32 or not w_scale.is_contiguous()
+            or w_scale.shape != (E, (N + 127) // 128, (K + 127) // 128)):
+        raise ValueError("w_scale must be a contiguous fp32 tensor of shape [E, ceil(N/128), ceil(K/128)] "
+                         "on w's device")
+    if out is None:
+        if out_dtype not in _CODES:
+            raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+        out, ldo = _empty((M, N), out_dtype, q.device, stream), N
+    else:
+        m, n, ldo = _rows(out, "out", _CODES, dev)
+        if m != M or n != N:
+            raise ValueError("out must have the shape (%d, %d)" % (M, N))
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return gemm_fp8_grouped(q, scale, offsets, w, w_scale, out, stream=stream)
+    _check((_lib or load()).qg_gemm_fp8_grouped(q.data_ptr(), scale.data_ptr(), lds, M, K, offsets.data_ptr(),
+                                                E, w.data_ptr(), ldw, lde, w_scale.data_ptr(), N,
+                                                out.data_ptr(), _CODES[out.dtype], ldo,
+                                                _raw_stream(stream, dev)))
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def add_lora_workspace_bytes(M, rank):
+    """Workspace bytes an add_lora call of these sizes needs (0: invalid sizes)."""
+    return int(load().qg_add_lora_workspace_bytes(M, rank))
+
+
+def add_lora(base, x, a, b, ids, scaling=None, out=None, workspace=None, stream=None):
+    """Low-rank adapters beside a projection: out = base + scaling[id] * (x . a[id]^T) . b[id]^T row by
+    row, id = ids[m]; rows whose id is no adapter's (-1) keep base's bits. base: cuda [M, N] bf16/fp32,
+    the projection's output; x: cuda [M, K] bf16/fp32, its input (K % 16 == 0); rows of both may be
+    strided; a, b: contiguous cuda bf16 [adapters, rank, K], [adapters, N, rank] (rank a multiple of 8,
+    at most 128); ids: cuda int64 [M]; scaling: cuda fp32 [adapters] or None for 1 -> out [M, N] of
+    base's dtype. `out` may be base itself. Through `workspace` (allocated here when not given)."""
+    M, N, ldb = _rows(base, "base", _CODES)
+    dev = _device(base, stream)
+    m, K, ldx = _rows(x, "x", _CODES, dev)
+    if m != M:
+        raise ValueError("x has %d rows, base %d" % (m, M))
+    for t, name in ((a, "a"), (b, "b")):
+        if t.get_device() != dev or t.dtype != _BF16 or t.dim() != 3 or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous 3-D bf16 tensor on base's device" % name)
+    count, rank, k = a.shape
+    if k != K or b.shape != (count, N, rank):
+        raise ValueError("a and b must have the shapes [adapters, rank, %d] and [adapters, %d, rank]" % (K, N))
+    if ids.get_device() != dev or ids.dtype != torch.int64 or ids.shape != (M,) or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int64 tensor of shape [M] on base's device")
+    if scaling is not None and (scaling.get_device() != dev or scaling.dtype != _F32
+                                or scaling.shape != (count,) or not scaling.is_contiguous()):
+        raise ValueError("scaling must be a contiguous fp32 tensor of shape [adapters] on base's device")
+    if out is None:
+        out, ldo = _empty((M, N), base.dtype, base.device, stream), N
+    else:
+        m, n, ldo = _rows(out, "out", (base.dtype,), dev)
+        if m != M or n != N:
+            raise ValueError("out must have the shape (%d, %d)" % (M, N))
+    if workspace is None:
+        nbytes = add_lora_workspace_bytes(M, rank)
+        workspace = _empty((nbytes,), torch.uint8, base.device, stream)
+    else:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on base's device")
+        nbytes = workspace.numel() * workspace.element_size()
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return add_lora(base, x, a, b, ids, scaling, out, workspace, stream)
+    _check((_lib or load()).qg_add_lora(base.data_ptr(), _CODES[base.dtype], ldb, x.data_ptr(),
+                                        _CODES[x.dtype], M, K, ldx, a.data_ptr(), b.data_ptr(), count, rank, N,
+                                        ids.data_ptr(), _ptr_or_none(scaling), out.data_ptr(), ldo,
+                                        workspace.data_ptr(), nbytes, _raw_stream(stream, dev)))
+    return out
 
 
 def linear_noalloc_scratch_bytes():

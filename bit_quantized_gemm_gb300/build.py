@@ -14,7 +14,8 @@ CSRC = os.path.join(HERE, "csrc")
 SO = os.path.join(HERE, "libqgemm.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "quantize.cu", "pack.cu", "gemm_small.cu", "gemm_large.cu", "gemm_skinny.cu",
-           "quantize_fp8.cu", "gemm_fp8_small.cu", "gemm_fp8_large.cu", "logprobs.cu"]
+           "quantize_fp8.cu", "gemm_fp8_small.cu", "gemm_fp8_large.cu", "logprobs.cu",
+           "norm_quantize.cu", "gemm_fp8_grouped.cu", "lora.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "-Xptxas", "-v", "-I", os.path.join(HERE, "..", "include")]

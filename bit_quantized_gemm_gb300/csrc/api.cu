@@ -55,6 +55,23 @@ cudaError_t launch_token_logprobs(const void* logits, bool bf16, int64_t M, int6
                                   const int64_t* ids, int64_t G, float* logprobs, float* entropy,
                                   int top, int64_t* top_ids, float* top_logprobs, cudaStream_t st);
 void fp8_tile(int64_t M, int64_t N, int sms, int* tokens, int* rows);
+cudaError_t launch_norm_quantize(const void* x, const void* res, bool bf16, int64_t M, int64_t K,
+                                 int64_t ldx, int64_t ldr, const void* weight, bool weight_bf16,
+                                 float eps, void* sum, int64_t ldsum, bool fp8, uint8_t* q,
+                                 uint16_t* q16, int32_t* bsum, float* scale, int64_t lds,
+                                 cudaStream_t st);
+cudaError_t launch_silu_mul_quantize_fp8(const void* x, bool bf16, int64_t M, int64_t K, int64_t ldx,
+                                         uint8_t* q, float* scale, int64_t lds, cudaStream_t st);
+cudaError_t launch_gemm_fp8_grouped(const uint8_t* q, const float* scale, int64_t lds, int64_t M,
+                                    int64_t K, const int64_t* offsets, int64_t E, const uint8_t* w,
+                                    int64_t ldw, int64_t lde, const float* w_scale, int64_t N,
+                                    void* out, bool out_f32, int64_t ldo, uint32_t* err,
+                                    cudaStream_t st);
+int lora_padded_rank(int64_t rank);
+cudaError_t launch_add_lora(const void* base, bool bf16, int64_t ldb, const void* x, bool x_bf16,
+                            int64_t M, int64_t K, int64_t ldx, const void* A, const void* B,
+                            int64_t count, int64_t rank, int64_t N, const int64_t* ids,
+                            const float* scaling, void* out, int64_t ldo, void* ws, cudaStream_t st);
 int lp_splits(int64_t M, int64_t V, int sms);
 }  // namespace qg
 
@@ -79,6 +96,9 @@ constexpr int64_t kMaxN = int64_t(1) << 24;
 constexpr int64_t kMaxM = int64_t(1) << 24;
 constexpr int64_t kMaxV = int64_t(1) << 24;
 constexpr int64_t kMaxGiven = int64_t(1) << 16;
+constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxLoraM = int64_t(1) << 20;
+constexpr int64_t kMaxLoras = int64_t(1) << 20;
 constexpr int kFp8Block = 128;         // values of K (and rows of N) that share an FP8 scale
 
 thread_local char t_last_error[256] = "";
@@ -277,6 +297,41 @@ struct LinearFp8Ws {
     total = align_up(off_q + M * K, 256);
   }
 };
+
+qg_status check_dtype(qg_dtype dt, const char* name) {
+  if (dt != QG_BF16 && dt != QG_F32) return fail(QG_EINVAL, "%s must be QG_BF16 or QG_F32", name);
+  return QG_OK;
+}
+
+// a matrix of M rows of `cols` values in 16-byte pieces
+qg_status check_rows16(const void* p, qg_dtype dt, int64_t ld, int64_t cols, const char* name) {
+  if (ld < cols)
+    return fail(QG_EINVAL, "ld%s=%lld < %lld", name, (long long)ld, (long long)cols);
+  if (!aligned(p, 16) || (ld * (dt == QG_BF16 ? 2 : 4)) % 16 != 0)
+    return fail(QG_EALIGN, "%s needs 16-byte alignment and a row stride that is a multiple of 16 bytes",
+                name);
+  return QG_OK;
+}
+
+// the inputs of both norms, and the sum that they write
+qg_status check_norm(const void* x, const void* residual, qg_dtype xdt, int64_t M, int64_t K,
+                     int64_t ldx, int64_t ldr, const void* weight, qg_dtype wdt, float eps,
+                     const void* sum, int64_t ldsum) {
+  if (!x || !weight) return fail(QG_EINVAL, "null pointer argument");
+  if ((residual == nullptr) != (sum == nullptr))
+    return fail(QG_EINVAL, "residual and sum are given together or not at all");
+  qg_status s = check_dtype(xdt, "x_dtype");
+  if (s == QG_OK) s = check_dtype(wdt, "weight_dtype");
+  if (s != QG_OK) return s;
+  if (M < 1 || M > kMaxM) return fail(QG_EINVAL, "M=%lld out of range [1, 2^24]", (long long)M);
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return fail(QG_EINVAL, "eps must be a finite number, 0 or more");
+  s = check_rows16(x, xdt, ldx, K, "x");
+  if (s == QG_OK && residual) s = check_rows16(residual, xdt, ldr, K, "r");
+  if (s == QG_OK && residual) s = check_rows16(sum, xdt, ldsum, K, "sum");
+  if (s != QG_OK) return s;
+  if (!aligned(weight, 16)) return fail(QG_EALIGN, "weight needs 16-byte alignment");
+  return QG_OK;
+}
 
 // Device address of g_linear_scratch on the current device, looked up once
 // per device (with that device current) and cached; nullptr if the lookup
@@ -657,6 +712,124 @@ qg_status qg_linear_fp8(const void* x, qg_dtype x_dtype, int64_t M, int64_t K, i
   return from_cuda(launch_gemm_fp8(q, scale, L.lds, M, K, w, ldw, w_scale, N, out,
                                    out_dtype == QG_F32, ldo, error_word(), true, st),
                    "FP8 GEMM launch");
+}
+
+qg_status qg_rmsnorm_quantize_act_fp8(const void* x, const void* residual, qg_dtype x_dtype,
+                                      int64_t M, int64_t K, int64_t ldx, int64_t ldr,
+                                      const void* weight, qg_dtype weight_dtype, float eps,
+                                      void* sum, int64_t ldsum, uint8_t* q, float* scale,
+                                      int64_t lds, void* stream) {
+  if (!q || !scale) return fail(QG_EINVAL, "null pointer argument");
+  qg_status s = check_fp8_k(K);
+  if (s == QG_OK) s = check_norm(x, residual, x_dtype, M, K, ldx, ldr, weight, weight_dtype, eps, sum, ldsum);
+  if (s == QG_OK) s = check_fp8_scale(scale, lds, M);
+  if (s != QG_OK) return s;
+  if (!aligned(q, 16)) return fail(QG_EALIGN, "q needs 16-byte alignment");
+  return from_cuda(launch_norm_quantize(x, residual, x_dtype == QG_BF16, M, K, ldx, ldr, weight,
+                                        weight_dtype == QG_BF16, eps, sum, ldsum, true, q, nullptr,
+                                        nullptr, scale, lds, reinterpret_cast<cudaStream_t>(stream)),
+                   "norm launch");
+}
+
+qg_status qg_rmsnorm_quantize_act(const void* x, const void* residual, qg_dtype x_dtype, int64_t M,
+                                  int64_t K, int64_t ldx, int64_t ldr, const void* weight,
+                                  qg_dtype weight_dtype, float eps, void* sum, int64_t ldsum,
+                                  int8_t* q, float* scale, int32_t* block_sums, uint16_t* q16,
+                                  void* stream) {
+  if (!scale || (!q && !q16)) return fail(QG_EINVAL, "null pointer argument (scale, or both q and q16)");
+  qg_status s = check_k(K, kBlk);
+  if (s == QG_OK) s = check_norm(x, residual, x_dtype, M, K, ldx, ldr, weight, weight_dtype, eps, sum, ldsum);
+  if (s != QG_OK) return s;
+  if ((q && !aligned(q, 16)) || (q16 && !aligned(q16, 16)) || !aligned(scale, 4) ||
+      (block_sums && !aligned(block_sums, 4)))
+    return fail(QG_EALIGN, "q and q16 need 16-byte, scale and block_sums 4-byte alignment");
+  return from_cuda(launch_norm_quantize(x, residual, x_dtype == QG_BF16, M, K, ldx, ldr, weight,
+                                        weight_dtype == QG_BF16, eps, sum, ldsum, false,
+                                        reinterpret_cast<uint8_t*>(q), q16, block_sums, scale, 0,
+                                        reinterpret_cast<cudaStream_t>(stream)),
+                   "norm launch");
+}
+
+qg_status qg_silu_mul_quantize_act_fp8(const void* x, qg_dtype x_dtype, int64_t M, int64_t K,
+                                       int64_t ldx, uint8_t* q, float* scale, int64_t lds,
+                                       void* stream) {
+  if (!x || !q || !scale) return fail(QG_EINVAL, "null pointer argument");
+  qg_status s = check_dtype(x_dtype, "x_dtype");
+  if (s != QG_OK) return s;
+  if (M < 1 || M > kMaxM) return fail(QG_EINVAL, "M=%lld out of range [1, 2^24]", (long long)M);
+  s = check_fp8_k(K);
+  if (s == QG_OK) s = check_rows16(x, x_dtype, ldx, 2 * K, "x");
+  if (s == QG_OK) s = check_fp8_scale(scale, lds, M);
+  if (s != QG_OK) return s;
+  if (!aligned(q, 16)) return fail(QG_EALIGN, "q needs 16-byte alignment");
+  return from_cuda(launch_silu_mul_quantize_fp8(x, x_dtype == QG_BF16, M, K, ldx, q, scale, lds,
+                                                reinterpret_cast<cudaStream_t>(stream)),
+                   "gate launch");
+}
+
+qg_status qg_gemm_fp8_grouped(const uint8_t* q, const float* scale, int64_t lds, int64_t M, int64_t K,
+                              const int64_t* offsets, int64_t experts, const uint8_t* w, int64_t ldw,
+                              int64_t lde, const float* w_scale, int64_t N, void* out,
+                              qg_dtype out_dtype, int64_t ldo, void* stream) {
+  if (!q || !scale || !offsets || !w || !w_scale || !out) return fail(QG_EINVAL, "null pointer argument");
+  if (M < 1 || M > kMaxM) return fail(QG_EINVAL, "M=%lld out of range [1, 2^24]", (long long)M);
+  if (experts < 1 || experts > kMaxExperts)
+    return fail(QG_EINVAL, "experts=%lld out of range [1, %lld]", (long long)experts, (long long)kMaxExperts);
+  qg_status s = check_fp8_k(K);
+  if (s == QG_OK) s = check_fp8_scale(scale, lds, M);
+  if (s == QG_OK) s = check_fp8_w(w, ldw, w_scale, N, K, out, out_dtype, ldo);
+  if (s != QG_OK) return s;
+  // (the distance of a single expert to the next says nothing)
+  if (experts == 1) lde = N * ldw;
+  if (lde < (N - 1) * ldw + K)
+    return fail(QG_EINVAL, "lde=%lld < %lld, an expert's weights", (long long)lde,
+                (long long)((N - 1) * ldw + K));
+  if (!aligned(q, 16) || !aligned(offsets, 8) || lde % 16 != 0)
+    return fail(QG_EALIGN, "q needs 16-byte, offsets 8-byte alignment, lde a multiple of 16");
+  return from_cuda(launch_gemm_fp8_grouped(q, scale, lds, M, K, offsets, experts, w, ldw, lde, w_scale,
+                                           N, out, out_dtype == QG_F32, ldo, error_word(),
+                                           reinterpret_cast<cudaStream_t>(stream)),
+                   "grouped FP8 GEMM launch");
+}
+
+size_t qg_add_lora_workspace_bytes(int64_t M, int64_t rank) {
+  if (M < 1 || M > kMaxLoraM || rank < 8 || rank > QG_LORA_MAX_RANK || rank % 8 != 0) return 0;
+  return (size_t)align_up(M * lora_padded_rank(rank) * 4, 256);
+}
+
+qg_status qg_add_lora(const void* base, qg_dtype dtype, int64_t ldb, const void* x, qg_dtype x_dtype,
+                      int64_t M, int64_t K, int64_t ldx, const uint16_t* a, const uint16_t* b,
+                      int64_t adapters, int64_t rank, int64_t N, const int64_t* ids,
+                      const float* scaling, void* out, int64_t ldo, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  if (!base || !x || !a || !b || !ids || !out) return fail(QG_EINVAL, "null pointer argument");
+  qg_status s = check_dtype(dtype, "dtype");
+  if (s == QG_OK) s = check_dtype(x_dtype, "x_dtype");
+  if (s == QG_OK) s = check_fp8_k(K);
+  if (s != QG_OK) return s;
+  if (M < 1 || M > kMaxLoraM) return fail(QG_EINVAL, "M=%lld out of range [1, 2^20]", (long long)M);
+  if (N < 1 || N > kMaxN) return fail(QG_EINVAL, "N=%lld out of range [1, 2^24]", (long long)N);
+  if (adapters < 1 || adapters > kMaxLoras)
+    return fail(QG_EINVAL, "adapters=%lld out of range [1, 2^20]", (long long)adapters);
+  if (rank < 8 || rank > QG_LORA_MAX_RANK || rank % 8 != 0)
+    return fail(QG_EINVAL, "rank=%lld must be a multiple of 8, at most %d", (long long)rank, QG_LORA_MAX_RANK);
+  s = check_rows16(x, x_dtype, ldx, K, "x");
+  if (s != QG_OK) return s;
+  if (ldb < N) return fail(QG_EINVAL, "ldb=%lld < N=%lld", (long long)ldb, (long long)N);
+  if (ldo < N) return fail(QG_EINVAL, "ldo=%lld < N=%lld", (long long)ldo, (long long)N);
+  const uintptr_t es = dtype == QG_BF16 ? 2 : 4;
+  if (!aligned(base, es) || !aligned(out, es) || !aligned(a, 16) || !aligned(b, 16) || !aligned(ids, 8) ||
+      (scaling && !aligned(scaling, 4)))
+    return fail(QG_EALIGN, "a and b need 16-byte alignment, every other array that of its elements");
+  const size_t need = qg_add_lora_workspace_bytes(M, rank);
+  if (!workspace || workspace_bytes < need)
+    return fail(QG_EINVAL, "workspace of %lld bytes needed for M=%lld (qg_add_lora_workspace_bytes)",
+                (long long)need, (long long)M);
+  if (!aligned(workspace, 256)) return fail(QG_EALIGN, "workspace needs 256-byte alignment");
+  return from_cuda(launch_add_lora(base, dtype == QG_BF16, ldb, x, x_dtype == QG_BF16, M, K, ldx, a, b,
+                                   adapters, rank, N, ids, scaling, out, ldo, workspace,
+                                   reinterpret_cast<cudaStream_t>(stream)),
+                   "adapter launch");
 }
 
 qg_status qg_token_logprobs(const void* logits, qg_dtype dtype, int64_t M, int64_t V, int64_t ldl,

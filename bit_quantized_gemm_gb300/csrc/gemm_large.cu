@@ -759,6 +759,23 @@ bool make_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// `mats` matrices of rows of `cols` values, `pitch` bytes from row to row and
+// `mat_pitch` from matrix to matrix; box = box_cols x box_rows of one matrix
+bool make_tmap_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t cols,
+                  int64_t rows, int64_t mats, int64_t pitch, int64_t mat_pitch, uint32_t box_cols,
+                  uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc || !base || (reinterpret_cast<uintptr_t>(base) & 15) || pitch % 16 || mat_pitch % 16)
+    return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)mats};
+  cuuint64_t strides[2] = {(cuuint64_t)pitch, (cuuint64_t)mat_pitch};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // rows of `row_bytes` bytes (a multiple of 16), read as 8-byte words:
 // box = box_words x box_rows, no swizzle, so the box lands row after row at a
 // pitch of 8 * box_words bytes; words past a row's end read as zero (used by

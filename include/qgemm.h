@@ -335,6 +335,97 @@ qg_status qg_linear_fp8(const void* x, qg_dtype x_dtype, int64_t M, int64_t K, i
                         void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Root-mean-square norm of each row, with the residual's addition, into 8-bit */
+/* activations with their scales: what stands before a projection.            */
+/*   h = x + residual, rounded to x_dtype and written to sum (h = x without a  */
+/*       residual: residual and sum both NULL)                                 */
+/*   y = (h * (1 / sqrt(sum h^2 / K + eps))) * weight   (fp32 throughout)      */
+/* and y is quantized as qg_quantize_act_fp8 (the first call) or               */
+/* qg_quantize_act (the second) quantizes fp32 values; there is no rounding in  */
+/* between. The norm reads h as it is stored: a call on x and a residual gives  */
+/* the bits of a call on their sum. A row's bits do not depend on the other     */
+/* rows of its call. NaN and infinities spread by IEEE rules: a NaN makes a      */
+/* row's scales NaN; an infinity (r is 0 then) makes its block's scale NaN       */
+/* (int8: the row's, with q 0) and the row's products with it.                   */
+/*   x, residual, sum  [M][ld*] of x_dtype, rows of K values, 16-byte aligned,  */
+/*          ld* >= K, ld*elem_size % 16 == 0. sum may be x or residual itself.  */
+/*   weight [K] of weight_dtype, 16-byte aligned. eps >= 0.                     */
+/*   q, scale, lds (fp8), q, scale, block_sums, q16 (int8): as the two calls     */
+/*          named above write them. K as there (a multiple of 16; of 32).        */
+/* ------------------------------------------------------------------------ */
+qg_status qg_rmsnorm_quantize_act_fp8(const void* x, const void* residual, qg_dtype x_dtype,
+                                      int64_t M, int64_t K, int64_t ldx, int64_t ldr,
+                                      const void* weight, qg_dtype weight_dtype, float eps,
+                                      void* sum, int64_t ldsum, uint8_t* q, float* scale,
+                                      int64_t lds, void* stream);
+qg_status qg_rmsnorm_quantize_act(const void* x, const void* residual, qg_dtype x_dtype, int64_t M,
+                                  int64_t K, int64_t ldx, int64_t ldr, const void* weight,
+                                  qg_dtype weight_dtype, float eps, void* sum, int64_t ldsum,
+                                  int8_t* q, float* scale, int32_t* block_sums, uint16_t* q16,
+                                  void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* silu(gate) * up into e4m3 activations: what stands between the two          */
+/* projections of an MLP. Row m of x holds K gates, then K values up:          */
+/*   y = g / (1 + e^-g) * u  (fp32, off by less than (8 + |g|) 2^-23 of itself;  */
+/*       e^-|g| below 2^-126 counts as 0), quantized as qg_quantize_act_fp8.     */
+/*   x [M][ldx] of x_dtype, rows of 2K values, 16-byte aligned, ldx >= 2K,      */
+/*     ldx*elem_size % 16 == 0; q, scale, lds, K as for qg_quantize_act_fp8.     */
+/* ------------------------------------------------------------------------ */
+qg_status qg_silu_mul_quantize_act_fp8(const void* x, qg_dtype x_dtype, int64_t M, int64_t K,
+                                       int64_t ldx, uint8_t* q, float* scale, int64_t lds,
+                                       void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* qg_gemm_fp8 with the weights of each row's expert. The rows are sorted by    */
+/* expert: expert e owns rows offsets[e] <= m < offsets[e+1]; other rows of out */
+/* are left as they were. A row's bits are those of qg_gemm_fp8 with its        */
+/* expert's weights.                                                            */
+/*   offsets  [experts+1] int64 on the device, ascending. Values outside 0..M   */
+/*            are taken as 0 or M, an expert that ends before it begins has no   */
+/*            rows; where two experts claim a row, either's result may stand.    */
+/*   w        [experts] matrices [N][ldw] of e4m3, lde bytes from one to the     */
+/*            next (a multiple of 16, no overlap).                               */
+/*   w_scale  [experts][ceil(N/128)][ceil(K/128)] fp32, 4-byte aligned.          */
+/*   1 <= experts <= 1024; all else as for qg_gemm_fp8.                          */
+/* ------------------------------------------------------------------------ */
+qg_status qg_gemm_fp8_grouped(const uint8_t* q, const float* scale, int64_t lds, int64_t M, int64_t K,
+                              const int64_t* offsets, int64_t experts, const uint8_t* w, int64_t ldw,
+                              int64_t lde, const float* w_scale, int64_t N, void* out,
+                              qg_dtype out_dtype, int64_t ldo, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Low-rank adapters of many requests beside a shared projection:               */
+/*   h[m][r]   = sum_k x[m][k] * a[id][r][k]                     id = ids[m]     */
+/*   out[m][n] = base[m][n] + sum_r (scaling[id] * h[m][r]) * b[id][n][r]        */
+/* in fp32 (scaling * h as the sum of two bf16 numbers, off by 2^-17 of itself;  */
+/* fp32 x as the sum of three), rounded once to dtype. A row whose id is outside */
+/* 0..adapters-1 keeps base's bits. Rows may come in any order; rows of one       */
+/* adapter that follow one another cost least. A row's bits do not depend on the  */
+/* other rows of its call.                                                        */
+/*   base, out  [M][ldb], [M][ldo] of dtype, rows of N values, aligned to their   */
+/*            elements (fastest where rows start on 16 bytes). out may be base     */
+/*            itself (with ldo = ldb); it overlaps nothing else of the call.       */
+/*   x        [M][ldx] of x_dtype, rows of K values, 16-byte aligned, ldx >= K,    */
+/*            ldx*elem_size % 16 == 0.                                              */
+/*   a, b     bf16 [adapters][rank][K], [adapters][N][rank], 16-byte aligned;      */
+/*            adapters of a smaller rank are filled up with zeros.                  */
+/*   ids      [M] int64; scaling [adapters] fp32, or NULL for 1.                    */
+/*   workspace  qg_add_lora_workspace_bytes(M, rank) bytes (0: invalid sizes),      */
+/*            256-byte aligned, owned by the caller; calls that may run at once      */
+/*            need one each.                                                         */
+/* K % 16 == 0, K <= 65536; rank % 8 == 0, 8 <= rank <= QG_LORA_MAX_RANK;            */
+/* 1 <= M <= 2^20, 1 <= N <= 2^24, 1 <= adapters <= 2^20.                            */
+/* ------------------------------------------------------------------------ */
+#define QG_LORA_MAX_RANK 128
+size_t qg_add_lora_workspace_bytes(int64_t M, int64_t rank);
+qg_status qg_add_lora(const void* base, qg_dtype dtype, int64_t ldb, const void* x, qg_dtype x_dtype,
+                      int64_t M, int64_t K, int64_t ldx, const uint16_t* a, const uint16_t* b,
+                      int64_t adapters, int64_t rank, int64_t N, const int64_t* ids,
+                      const float* scaling, void* out, int64_t ldo, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Log probabilities of given tokens, entropy and top alternatives, from the  */
 /* logits that an output head writes. Row by row, with m = max x,             */
 /* S = sum e^(x-m), T = sum e^(x-m) (x-m):                                    */

@@ -1,0 +1,141 @@
+"""GPU tests of the low-rank adapters against 64 bits.
+
+Bound. h: a warp's share of K goes through 2 * ceil(ceil(K/32) / 64) MMAs (three times
+that for fp32 x), each adding 16 exact products to its sum, every addition off by at
+most one unit, 2^-23 of the sum of |terms|; then 16 sums in fp32. scaling * h: 2^-24, and
+2^-17 for its two bf16 parts. The second product likewise: 2 * ceil(rank / 16) MMAs of
+16. The sum with base rounds once to fp32 and once to the output: half a step,
+2^-8 (bf16) or 2^-24.
+"""
+import pytest
+import torch
+
+import bit_quantized_gemm_gb300 as qg
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from bit_quantized_gemm_gb300 import build
+    build.build()
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    yield
+    qg.check_device_error()
+
+
+def inputs(seed, m, k, n, rank, count, x=BF16, out=BF16, pad=0):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    xs = torch.randn(m, k + pad, generator=g, device=DEV).to(x)[:, :k]
+    base = torch.randn(m, n + pad, generator=g, device=DEV).to(out)[:, :n]
+    a = (torch.randn(count, rank, k, generator=g, device=DEV) / k ** 0.5).to(BF16)
+    b = torch.randn(count, n, rank, generator=g, device=DEV).to(BF16)
+    scaling = 0.25 + torch.rand(count, generator=g, device=DEV)
+    ids = torch.randint(-1, count, (m,), generator=g, device=DEV)
+    return base, xs, a, b, ids, scaling
+
+
+def check(got, base, x, a, b, ids, scaling):
+    k, rank, count = x.shape[1], a.shape[1], a.shape[0]
+    mmas = 2 * -(-(-(-k // 32)) // 64) * (1 if x.dtype == BF16 else 3)
+    c1, c2 = 16 * mmas + 16, 2 * 16 * -(-rank // 16)
+    half = 2.0 ** -8 if got.dtype == BF16 else 2.0 ** -24
+    assert got.shape == base.shape and got.dtype == base.dtype
+    for i in range(-1, count):
+        rows = (ids == i).nonzero()[:, 0]
+        if not len(rows):
+            continue
+        if i < 0:
+            assert torch.equal(got[rows], base[rows])
+            continue
+        f = 1.0 if scaling is None else float(scaling[i])
+        xd, ad, bd = x[rows].double(), a[i].double(), b[i].double()
+        h, hm = xd @ ad.t(), xd.abs() @ ad.abs().t()
+        y = base[rows].double() + f * (h @ bd.t())
+        bound = f * ((c1 * 2.0 ** -23 * hm + 2.0 ** -16.9 * h.abs()) @ bd.abs().t())
+        bound += c2 * 2.0 ** -23 * f * (h.abs() @ bd.abs().t())
+        bound += (half + 2.0 ** -24) * (y.abs() + bound)
+        assert bool(((got[rows].double() - y).abs() <= bound).all())
+
+
+CASES = [
+    (1, 16, 1, 8, 1), (1, 17408, 5120, 16, 3), (5, 272, 100, 16, 2), (16, 2560, 333, 8, 20), (31, 528, 256, 24, 4),
+    (64, 5120, 1000, 16, 64), (33, 1040, 257, 32, 5), (100, 640, 129, 64, 3), (65, 2064, 520, 128, 9),
+    (300, 256, 72, 40, 7), (700, 1280, 2000, 64, 2), (40, 65536, 64, 16, 3),
+]
+
+
+@pytest.mark.parametrize("m,k,n,rank,count", CASES)
+@pytest.mark.parametrize("x,out", [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)])
+def test_adapters(m, k, n, rank, count, x, out):
+    base, xs, a, b, ids, scaling = inputs(m + k + n, m, k, n, rank, count, x, out)
+    check(qg.add_lora(base, xs, a, b, ids, scaling), base, xs, a, b, ids, scaling)
+    # runs of rows, and no scaling
+    ids = ids.sort().values
+    check(qg.add_lora(base, xs, a, b, ids), base, xs, a, b, ids, None)
+
+
+@pytest.mark.parametrize("n", [64, 77, 200])
+def test_strides_and_in_place(n):
+    base, xs, a, b, ids, scaling = inputs(n, 90, 512, n, 16, 4, pad=16)
+    want = qg.add_lora(base, xs, a, b, ids, scaling)
+    check(want, base, xs, a, b, ids, scaling)
+    room = torch.full((90, n + 24), 7.0, device=DEV, dtype=BF16)
+    got = qg.add_lora(base, xs, a, b, ids, scaling, out=room[:, :n])
+    assert torch.equal(got, want) and bool((room[:, n:] == 7.0).all())
+    room[:, :n] = base
+    got = qg.add_lora(room[:, :n], xs, a, b, ids, scaling, out=room[:, :n])
+    assert torch.equal(got, want) and bool((room[:, n:] == 7.0).all())
+    # rows that start off 16-byte boundaries
+    odd = torch.full((90, n + 25), 7.0, device=DEV, dtype=BF16)
+    got = qg.add_lora(base, xs, a, b, ids, scaling, out=odd[:, 3:3 + n])
+    assert torch.equal(got, want) and bool((odd[:, :3] == 7.0).all()) and bool((odd[:, 3 + n:] == 7.0).all())
+
+
+@pytest.mark.parametrize("x", [BF16, F32])
+def test_bits_of_a_row_do_not_depend_on_the_others(x):
+    base, xs, a, b, ids, scaling = inputs(1, 500, 1296, 300, 24, 6, x)
+    want = qg.add_lora(base, xs, a, b, ids, scaling)
+    for rows in (slice(7, 8), slice(30, 70), slice(3, 499)):
+        got = qg.add_lora(base[rows], xs[rows], a, b, ids[rows].contiguous(), scaling)
+        assert torch.equal(got, want[rows])
+    turn = torch.randperm(500, device=DEV)
+    got = qg.add_lora(base[turn], xs[turn], a, b, ids[turn], scaling)
+    assert torch.equal(got, want[turn])
+
+
+def test_rows_without_an_adapter_keep_their_bits():
+    base, xs, a, b, ids, scaling = inputs(4, 50, 256, 96, 8, 3)
+    base.view(torch.int16)[:, 5] = 0x7FA3      # a NaN with a payload
+    base.view(torch.int16)[:, 6] = -32768      # -0
+    ids[:] = torch.tensor([-1, 3, 2 ** 40, -2 ** 40, 99] * 10, device=DEV)
+    got = qg.add_lora(base, xs, a, b, ids, scaling)
+    assert torch.equal(got.view(torch.int16), base.view(torch.int16))
+
+
+def test_non_finite_values_stay_to_their_rows_and_adapters():
+    base, xs, a, b, ids, scaling = inputs(5, 64, 256, 96, 8, 4, F32, F32)
+    ids = torch.arange(64, device=DEV) % 5 - 1
+    want = qg.add_lora(base, xs, a, b, ids, scaling)
+    a[2, 3, 100], b[3, 40, 2] = float("nan"), float("inf")
+    xs[6, 9] = float("inf")             # row 6 has adapter 0
+    got = qg.add_lora(base, xs, a, b, ids, scaling)
+    fine = (ids != 2) & (ids != 3)
+    fine[6] = False
+    assert torch.equal(got[fine], want[fine])
+    assert bool(got[ids == 2].isnan().all())
+    assert torch.equal(got[ids == 3][:, :40], want[ids == 3][:, :40])
+    assert not bool(got[ids == 3][:, 40].isfinite().any()) and not bool(got[6].isfinite().any())
+    # (an infinite h alone: h * b is infinite, not NaN)
+    xs[6] = 0
+    a[0] = 0
+    a[0, 1, 0], xs[6, 0] = 1.0, float("inf")
+    b[0, :, 1] = 1.0
+    xs[6, 1:] = 0
+    got = qg.add_lora(base, xs, a, b, ids, scaling)
+    assert got[6].isnan().all() or got[6].isinf().all()
