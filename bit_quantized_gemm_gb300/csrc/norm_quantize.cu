@@ -7,17 +7,17 @@
 //          norm of what the next layer finds in memory.
 //   r    = 1 / sqrt(sum h^2 / K + eps)    (fp32: IEEE quotients and root)
 //   y[k] = (h[k] * r) * weight[k]         (fp32, not rounded to the input's type)
-// and y is quantized as qg_quantize_act_fp8 or qg_quantize_act would.
+// and y is quantized: e4m3 per 128 values with s = max|y| * fl(1/448), or int8
+// per row with s = max|y| / 127, by products with fl(1/s).
 // Gate, row m of 2K values: y[k] = g / (1 + e^-g) * u, g = x[k], u = x[K + k].
 //
-// The sum of squares: a lane's 16 values in order, the 32 lanes of a unit (512
-// values) as a butterfly, a row's units by their number -- whichever warps hold
-// them. So a row's bits depend neither on its batch nor on the launch.
+// The sum of squares: a lane's 16 values in two chains, the 32 lanes of a unit
+// (512 values) as a butterfly, a row's units by their number -- whichever warps
+// hold them. So a row's bits depend neither on its batch nor on the launch.
 //
 // HBM-bound: 2 + 2 bytes read and 2 + 1 written a value (bf16, residual). Every
-// value is read once and held in registers over the row's barrier; a CTA takes
-// rows in turn and has the next row's loads in flight while it works on one, so
-// the barrier costs no bandwidth. The weight lies in registers for all rows.
+// value is read once and held in registers over the row's barrier; several rows'
+// CTAs on an SM fill one another's waits.
 #include "quantize_fp8.cuh"
 
 namespace qg {
@@ -32,250 +32,248 @@ struct NormArgs {
   int32_t* bsum;       // int8: or null
   float* scale;        // e4m3: [ceil(K/128)][lds]; int8: [M]
   int64_t ldx, ldr, ldsum, lds, M;
-  int K, weight_bf16;
+  int K;
   float eps;
 };
 
-// the 16 values of x + res, rounded to their type, in place of x
-template <bool kBf16>
-__device__ __forceinline__ void add_rounded(Raw16<kBf16>& x, const Raw16<kBf16>& r) {
+// the 16 values of x + r, each rounded once to their type, in place of x
+__device__ __forceinline__ void add_rounded(Raw16<true>& x, const Raw16<true>& r) {
+  auto add = [](uint32_t& a, uint32_t b) { asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b)); };
 #pragma unroll
-  for (int i = 0; i < Raw16<kBf16>::kWords; ++i) {
-    constexpr int kPer = 16 / Raw16<kBf16>::kWords;
-    uint32_t w[4];
+  for (int i = 0; i < 2; ++i) {
+    add(x.w[i].x, r.w[i].x);
+    add(x.w[i].y, r.w[i].y);
+    add(x.w[i].z, r.w[i].z);
+    add(x.w[i].w, r.w[i].w);
+  }
+}
+__device__ __forceinline__ void add_rounded(Raw16<false>& x, const Raw16<false>& r) {
+  auto add = [](uint32_t& a, uint32_t b) { a = __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); };
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (kBf16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x.at(i * kPer + 2 * j) + r.at(i * kPer + 2 * j),
-                                                       x.at(i * kPer + 2 * j + 1) + r.at(i * kPer + 2 * j + 1));
-        w[j] = *reinterpret_cast<const uint32_t*>(&h);
-      } else {
-        w[j] = __float_as_uint(x.at(i * 4 + j) + r.at(i * 4 + j));
-      }
-    }
-    x.w[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < 4; ++i) {
+    add(x.w[i].x, r.w[i].x);
+    add(x.w[i].y, r.w[i].y);
+    add(x.w[i].z, r.w[i].z);
+    add(x.w[i].w, r.w[i].w);
   }
 }
 
-// a lane's 16 values quantized to int8 with the row's scale s (as
-// qg_quantize_act does): bytes, fp16 copy, sums of 32 (a pair of lanes)
-template <class At>
-__device__ __forceinline__ void emit_int8(const NormArgs& a, const At& at, int64_t m, int k, bool valid, float s,
-                                          float inv) {
-  float f[16];
+// 1 / sqrt(v): the hardware's, and one step of Newton's iteration (v = 0 and
+// infinity have none: it would make a NaN of them)
+__device__ __forceinline__ float rsqrt_refined(float v) {
+  float r;
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  const float e = fmaf(-v * r, r, 1.0f);
+  return v > 0.0f && v < 3.0e38f ? fmaf(0.5f * r, e, r) : r;
+}
+
+// a lane's 16 values quantized to int8 with the row's scale s: bytes, fp16 copy,
+// sums of 32 (a pair of lanes). |y * fl(1/s)| rounds to at most 127, so nothing
+// is clamped. s = 0, NaN or infinite: q is 0.
+__device__ __forceinline__ void emit_int8(const NormArgs& a, const float2 (&y)[8], int64_t m, int k, bool valid,
+                                          float s, float inv) {
+  float2 f[8];  // whole numbers + 1.5 * 2^23: the low byte is the int8 value
+  const float magic = 12582912.0f;
+  if (inv != 0.0f) {
+    const float2 i2 = make_float2(inv, inv), m2 = make_float2(magic, magic);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    // (a NaN scale: 0, the products are NaN by the scale)
-    const float v = s > 0.0f ? qround(at(i), s, inv) : 0.0f;
-    f[i] = fminf(127.0f, fmaxf(-127.0f, v));
+    for (int i = 0; i < 8; ++i) f[i] = __ffma2_rn(y[i], i2, m2);
+  } else {
+    // s is subnormal (its reciprocal is not exact enough), or there is nothing to divide by
+    const bool divide = s > 0.0f && s < 3.4e38f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      f[i] = divide ? make_float2(__fdiv_rn(y[i].x, s) + magic, __fdiv_rn(y[i].y, s) + magic)
+                    : make_float2(magic, magic);
   }
-  if (valid && a.q) {
+  if (a.q || a.bsum) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint32_t b[4], lo, hi;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = (uint32_t)__float2int_rz(f[4 * i + j]);
-      asm("prmt.b32 %0, %1, %2, 0x0040;" : "=r"(lo) : "r"(b[0]), "r"(b[1]));
-      asm("prmt.b32 %0, %1, %2, 0x0040;" : "=r"(hi) : "r"(b[2]), "r"(b[3]));
+      uint32_t lo, hi;
+      asm("prmt.b32 %0, %1, %2, 0x0040;" : "=r"(lo) : "r"(__float_as_uint(f[2 * i].x)), "r"(__float_as_uint(f[2 * i].y)));
+      asm("prmt.b32 %0, %1, %2, 0x0040;"
+          : "=r"(hi)
+          : "r"(__float_as_uint(f[2 * i + 1].x)), "r"(__float_as_uint(f[2 * i + 1].y)));
       asm("prmt.b32 %0, %1, %2, 0x5410;" : "=r"(w[i]) : "r"(lo), "r"(hi));
     }
-    *reinterpret_cast<uint4*>(a.q + m * (int64_t)a.K + k) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (valid && a.q) *reinterpret_cast<uint4*>(a.q + m * (int64_t)a.K + k) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (a.bsum) {  // (the same for every lane)
+      int part = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part = __dp4a((int)w[i], 0x01010101, part);
+      part += __shfl_xor_sync(0xffffffffu, part, 1);
+      if (valid && (threadIdx.x & 1) == 0) a.bsum[m * (int64_t)(a.K / kBlk) + k / kBlk] = part;
+    }
   }
   if (valid && a.q16) {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);  // exact
+      const __half2 h = __floats2half2_rn(f[i].x - magic, f[i].y - magic);  // exact
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     uint4* p = reinterpret_cast<uint4*>(a.q16 + m * (int64_t)a.K + k);
     p[0] = make_uint4(w[0], w[1], w[2], w[3]);
     p[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
-  if (a.bsum) {  // (the same for every lane)
-    float part = 0.0f;  // exact: |sum| <= 32 * 127
-#pragma unroll
-    for (int i = 0; i < 16; ++i) part += f[i];
-    part += __shfl_xor_sync(0xffffffffu, part, 1);
-    if (valid && (threadIdx.x & 1) == 0) a.bsum[m * (int64_t)(a.K / kBlk) + k / kBlk] = (int32_t)part;
-  }
 }
 
 constexpr int kNormMaxWarps = 32, kNormMaxUnits = kMaxK / 512;
 
-// One row at a time by the W = blockDim.y warps of a group; blockDim.z groups a
-// CTA, each with rows of its own, in step. A warp holds kU units of 512 values.
-template <bool kBf16, bool kFp8, int kU>
-__global__ void __launch_bounds__(kU == 4 ? 1024 : kU == 2 ? 544 : 512)
-    norm_quantize_kernel(const NormArgs a) {
+// Registers decide how many rows an SM works on at once: 8192 x 5120 bf16 with a
+// residual 48.2 us with 40 (five CTAs), 51.4 with 52 (three); without one 31.0 and
+// 36.8. Rows in two units a warp, 8192 x 17408 bf16 without a residual: 132 us with 56 (two CTAs),
+// 145 with 77 (one).
+template <bool kBf16, bool kWBf16, int kU>
+constexpr int kNormRegs = kU == 4 ? 64 : kU == 2 ? (kBf16 ? 56 : 96) : kBf16 ? 40 : kWBf16 ? 48 : 56;
+
+// A row by the W = blockDim.y warps of a group (threadIdx.z: the groups of a CTA
+// have a row each). A warp holds kU units of 512 values.
+template <bool kBf16, bool kWBf16, bool kFp8, int kU>
+__global__ void __maxnreg__((kNormRegs<kBf16, kWBf16, kU>)) norm_quantize_kernel(const NormArgs a) {
   griddep_launch_dependents();
-  // [row parity][group][unit], then the int8 maxima likewise by warp
-  __shared__ float part[2][kNormMaxUnits], top[2][kNormMaxWarps];
+  // sums by group and unit (at most kNormMaxUnits), int8 maxima by group and warp
+  __shared__ float part[kNormMaxUnits], top[kNormMaxWarps];
   const int lane = threadIdx.x, warp = threadIdx.y, W = blockDim.y, group = threadIdx.z;
   const int K = a.K, units = (K + 511) >> 9;
-  const int64_t step = (int64_t)gridDim.x * blockDim.z;
-  float* const row_part = part[0] + group * units;  // (units x groups is at most kNormMaxUnits)
-  float* const row_top = top[0] + group * W;
-  constexpr bool kAhead = kU <= 2;  // the next row's loads during this one's work; the weight in registers
-  constexpr int kHeld = kAhead ? kU : 1;
-
-  auto where = [&](int u) { return ((u * W + warp) << 9) + lane * 16; };  // k of this lane in its unit u
-  auto load_weight = [&](int k, float (&w)[16]) {
-    if (a.weight_bf16) {
-      Raw16<true> r;
-      const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.weight) + k);
-      r.w[0] = __ldg(p);
-      r.w[1] = __ldg(p + 1);
+  const int64_t m = (int64_t)blockIdx.x * blockDim.z + group;
+  const bool row = m < a.M;
+  auto at = [&](int u) { return ((u * W + warp) << 9) + lane * 16; };  // k of this lane in its unit u
+  Raw16<kBf16> h[kU];
+  constexpr bool kHeld = kU <= 2;  // the weight, too, before the barrier
+  Raw16<kWBf16> w[kHeld ? kU : 1];
+  auto load_weight = [&](int u) {
+    if (at(u) >= K) return;
+    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(a.weight) +
+                                                    (size_t)at(u) * (kWBf16 ? 2 : 4));
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = r.at(i);
-    } else {
-      const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.weight) + k);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 v = __ldg(p + i);
-        w[4 * i] = v.x;
-        w[4 * i + 1] = v.y;
-        w[4 * i + 2] = v.z;
-        w[4 * i + 3] = v.w;
-      }
-    }
+    for (int i = 0; i < Raw16<kWBf16>::kWords; ++i) w[kHeld ? u : 0].w[i] = __ldg(p + i);
   };
-  float w[kHeld][16];
-  if (kAhead) {
-#pragma unroll
-    for (int u = 0; u < kHeld; ++u)
-      if (where(u) < K) load_weight(where(u), w[u]);
-  }
-  Raw16<kBf16> v[kU], r[kU];
-  auto load = [&](int64_t m) {
+  {
+    Raw16<kBf16> r[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int k = where(u);
-      v[u].zero();
-      if (m < a.M && k < K) {
-        v[u].load(reinterpret_cast<const char*>(a.x) + m * a.ldx * (kBf16 ? 2 : 4), k);
+      const int k = at(u);
+      h[u].zero();
+      if (row && k < K) {
+        h[u].load(reinterpret_cast<const char*>(a.x) + m * a.ldx * (kBf16 ? 2 : 4), k);
         if (a.res) r[u].load(reinterpret_cast<const char*>(a.res) + m * a.ldr * (kBf16 ? 2 : 4), k);
       }
     }
-  };
-  int64_t m = (int64_t)blockIdx.x * blockDim.z + group;
-  load(m);
-  // (the groups of a CTA pass the barriers together: trips by the first group's row)
-  for (int odd = 0; m - group < a.M; m += step, odd ^= 1) {
-    const bool row = m < a.M;
-    Raw16<kBf16> h[kU];
+    if (kHeld) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int k = where(u);
-      h[u] = v[u];
-      if (a.res && row && k < K) {
-        add_rounded(h[u], r[u]);
-        uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<char*>(a.sum) + (m * a.ldsum + k) * (kBf16 ? 2 : 4));
-#pragma unroll
-        for (int i = 0; i < Raw16<kBf16>::kWords; ++i) p[i] = h[u].w[i];
-      }
+      for (int u = 0; u < kU; ++u) load_weight(u);
     }
-    if (kAhead) load(m + step);
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int unit = u * W + warp;
-      float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s = fmaf(h[u].at(i), h[u].at(i), s);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (lane == 0 && unit < units) row_part[odd * kNormMaxUnits + unit] = s;
-    }
-    __syncthreads();
-    float sum = 0.0f;
-    for (int u = lane; u < units; u += 32) sum += row_part[odd * kNormMaxUnits + u];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float rms = __frcp_rn(__fsqrt_rn(__fdiv_rn(sum, (float)K) + a.eps));
-
-    auto normed = [&](int u, float (&y)[16]) {
-      if (!kAhead && where(u) < K) load_weight(where(u), w[0]);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = (h[u].at(i) * rms) * w[kAhead ? u : 0][i];
-    };
-    if (kFp8) {
+    if (a.res) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const int k = where(u);
-        float y[16], amax = 0.0f;
-        normed(u, y);
-        if (k < K) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(y[i]));
-        }
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int k = at(u);
         if (row && k < K) {
-          const float s = amax * (1.0f / 448.0f);
-          if ((lane & 7) == 0) a.scale[(int64_t)(k >> 7) * a.lds + m] = s;
-          *reinterpret_cast<uint4*>(a.q + m * (int64_t)K + k) = e4m3x16([&](int i) { return y[i]; }, s);
+          add_rounded(h[u], r[u]);
+          uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<char*>(a.sum) + (m * a.ldsum + k) * (kBf16 ? 2 : 4));
+#pragma unroll
+          for (int i = 0; i < Raw16<kBf16>::kWords; ++i) p[i] = h[u].w[i];
         }
-      }
-    } else {
-      float amax = 0.0f;
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        float y[16];
-        normed(u, y);
-        if (where(u) < K) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(y[i]));
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      if (lane == 0) row_top[odd * kNormMaxWarps + warp] = amax;
-      __syncthreads();
-      amax = lane < W ? row_top[odd * kNormMaxWarps + lane] : 0.0f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const float s = act_scale(amax), inv = act_scale_rcp(s);
-      if (row && warp == 0 && lane == 0) a.scale[m] = s;
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        float y[16];
-        normed(u, y);
-        emit_int8(a, [&](int i) { return y[i]; }, m, where(u), row && where(u) < K, s, inv);
       }
     }
-    if (!kAhead) load(m + step);
+  }
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    const int unit = u * W + warp;
+    float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s2 = __ffma2_rn(h[u].two(i), h[u].two(i), s2);
+    float s = s2.x + s2.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0 && unit < units) part[group * units + unit] = s;
+  }
+  __syncthreads();
+  float sum = lane < units ? part[group * units + lane] : 0.0f;
+  if (units > 32)
+    for (int u = lane + 32; u < units; u += 32) sum += part[u];  // (one group)
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float rms = rsqrt_refined(__fdividef(sum, (float)K) + a.eps);
+  const float2 rms2 = make_float2(rms, rms);
+
+  auto normed = [&](int u, float2 (&y)[8]) {
+    if (!kHeld) load_weight(u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __fmul2_rn(__fmul2_rn(h[u].two(i), rms2), w[kHeld ? u : 0].two(i));
+  };
+  if (kFp8) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int k = at(u);
+      float2 y[8];
+      normed(u, y);
+      float amax = k < K ? absmax16(y) : 0.0f;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      if (row && k < K) {
+        const float s = amax * (1.0f / 448.0f);
+        if ((lane & 7) == 0) a.scale[(int64_t)(k >> 7) * a.lds + m] = s;
+        *reinterpret_cast<uint4*>(a.q + m * (int64_t)K + k) = e4m3x16_by_product(y, s);
+      }
+    }
+  } else {
+    float amax = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      float2 y[8];
+      normed(u, y);
+      if (at(u) < K) amax = max_nan(amax, absmax16(y));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (lane == 0) top[group * W + warp] = amax;
+    __syncthreads();
+    amax = lane < W ? top[group * W + lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float s = act_scale(amax), inv = act_scale_rcp(s);
+    if (row && warp == 0 && lane == 0) a.scale[m] = s;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      float2 y[8];
+      normed(u, y);
+      emit_int8(a, y, m, at(u), row && at(u) < K, s, inv);
+    }
   }
 }
 
-template <bool kBf16, bool kFp8, int kU>
+template <bool kBf16, bool kWBf16, bool kFp8, int kU>
 static cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
-  const int units = (int)ceil_div(a.K, 512), W = (int)ceil_div(units, kU);
-  // short rows: several to a CTA, 256 threads in all
-  const int groups = W >= 8 ? 1 : 8 / W;
-  auto kern = norm_quantize_kernel<kBf16, kFp8, kU>;
-  int per_sm = 0;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 32 * W * groups, 0);
-  if (e != cudaSuccess) return e;
-  const int64_t ctas = ceil_div(a.M, groups), most = (int64_t)num_sms() * (per_sm > 0 ? per_sm : 1);
-  kern<<<(unsigned)(ctas < most ? ctas : most), dim3(32, W, groups), 0, st>>>(a);
+  const int W = (int)ceil_div(ceil_div(a.K, 512), kU);
+  const int groups = W >= 8 ? 1 : 8 / W;  // short rows: several to a CTA, 256 threads in all
+  norm_quantize_kernel<kBf16, kWBf16, kFp8, kU>
+      <<<(unsigned)ceil_div(a.M, groups), dim3(32, W, groups), 0, st>>>(a);
   return cudaGetLastError();
 }
 
+template <bool kBf16, bool kWBf16, bool kFp8>
+static cudaError_t launch_norm_k(const NormArgs& a, cudaStream_t st) {
+  // one unit a warp up to 20 warps (4096 x 9728 bf16: 48.1 us, 58.6 in two units),
+  // two up to 17 (4096 x 14336 int8: 91 us, 104 in one)
+  if (a.K <= 512 * 20) return launch_norm<kBf16, kWBf16, kFp8, 1>(a, st);
+  if (a.K <= 512 * 2 * 17) return launch_norm<kBf16, kWBf16, kFp8, 2>(a, st);
+  return launch_norm<kBf16, kWBf16, kFp8, 4>(a, st);
+}
+
 template <bool kBf16, bool kFp8>
-static cudaError_t launch_norm_any(const NormArgs& a, cudaStream_t st) {
-  if (a.K <= 512 * 16) return launch_norm<kBf16, kFp8, 1>(a, st);
-  if (a.K <= 512 * 2 * 17) return launch_norm<kBf16, kFp8, 2>(a, st);
-  return launch_norm<kBf16, kFp8, 4>(a, st);
+static cudaError_t launch_norm_w(const NormArgs& a, bool weight_bf16, cudaStream_t st) {
+  return weight_bf16 ? launch_norm_k<kBf16, true, kFp8>(a, st) : launch_norm_k<kBf16, false, kFp8>(a, st);
 }
 
 cudaError_t launch_norm_quantize(const void* x, const void* res, bool bf16, int64_t M, int64_t K, int64_t ldx,
                                  int64_t ldr, const void* weight, bool weight_bf16, float eps, void* sum,
                                  int64_t ldsum, bool fp8, uint8_t* q, uint16_t* q16, int32_t* bsum, float* scale,
                                  int64_t lds, cudaStream_t st) {
-  const NormArgs a{x, res, weight, sum, q, q16, bsum, scale, ldx, ldr, ldsum, lds, M, (int)K, weight_bf16, eps};
-  if (fp8) return bf16 ? launch_norm_any<true, true>(a, st) : launch_norm_any<false, true>(a, st);
-  return bf16 ? launch_norm_any<true, false>(a, st) : launch_norm_any<false, false>(a, st);
+  const NormArgs a{x, res, weight, sum, q, q16, bsum, scale, ldx, ldr, ldsum, lds, M, (int)K, eps};
+  if (fp8) return bf16 ? launch_norm_w<true, true>(a, weight_bf16, st) : launch_norm_w<false, true>(a, weight_bf16, st);
+  return bf16 ? launch_norm_w<true, false>(a, weight_bf16, st) : launch_norm_w<false, false>(a, weight_bf16, st);
 }
 
 // ------------------------------------------------------------------------ gate
@@ -309,18 +307,17 @@ __global__ void __launch_bounds__(128) silu_mul_quantize_kernel(const void* __re
     g.load(row, k);
     u.load(row, (int64_t)K + k);
   }
-  float y[16], amax = 0.0f;
+  float2 y[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    y[i] = silu_mul(g.at(i), u.at(i));
-    amax = max_nan(amax, fabsf(y[i]));
-  }
+  for (int i = 0; i < 8; ++i)
+    y[i] = make_float2(silu_mul(g.at(2 * i), u.at(2 * i)), silu_mul(g.at(2 * i + 1), u.at(2 * i + 1)));
+  float amax = absmax16(y);
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if (k < K) {
     const float s = amax * (1.0f / 448.0f);
     if ((lane & 7) == 0) scale[(int64_t)(k >> 7) * lds + m] = s;
-    *reinterpret_cast<uint4*>(q + m * (int64_t)K + k) = e4m3x16([&](int i) { return y[i]; }, s);
+    *reinterpret_cast<uint4*>(q + m * (int64_t)K + k) = e4m3x16_by_product(y, s);
   }
 }
 

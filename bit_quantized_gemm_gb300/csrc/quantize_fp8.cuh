@@ -37,6 +37,7 @@ struct Raw16 {
     }
     return __uint_as_float(j == 0 ? q.x : j == 1 ? q.y : j == 2 ? q.z : q.w);
   }
+  __device__ __forceinline__ float2 two(int i) const { return make_float2(at(2 * i), at(2 * i + 1)); }
   __device__ __forceinline__ float absmax() const {  // NaN if there is one
     if (kBf16) {  // without their signs, the bits are in the order of the values
       uint32_t m = 0;
@@ -84,7 +85,7 @@ static __device__ __noinline__ uint32_t divide_e4m3x4(float a, float b, float c,
   return e4m3x4(__fdiv_rn(a, s), __fdiv_rn(b, s), __fdiv_rn(c, s), __fdiv_rn(d, s));
 }
 
-// A lane's 16 values by the scale s of their block: 16 bytes of e4m3. `at` gives value i.
+// A lane's 16 values divided by the scale s of their block: 16 bytes of e4m3. `at` gives value i.
 template <class At>
 __device__ __forceinline__ uint4 e4m3x16(const At& at, float s) {
   uint32_t o[4];
@@ -101,6 +102,35 @@ __device__ __forceinline__ uint4 e4m3x16(const At& at, float s) {
     for (int j = 0; j < 4; ++j) o[j] = divide_e4m3x4(at(4 * j), at(4 * j + 1), at(4 * j + 2), at(4 * j + 3), s);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// The same of values that come out of fp32 arithmetic themselves, as products
+// with fl(1/s) (an IEEE quotient would differ beside ties of e4m3 alone, by less
+// than what the values are off; a third of the instructions).
+__device__ __forceinline__ uint4 e4m3x16_by_product(const float2 (&y)[8], float s) {
+  const float inv = act_scale_rcp(s);
+  uint32_t o[4];
+  if (inv != 0.0f) {
+    const float2 f = make_float2(inv, inv);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 a = __fmul2_rn(y[2 * j], f), b = __fmul2_rn(y[2 * j + 1], f);
+      o[j] = e4m3x4(a.x, a.y, b.x, b.y);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = divide_e4m3x4(y[2 * j].x, y[2 * j].y, y[2 * j + 1].x, y[2 * j + 1].y, s);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// max |y| of 16 values; NaN if there is one
+__device__ __forceinline__ float absmax16(const float2 (&y)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(y[i].x), "f"(y[i].y));
+  return m;
 }
 
 }  // namespace qg
