@@ -80,7 +80,7 @@ def load():
         "qg_rmsnorm_quantize_act": ([P, P, I, I64, I64, I64, I64, P, I, F, P, I64, P, P, P, P, P], I),
         "qg_silu_mul_quantize_act_fp8": ([P, I, I64, I64, I64, P, P, I64, P], I),
         "qg_gemm_fp8_grouped": ([P, P, I64, I64, I64, P, I64, P, I64, I64, P, I64, P, I, I64, P], I),
-        "qg_add_lora_workspace_bytes": ([I64, I64], SZ),
+        "qg_add_lora_workspace_bytes": ([I64, I64, I64], SZ),
         "qg_add_lora": ([P, I, I64, P, I, I64, I64, I64, P, P, I64, I64, I64, P, P, P, I64, P, SZ, P], I),
     }
     for name, (args, res) in sigs.items():
@@ -652,9 +652,9 @@ def gemm_fp8_grouped(q, scale, offsets, w, w_scale, out=None, out_dtype=torch.bf
 
 
 @functools.lru_cache(maxsize=4096)
-def add_lora_workspace_bytes(M, rank):
+def add_lora_workspace_bytes(M, K, rank):
     """Workspace bytes an add_lora call of these sizes needs (0: invalid sizes)."""
-    return int(load().qg_add_lora_workspace_bytes(M, rank))
+    return int(load().qg_add_lora_workspace_bytes(M, K, rank))
 
 
 def add_lora(base, x, a, b, ids, scaling=None, out=None, workspace=None, stream=None):
@@ -687,7 +687,7 @@ def add_lora(base, x, a, b, ids, scaling=None, out=None, workspace=None, stream=
         if m != M or n != N:
             raise ValueError("out must have the shape (%d, %d)" % (M, N))
     if workspace is None:
-        nbytes = add_lora_workspace_bytes(M, rank)
+        nbytes = add_lora_workspace_bytes(M, K, rank)
         workspace = _empty((nbytes,), torch.uint8, base.device, stream)
     else:
         if workspace.get_device() != dev or not workspace.is_contiguous():

@@ -67,11 +67,12 @@ cudaError_t launch_gemm_fp8_grouped(const uint8_t* q, const float* scale, int64_
                                     int64_t ldw, int64_t lde, const float* w_scale, int64_t N,
                                     void* out, bool out_f32, int64_t ldo, uint32_t* err,
                                     cudaStream_t st);
-int lora_padded_rank(int64_t rank);
+int64_t lora_workspace(int64_t M, int64_t K, int64_t rank);
 cudaError_t launch_add_lora(const void* base, bool bf16, int64_t ldb, const void* x, bool x_bf16,
                             int64_t M, int64_t K, int64_t ldx, const void* A, const void* B,
                             int64_t count, int64_t rank, int64_t N, const int64_t* ids,
-                            const float* scaling, void* out, int64_t ldo, void* ws, cudaStream_t st);
+                            const float* scaling, void* out, int64_t ldo, void* ws, uint32_t* err,
+                            cudaStream_t st);
 int lp_splits(int64_t M, int64_t V, int sms);
 }  // namespace qg
 
@@ -792,9 +793,9 @@ qg_status qg_gemm_fp8_grouped(const uint8_t* q, const float* scale, int64_t lds,
                    "grouped FP8 GEMM launch");
 }
 
-size_t qg_add_lora_workspace_bytes(int64_t M, int64_t rank) {
-  if (M < 1 || M > kMaxLoraM || rank < 8 || rank > QG_LORA_MAX_RANK || rank % 8 != 0) return 0;
-  return (size_t)align_up(M * lora_padded_rank(rank) * 4, 256);
+size_t qg_add_lora_workspace_bytes(int64_t M, int64_t K, int64_t rank) {
+  if (M < 1 || check_fp8_k(K) != QG_OK || M > kMaxLoraM || rank < 8 || rank > QG_LORA_MAX_RANK || rank % 8 != 0) return 0;
+  return (size_t)align_up(lora_workspace(M, K, rank), 256);
 }
 
 qg_status qg_add_lora(const void* base, qg_dtype dtype, int64_t ldb, const void* x, qg_dtype x_dtype,
@@ -821,13 +822,13 @@ qg_status qg_add_lora(const void* base, qg_dtype dtype, int64_t ldb, const void*
   if (!aligned(base, es) || !aligned(out, es) || !aligned(a, 16) || !aligned(b, 16) || !aligned(ids, 8) ||
       (scaling && !aligned(scaling, 4)))
     return fail(QG_EALIGN, "a and b need 16-byte alignment, every other array that of its elements");
-  const size_t need = qg_add_lora_workspace_bytes(M, rank);
+  const size_t need = qg_add_lora_workspace_bytes(M, K, rank);
   if (!workspace || workspace_bytes < need)
     return fail(QG_EINVAL, "workspace of %lld bytes needed for M=%lld (qg_add_lora_workspace_bytes)",
                 (long long)need, (long long)M);
   if (!aligned(workspace, 256)) return fail(QG_EALIGN, "workspace needs 256-byte alignment");
   return from_cuda(launch_add_lora(base, dtype == QG_BF16, ldb, x, x_dtype == QG_BF16, M, K, ldx, a, b,
-                                   adapters, rank, N, ids, scaling, out, ldo, workspace,
+                                   adapters, rank, N, ids, scaling, out, ldo, workspace, error_word(),
                                    reinterpret_cast<cudaStream_t>(stream)),
                    "adapter launch");
 }

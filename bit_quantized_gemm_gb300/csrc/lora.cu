@@ -4,20 +4,34 @@
 //   out[m][n] = base[m][n] + sum_r (scaling[id] * h[m][r]) * B[id][n][r]
 // A row whose id is not one of the adapters keeps base's bits.
 //
-// Two kernels. `shrink` forms scaling * h and leaves it as the sum of two bf16
-// numbers (off by 2^-17 of itself: the sum of the two products is then as good
-// as one with an fp32 h); `expand`, its programmatic dependent, adds the second
-// product to base. Both use warp-level m16n8k16 MMAs with operands straight from
-// global memory: the products are short (rank 8 to 128) beside what is moved, x
-// and the adapters once, base and out.
-//
-// Rows may come in any order. In a window of consecutive rows the different ids
-// are found by votes, and the rows of each, wherever they lie in it, are one
-// piece of work: rows of one request that follow one another cost one pass, the
-// rows of 32 requests 32, which are dealt out over CTAs when there are few rows.
+// `shrink` leaves h as sums over parts of K, which are added up in order and
+// scaled; `expand` adds the second product to base. The parts are cut by K alone,
+// so a row's bits do not depend on the other rows, but for the choice of the kernels:
+//   up to 128 rows (decode), bound by reading the adapters that the rows use: a
+//   row at a time on the fp32 units, a few products for every value read;
+//   more rows, bound by x, base and out: products on the tensor cores, where
+//   scaling * h goes in as the sum of two bf16 numbers (off by 2^-17 of itself:
+//   as good as an fp32 h), everything by TMA.
+// Each kernel is a programmatic dependent of the one before it. Rows may come in
+// any order. Many rows are taken in tiles of 128, in which the different ids are
+// found by votes; each costs a pass over the tile.
+#include <cuda.h>
+
+#include <cstring>
+
 #include "qg_common.cuh"
 
 namespace qg {
+
+bool make_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t cols,
+                  int64_t rows, int64_t pitch, uint32_t box_cols, uint32_t box_rows,
+                  CUtensorMapSwizzle swizzle);
+bool make_tmap_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t cols,
+                  int64_t rows, int64_t mats, int64_t pitch, int64_t mat_pitch, uint32_t box_cols,
+                  uint32_t box_rows, CUtensorMapSwizzle swizzle);
+
+constexpr int kLoraFew = 128;                      // rows that are taken one at a time
+constexpr int kManyParts = 8;                      // parts of K of many rows
 
 struct LoraArgs {
   const void* x;
@@ -26,19 +40,11 @@ struct LoraArgs {
   const float* scaling;   // [count] or null
   const void* base;
   void* out;
-  uint32_t* h;            // [M][2][padded rank / 2] pairs of bf16: of each row the large parts, the small parts
+  float* h;               // [parts][M][rp], rp ranks a row (many rows: up to 16, 32, 64 or 128)
+  uint32_t* parts;        // many rows: scaling * h as [large, small parts][M][rp / 2] pairs of bf16
   int64_t ldx, ldb, ldo, M;
-  int K, N, rank, count;
+  int K, N, rank, count, rp;
 };
-
-// D (16 x 8) += A (16 x 16) * B (16 x 8), bf16 operands, fp32 sums
-__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -52,6 +58,231 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& a, int64_t m) {
   if (m >= a.M) return -1;
   const int64_t id = __ldg(a.ids + m);
   return id >= 0 && id < a.count ? (int)id : -1;
+}
+
+// one value of base or out
+template <bool kBf16>
+__device__ __forceinline__ uint32_t load_raw(const void* p, int64_t i) {
+  if (kBf16) return reinterpret_cast<const uint16_t*>(p)[i];
+  return reinterpret_cast<const uint32_t*>(p)[i];
+}
+template <bool kBf16>
+__device__ __forceinline__ void store_raw(void* p, int64_t i, uint32_t v) {
+  if (kBf16) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)v;
+  else reinterpret_cast<uint32_t*>(p)[i] = v;
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t add_raw(uint32_t v, float y) {
+  if (kBf16) return f32_to_bf16_rne(__uint_as_float(v << 16) + y);
+  return __float_as_uint(__uint_as_float(v) + y);
+}
+
+// -------------------------------------------------------------------- few rows
+// A CTA sums one part of K (up to 1024 values) of one row, a warp the ranks warp,
+// warp + 8, ...: 8 values a lane at a time, up to kU times, all loads of R ranks
+// ahead of the first product.
+constexpr int kFewWarps = 8, kFewPart = 128;  // eights of a part
+__host__ __device__ inline int few_parts(int K) { return (K / 8 + kFewPart - 1) / kFewPart; }
+
+template <bool kBf16, int R>
+__global__ void __launch_bounds__(32 * kFewWarps) lora_shrink_few_kernel(const LoraArgs a) {
+  griddep_launch_dependents();
+  constexpr int kU = R <= 2 ? 4 : R == 4 ? 2 : 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = blockIdx.x, parts = gridDim.x;
+  const int64_t m = blockIdx.y;
+  const int id = adapter_of(a, m);
+  if (id < 0) return;
+  const int eights = a.K / 8;
+  const int e0 = eights * part / parts, e1 = eights * (part + 1) / parts;
+  const char* px = reinterpret_cast<const char*>(a.x) + m * a.ldx * (kBf16 ? 2 : 4);
+  const uint16_t* pa = a.a + (int64_t)id * a.rank * a.K;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  float acc[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) acc[i] = 0.0f;
+  for (int base = e0 + lane; base - lane < e1; base += 32 * kU) {
+    uint4 x[kU][kBf16 ? 1 : 2], w[kU][R];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int e = base + 32 * u;
+#pragma unroll
+      for (int j = 0; j < (kBf16 ? 1 : 2); ++j)
+        x[u][j] = e < e1 ? __ldg(reinterpret_cast<const uint4*>(px) + (kBf16 ? 1 : 2) * e + j) : zero;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int r = i * kFewWarps + warp;
+        w[u][i] = e < e1 && r < a.rank ? __ldg(reinterpret_cast<const uint4*>(pa + (int64_t)r * a.K) + e) : zero;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      float f[8];
+      if (kBf16) {
+        const uint32_t v[4] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[2 * j] = bf16_lo(v[j]);
+          f[2 * j + 1] = bf16_hi(v[j]);
+        }
+      } else {
+        const uint4 lo = x[u][0], hi = x[u][kBf16 ? 0 : 1];
+        const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(v[j]);
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const uint32_t v[4] = {w[u][i].x, w[u][i].y, w[u][i].z, w[u][i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[i] = fmaf(f[2 * j], bf16_lo(v[j]), acc[i]);
+          acc[i] = fmaf(f[2 * j + 1], bf16_hi(v[j]), acc[i]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int r = i * kFewWarps + warp;
+    if (r >= a.rank) break;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    if (lane == 0) a.h[((int64_t)part * a.M + m) * a.rp + r] = acc[i];
+  }
+}
+
+// A warp adds to 32 C columns of kFewRows rows, one after another, a lane to
+// column lane (+ 32). B's part for a row (contiguous: columns x rank) comes
+// through a ring of the warp's own by bulk copies, once for rows that follow one
+// another with one id. A lane reads its column's ranks eight at a time, starting
+// with another eight than its neighbours, so that their reads do not conflict.
+constexpr int kExpandWarps = 4, kExpandRing = 4, kFewRows = 8;
+template <bool kBf16, int C>
+__global__ void __launch_bounds__(32 * kExpandWarps) lora_expand_few_kernel(const LoraArgs a, uint32_t* err) {
+  extern __shared__ __align__(128) uint8_t smem[];  // [warp][slot][column][rank], then h [row][rank]
+  __shared__ uint64_t full[kExpandWarps][kExpandRing];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = a.rank;
+  const int slot_bytes = 32 * C * rank * 2;
+  uint8_t* const ring = smem + warp * kExpandRing * slot_bytes;
+  float* const h = reinterpret_cast<float*>(smem + kExpandWarps * kExpandRing * slot_bytes);
+  const int col0 = ((int)blockIdx.x * kExpandWarps + warp) * 32 * C;
+  const int cols = min(32 * C, a.N - col0);  // (none: a warp behind the last column)
+  const int64_t m0 = (int64_t)blockIdx.y * kFewRows;
+  const int rows = (int)min((int64_t)kFewRows, a.M - m0);
+  const bool keep = a.base == a.out && a.ldb == a.ldo;  // rows without an adapter are in place
+  const int mine = lane < rows ? adapter_of(a, m0 + lane) : -1;
+  // a row brings B unless the last row before it that has an adapter has the same
+  const uint32_t with = __ballot_sync(0xffffffffu, mine >= 0);
+  const uint32_t before = with & ((1u << lane) - 1);
+  const int last = __shfl_sync(0xffffffffu, mine, before ? 31 - __clz(before) : 0);
+  const uint32_t brings = cols > 0 ? __ballot_sync(0xffffffffu, mine >= 0 && (!before || last != mine)) : 0;
+  if (lane == 0) {
+    for (int i = 0; i < kExpandRing; ++i) mbar_init(&full[warp][i], 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  uint32_t left = brings;  // rows whose B has not been asked for
+  int asked = 0;
+  auto ask = [&] {
+    if (!left) return;
+    const int id = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1), s = asked % kExpandRing;
+    left &= left - 1;
+    ++asked;
+    if (lane == 0) {
+      fence_proxy_async_smem();  // (the slot's reads come before its refill)
+      mbar_arrive_expect_tx(&full[warp][s], cols * rank * 2);
+      bulk_copy_g2s(ring + s * slot_bytes, a.b + ((int64_t)id * a.N + col0) * rank, cols * rank * 2, &full[warp][s]);
+    }
+    __syncwarp();
+  };
+#pragma unroll
+  for (int i = 0; i < kExpandRing; ++i) ask();
+  uint32_t raw[C], raw_next[C];
+  auto load_base = [&](int row, uint32_t (&v)[C]) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      v[c] = row < rows && lane + 32 * c < cols ? load_raw<kBf16>(a.base, (m0 + row) * a.ldb + col0 + lane + 32 * c) : 0;
+  };
+  load_base(0, raw);
+  // nothing above is shrink's work; out may be what a kernel before it reads
+  griddep_wait();
+  const int parts = few_parts(a.K);
+  for (int e = threadIdx.x; e < rows * (rank / 4); e += 32 * kExpandWarps) {
+    const int row = e / (rank / 4), r = e % (rank / 4) * 4;
+    const int id = adapter_of(a, m0 + row);
+    if (id < 0) continue;
+    float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+    for (int i = 0; i < parts; ++i) {
+      const float4 p = *reinterpret_cast<const float4*>(a.h + ((int64_t)i * a.M + m0 + row) * a.rp + r);
+      v.x += p.x;
+      v.y += p.y;
+      v.z += p.z;
+      v.w += p.w;
+    }
+    const float scale = a.scaling ? __ldg(a.scaling + id) : 1.0f;
+    *reinterpret_cast<float4*>(h + row * rank + r) = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+  }
+  __syncthreads();
+  int used = -1;  // the slot in use, counted from the first
+  bool ok = true;
+  for (int row = 0; row < rows && cols > 0; ++row) {
+    load_base(row + 1, raw_next);
+    if (with >> row & 1) {
+      if (brings >> row & 1) {
+        if (used >= 0) {
+          __syncwarp();  // every lane has read the slot that is asked for again
+          ask();
+        }
+        ++used;
+        if (ok) ok = mbar_wait_warp(&full[warp][used % kExpandRing], (uint32_t)(used / kExpandRing) & 1u, err);
+      }
+      const uint8_t* from = ring + (used % kExpandRing) * slot_bytes;
+      const int eights = rank >> 3;
+      float acc[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] = 0.0f;
+      int e = lane % eights;
+#pragma unroll 2
+      for (int i = 0; i < eights; ++i) {
+        const float4 h0 = *reinterpret_cast<const float4*>(h + row * rank + e * 8);
+        const float4 h1 = *reinterpret_cast<const float4*>(h + row * rank + e * 8 + 4);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const uint4 v = *reinterpret_cast<const uint4*>(from + (lane + 32 * c) * rank * 2 + e * 16);
+          acc[c] = fmaf(h0.x, bf16_lo(v.x), acc[c]);
+          acc[c] = fmaf(h0.y, bf16_hi(v.x), acc[c]);
+          acc[c] = fmaf(h0.z, bf16_lo(v.y), acc[c]);
+          acc[c] = fmaf(h0.w, bf16_hi(v.y), acc[c]);
+          acc[c] = fmaf(h1.x, bf16_lo(v.z), acc[c]);
+          acc[c] = fmaf(h1.y, bf16_hi(v.z), acc[c]);
+          acc[c] = fmaf(h1.z, bf16_lo(v.w), acc[c]);
+          acc[c] = fmaf(h1.w, bf16_hi(v.w), acc[c]);
+        }
+        if (++e == eights) e = 0;
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) raw[c] = add_raw<kBf16>(raw[c], acc[c]);
+    }
+    if ((with >> row & 1) || !keep) {  // (a row without an adapter keeps base's bits)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (lane + 32 * c < cols) store_raw<kBf16>(a.out, (m0 + row) * a.ldo + col0 + lane + 32 * c, raw[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) raw[c] = raw_next[c];
+  }
+  // (every copy asked for has been waited for: each is some row's)
+}
+
+// ------------------------------------------------------------------- many rows
+// D (16 x 8) += A (16 x 16) * B (16 x 8), bf16 operands, fp32 sums
+__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // position of set bit number n (from 0) of a mask that has more than n
@@ -90,184 +321,38 @@ struct LoraPieces {
   }
 };
 
-// ---------------------------------------------------------------------- shrink
-// K is cut into 64 shares, eight groups of eight. A share's sum is a chain of
-// MMAs; the eight shares of a group are added in order, then the eight groups.
-// Where shares lie on different warps or CTAs does not change that order, and it
-// depends on K alone: a row's bits do not depend on the other rows of its call.
-constexpr int kShares = 8, kGroups = 8;
-
-// A's rows are the MMA's 16, NT times 8 rows of x its columns. A lane loads 8
-// consecutive k of a row (16 bytes): they are k 8t.. of 32, t = lane % 4, of
-// both operands, in whatever order the MMA sums them.
-template <bool kBf16, int RT, int NT>
+// One step of 32 values of K: A's rows are the MMA's 16, 8 rows of x its columns. A
+// lane has 8 consecutive k of a row of each: k 8t.. of 32, t = lane % 4, in
+// whatever order the MMA sums them. A value of x goes in as the sum of three bf16
+// numbers (24 bits).
+template <int RT>
 struct ShrinkStep {
-  static constexpr int P = kBf16 ? 1 : 3;  // bf16 numbers a value of x: fp32 as the sum of three (24 bits)
-  uint4 w[RT][2];
-  uint4 x[NT][kBf16 ? 1 : 2];
-  __device__ __forceinline__ void load(const uint16_t* pa, const char* const (&px)[NT], int k, int K, int rank) {
-    const int g = (threadIdx.x & 31) >> 2;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 w[RT][2], x[2];
+  __device__ __forceinline__ void multiply(float (&acc)[RT][4]) const {
+    const uint32_t u[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    float f[8];
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int c = 0; c < 8; ++c) f[c] = __uint_as_float(u[c]);
 #pragma unroll
-      for (int j = 0; j < (kBf16 ? 1 : 2); ++j)
-        x[i][j] = k < K ? __ldg(reinterpret_cast<const uint4*>(px[i] + (int64_t)k * (kBf16 ? 2 : 4)) + j) : zero;
+    for (int q = 0; q < 3; ++q) {
+      uint32_t v[4];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = r * 16 + h * 8 + g;
-        w[r][h] = k < K && row < rank ? __ldg(reinterpret_cast<const uint4*>(pa + (int64_t)row * K + k)) : zero;
-      }
-  }
-  __device__ __forceinline__ void multiply(float (&acc)[RT][NT][4]) const {
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      uint32_t v[P][4];
-      if (kBf16) {
-        v[0][0] = x[i][0].x;
-        v[0][1] = x[i][0].y;
-        v[0][2] = x[i][0].z;
-        v[0][3] = x[i][0].w;
-      } else {
-        const uint4 lo = x[i][0], hi = x[i][kBf16 ? 0 : 1];
-        const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        float f[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) f[c] = __uint_as_float(u[c]);
-#pragma unroll
-        for (int q = 0; q < P; ++q)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t b = bf16x2(f[2 * c], f[2 * c + 1]);
-            v[q][c] = b;
-            // (an infinity's rest would be NaN)
-            f[2 * c] = isfinite(bf16_lo(b)) ? f[2 * c] - bf16_lo(b) : 0.0f;
-            f[2 * c + 1] = isfinite(bf16_hi(b)) ? f[2 * c + 1] - bf16_hi(b) : 0.0f;
-          }
+      for (int c = 0; c < 4; ++c) {
+        v[c] = bf16x2(f[2 * c], f[2 * c + 1]);
+        // (an infinity's rest would be NaN)
+        f[2 * c] = isfinite(bf16_lo(v[c])) ? f[2 * c] - bf16_lo(v[c]) : 0.0f;
+        f[2 * c + 1] = isfinite(bf16_hi(v[c])) ? f[2 * c + 1] - bf16_hi(v[c]) : 0.0f;
       }
 #pragma unroll
-      for (int q = 0; q < P; ++q)
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const uint32_t f0[4] = {w[r][0].x, w[r][1].x, w[r][0].y, w[r][1].y};
-          const uint32_t f1[4] = {w[r][0].z, w[r][1].z, w[r][0].w, w[r][1].w};
-          mma_bf16_16816(acc[r][i], f0, v[q][0], v[q][1]);
-          mma_bf16_16816(acc[r][i], f1, v[q][2], v[q][3]);
-        }
+      for (int r = 0; r < RT; ++r) {
+        const uint32_t f0[4] = {w[r][0].x, w[r][1].x, w[r][0].y, w[r][1].y};
+        const uint32_t f1[4] = {w[r][0].z, w[r][1].z, w[r][0].w, w[r][1].w};
+        mma_bf16_16816(acc[r], f0, v[0], v[1]);
+        mma_bf16_16816(acc[r], f1, v[2], v[3]);
+      }
     }
   }
 };
-
-template <int RT, int NT>
-__device__ __forceinline__ void zero(float (&acc)[RT][NT][4]) {
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[r][i][c] = 0.0f;
-}
-
-// kU steps loaded before the first is worked on
-template <bool kBf16, int RT, int NT, int kU>
-__device__ __forceinline__ void add_share(float (&acc)[RT][NT][4], const LoraArgs& a, const uint16_t* pa,
-                                          const char* const (&px)[NT], int share) {
-  const int units = (a.K + 31) >> 5, t = threadIdx.x & 3;
-  const int u0 = units * share / (kShares * kGroups), u1 = units * (share + 1) / (kShares * kGroups);
-  for (int u = u0; u < u1; u += kU) {
-    ShrinkStep<kBf16, RT, NT> s[kU];
-#pragma unroll
-    for (int i = 0; i < kU; ++i)
-      if (u + i < u1) s[i].load(pa, px, (u + i) * 32 + t * 8, a.K, a.rank);
-#pragma unroll
-    for (int i = 0; i < kU; ++i)
-      if (u + i < u1) s[i].multiply(acc);
-  }
-}
-
-// acc[r][i]: ranks 16r + g (c 0, 1) and + 8 (c 2, 3) of rows 8i + 2t and + 1
-template <int RT, int NT>
-__device__ __forceinline__ void put(float* part, const float (&acc)[RT][NT][4]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        part[(8 * i + 2 * t + (c & 1)) * (RT * 16 + 4) + r * 16 + g + 8 * (c >> 1)] = acc[r][i][c];
-}
-
-// ranks r and r + 1 of a row's sum v, scaled, as two bf16 numbers each
-__device__ __forceinline__ void put_h(const LoraArgs& a, int64_t m, int rp, int r, float scale, float v0, float v1) {
-  // (ranks that only pad: 0, also where x is infinite)
-  v0 = r < a.rank ? v0 * scale : 0.0f;
-  v1 = r < a.rank ? v1 * scale : 0.0f;
-  const uint32_t hi = bf16x2(v0, v1);
-  const uint32_t lo = bf16x2(isfinite(bf16_lo(hi)) ? v0 - bf16_lo(hi) : 0.0f,
-                             isfinite(bf16_hi(hi)) ? v1 - bf16_hi(hi) : 0.0f);
-  uint32_t* h = a.h + m * rp + r / 2;
-  h[0] = hi;
-  h[rp / 2] = lo;
-}
-
-// The groups' sums of a piece's rows, added in order by the cluster's threads
-template <int RP>
-__device__ __forceinline__ void join_groups(const LoraArgs& a, const float* sum, int64_t m0, int id, uint32_t rows,
-                                            int rank) {
-  const int count = __popc(rows);
-  const float scale = a.scaling ? __ldg(a.scaling + id) : 1.0f;
-  for (int e = ((int)threadIdx.x * kGroups + rank) * 2; e < count * RP; e += 2 * (int)blockDim.x * kGroups) {
-    float v0 = 0.0f, v1 = 0.0f;
-#pragma unroll
-    for (int c = 0; c < kGroups; ++c) {
-      const uint32_t p = map_to_cta(sum + e, c);
-      v0 += ld_cluster_f32(p);
-      v1 += ld_cluster_f32(p + 4);
-    }
-    put_h(a, m0 + nth_bit(rows, e / RP), RP, e % RP, scale, v0, v1);
-  }
-}
-
-// Few rows: windows of 8 rows; a cluster of eight CTAs, one a group of K, one
-// warp a share. gridDim.z CTAs share a window's pieces.
-template <bool kBf16, int RT>
-__global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(32 * kShares)
-    lora_shrink_few_kernel(const LoraArgs a) {
-  griddep_launch_dependents();
-  constexpr int RP = RT * 16, kPitch = RP + 4;
-  __shared__ float part[kShares][8 * kPitch], sum[8 * RP];
-  const int warp = threadIdx.x >> 5, g = (threadIdx.x & 31) >> 2;
-  const uint32_t rank = cluster_ctarank();
-  const int64_t m0 = (int64_t)blockIdx.y * 8;
-  LoraPieces pieces(a, m0, 8);
-  int id, j = 0;
-  uint32_t rows;
-  while (pieces.next(j, blockIdx.z, gridDim.z, id, rows)) {
-    if (id < 0) continue;
-    const int count = __popc(rows);
-    // this lane's row of x, the g-th (past the last: the last)
-    const char* px[1] = {reinterpret_cast<const char*>(a.x) +
-                         (m0 + nth_bit(rows, min(g, count - 1))) * a.ldx * (kBf16 ? 2 : 4)};
-    float acc[RT][1][4];
-    zero(acc);
-    add_share<kBf16, RT, 1, RT == 1 ? 5 : RT == 2 ? 3 : RT == 4 ? 2 : 1>(
-        acc, a, a.a + (int64_t)id * a.rank * a.K, px, (int)rank * kShares + warp);
-    put(part[warp], acc);
-    __syncthreads();
-    for (int e = threadIdx.x; e < count * RP; e += 32 * kShares) {
-      float s = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kShares; ++w) s += part[w][e / RP * kPitch + e % RP];
-      sum[e] = s;
-    }
-    cluster_sync();
-    join_groups<RP>(a, sum, m0, id, rows, (int)rank);
-    cluster_sync();  // the sums have been read
-  }
-}
 
 // asynchronous 16-byte global -> shared copy; `in` false: zeros
 __device__ __forceinline__ void cp_async_16(void* to, const void* from, bool in) {
@@ -275,33 +360,31 @@ __device__ __forceinline__ void cp_async_16(void* to, const void* from, bool in)
                : "memory");
 }
 
-// Many rows: windows of 32; a cluster of eight CTAs, one a group of K, that
-// brings its steps of K (32 values of every row of x and of A) through a ring in
-// shared memory; warp w multiplies rows 8w.. of the piece. A step's rows lie 64
-// bytes apart (x in fp32: 128), which a lane's 16-byte reads of row lane / 4,
-// piece lane % 4, take without conflicts. Two steps are fetched at once, whole
-// 128-byte lines.
-constexpr int kManyWarps = 4, kManyRing = 4;
-template <bool kBf16, int RT>
+// Many rows of fp32 x, which tcgen05 has no type of enough bits for: windows of 32
+// rows; a CTA a part of K, whose steps (32 values of every row of x and of A) it
+// brings through a ring in shared memory; warp w multiplies rows 8w.. of the
+// piece. A step's rows of A lie 64 bytes apart, which a lane's 16-byte reads of row
+// lane / 4, piece lane % 4, take without conflicts. Two steps are fetched at once.
+// A part is cut into eight shares, whose sums are added in order (chains of MMAs of
+// bounded length).
+constexpr int kManyWarps = 4, kManyRing = 4, kShares = 8;
+template <int RT>
 struct ManyCfg {
-  static constexpr int kX = 32 * (kBf16 ? 64 : 128), kA = RT * 16 * 64, kStep = kX + kA;
-  static constexpr int kSum = 32 * RT * 16 * 4;
-  static constexpr int kSmem = kManyRing * 2 * kStep + kSum;
+  static constexpr int kX = 32 * 128, kA = RT * 16 * 64, kStep = kX + kA;
+  static constexpr int kSmem = kManyRing * 2 * kStep;
 };
 
-template <bool kBf16, int RT>
-__global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(32 * kManyWarps)
-    lora_shrink_many_kernel(const LoraArgs a) {
+template <int RT>
+__global__ void __launch_bounds__(32 * kManyWarps) lora_shrink_many_kernel(const LoraArgs a) {
   griddep_launch_dependents();
-  using C = ManyCfg<kBf16, RT>;
+  using C = ManyCfg<RT>;
   constexpr int RP = RT * 16, kThreads = 32 * kManyWarps;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* const sum = reinterpret_cast<float*>(smem + kManyRing * 2 * C::kStep);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint32_t rank = cluster_ctarank();
+  const int kg = blockIdx.x;
   const int64_t m0 = (int64_t)blockIdx.y * 32;
   const int units = (a.K + 31) >> 5;
-  const int u0 = units * (int)rank / kGroups, u1 = units * ((int)rank + 1) / kGroups;  // this group's steps
+  const int u0 = units * kg / kManyParts, u1 = units * (kg + 1) / kManyParts;  // this group's steps
   LoraPieces pieces(a, m0, 32);
   int id, j = 0;
   uint32_t rows;
@@ -309,14 +392,14 @@ __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(32 * kManyWarp
     if (id < 0) continue;
     const int count = __popc(rows);
     const uint16_t* pa = a.a + (int64_t)id * a.rank * a.K;
-    // x: four threads a row (eight of fp32), 32 or 16 rows a round
-    constexpr int kPer = kBf16 ? 4 : 8, kRounds = 32 * kPer / kThreads;
+    // x: eight threads a row, 16 rows a round
+    constexpr int kPer = 8, kRounds = 32 * kPer / kThreads;
     const char* px[kRounds];
 #pragma unroll
     for (int i = 0; i < kRounds; ++i)
       px[i] = reinterpret_cast<const char*>(a.x) +
               (m0 + nth_bit(rows, min(i * (kThreads / kPer) + (int)threadIdx.x / kPer, count - 1))) * a.ldx *
-                  (kBf16 ? 2 : 4);
+                  4;
     auto fetch = [&](int u) {  // steps u and u + 1
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
@@ -325,9 +408,9 @@ __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(32 * kManyWarp
 #pragma unroll
         for (int i = 0; i < kRounds; ++i) {
           const int c = threadIdx.x % kPer, row = i * (kThreads / kPer) + (int)threadIdx.x / kPer;
-          const int k = (u + d) * 32 + c * (kBf16 ? 8 : 4);
+          const int k = (u + d) * 32 + c * 4;
           const bool ok = in && row < count && k < a.K;
-          cp_async_16(to + row * (kBf16 ? 64 : 128) + c * 16, px[i] + (ok ? (int64_t)k * (kBf16 ? 2 : 4) : 0), ok);
+          cp_async_16(to + row * 128 + c * 16, px[i] + (ok ? (int64_t)k * 4 : 0), ok);
         }
 #pragma unroll
         for (int i = 0; i < (RP * 4 + kThreads - 1) / kThreads; ++i) {
@@ -341,22 +424,24 @@ __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(32 * kManyWarp
     };
 #pragma unroll
     for (int i = 0; i < kManyRing - 1; ++i) fetch(u0 + 2 * i);
-    float group[RT][1][4], acc[RT][1][4];
-    zero(group);
-    zero(acc);
-    int share = (int)rank * kShares;
-    int end = units * (share + 1) / (kShares * kGroups);  // of the share
+    float group[RT][4], acc[RT][4];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) group[r][c] = acc[r][c] = 0.0f;
+    int share = kg * kShares;
+    int end = units * (share + 1) / (kShares * kManyParts);  // of the share
     auto fold = [&](int u) {                              // shares that end at step u
-      while (u == end && share < ((int)rank + 1) * kShares) {
+      while (u == end && share < (kg + 1) * kShares) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            group[r][0][c] += acc[r][0][c];
-            acc[r][0][c] = 0.0f;
+            group[r][c] += acc[r][c];
+            acc[r][c] = 0.0f;
           }
         ++share;
-        end = units * (share + 1) / (kShares * kGroups);
+        end = units * (share + 1) / (kShares * kManyParts);
       }
     };
     fold(u0);
@@ -369,10 +454,10 @@ __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(32 * kManyWarp
         for (int d = 0; d < 2; ++d) {
           if (u + d >= u1) break;
           const uint8_t* from = smem + (((u - u0) / 2 % kManyRing) * 2 + d) * C::kStep;
-          ShrinkStep<kBf16, RT, 1> s;
-          const uint8_t* fx = from + (warp * 8 + g) * (kBf16 ? 64 : 128) + t * (kBf16 ? 16 : 32);
+          ShrinkStep<RT> s;
+          const uint8_t* fx = from + (warp * 8 + g) * 128 + t * 32;
 #pragma unroll
-          for (int i = 0; i < (kBf16 ? 1 : 2); ++i) s.x[0][i] = *(reinterpret_cast<const uint4*>(fx) + i);
+          for (int i = 0; i < 2; ++i) s.x[i] = *(reinterpret_cast<const uint4*>(fx) + i);
 #pragma unroll
           for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -384,317 +469,699 @@ __global__ void __cluster_dims__(kGroups, 1, 1) __launch_bounds__(32 * kManyWarp
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (warp * 8 < count) {
+    // group[r]: ranks 16r + g (c 0, 1) and + 8 (c 2, 3) of rows 2t and + 1 of the warp's eight
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
+    for (int c = 0; c < 2; ++c) {
+      const int n = warp * 8 + 2 * t + c;
+      if (n >= count) continue;
+      float* to = a.h + ((int64_t)kg * a.M + m0 + nth_bit(rows, n)) * RP + g;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          sum[(warp * 8 + 2 * t + (c & 1)) * RP + r * 16 + g + 8 * (c >> 1)] = group[r][0][c];
+      for (int r = 0; r < RT; ++r) {
+        to[r * 16] = group[r][c];
+        to[r * 16 + 8] = group[r][2 + c];
+      }
     }
-    cluster_sync();
-    join_groups<RP>(a, sum, m0, id, rows, (int)rank);
-    cluster_sync();  // the sums have been read
+    __syncthreads();  // the ring has been read
   }
 }
 
-// ---------------------------------------------------------------------- expand
-constexpr int kExpandWarps = 4, kExpandCols = 64;
-
-// eight consecutive columns of a row of base or out, as they lie in memory
-template <bool kBf16>
-struct Cols8 {
-  static constexpr int kWords = kBf16 ? 4 : 8, kEs = kBf16 ? 2 : 4;
-  uint32_t w[kWords];
-  __device__ __forceinline__ void load(const char* p, int n, bool vec) {  // n of them
-    if (vec && n >= 8) {
+// The different adapters of 128 rows, in the order of their first rows of a lane:
+// number k in lane k % 32 (every warp that asks finds them by itself).
+struct TileIds {
+  int list[4], count;
+  int v[4];  // the ids of rows lane, lane + 32, ...
+  __device__ __forceinline__ void load(const LoraArgs& a, int64_t m0) {
 #pragma unroll
-      for (int i = 0; i < kWords / 4; ++i) {
-        const uint4 v = *(reinterpret_cast<const uint4*>(p) + i);
-        w[4 * i] = v.x;
-        w[4 * i + 1] = v.y;
-        w[4 * i + 2] = v.z;
-        w[4 * i + 3] = v.w;
-      }
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) {
-        if (kBf16)
-          w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-        else
-          w[i % kWords] = reinterpret_cast<const uint32_t*>(p)[i];
-      }
+    for (int j = 0; j < 4; ++j) v[j] = adapter_of(a, m0 + j * 32 + (threadIdx.x & 31));
   }
-  __device__ __forceinline__ void add(int i, float y0, float y1) {  // to columns 2i and 2i + 1
-    if (kBf16) {
-      w[i] = bf16x2(bf16_lo(w[i]) + y0, bf16_hi(w[i]) + y1);
-    } else {
-      w[2 * i % kWords] = __float_as_uint(__uint_as_float(w[2 * i % kWords]) + y0);
-      w[(2 * i + 1) % kWords] = __float_as_uint(__uint_as_float(w[(2 * i + 1) % kWords]) + y1);
+  __device__ __forceinline__ void find() {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) list[j] = -1;
+    count = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t left;
+      while ((left = __ballot_sync(0xffffffffu, v[j] >= 0)) != 0) {
+        const int id = __shfl_sync(0xffffffffu, v[j], __ffs(left) - 1);
+#pragma unroll
+        for (int i = j; i < 4; ++i)
+          if (v[i] == id) v[i] = -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (count == i * 32 + lane) list[i] = id;
+        ++count;
+      }
     }
   }
-  __device__ __forceinline__ void store(char* p, int n, bool vec) const {
-    if (vec && n >= 8) {
-#pragma unroll
-      for (int i = 0; i < kWords / 4; ++i)
-        *(reinterpret_cast<uint4*>(p) + i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) {
-        if (kBf16)
-          reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-        else
-          reinterpret_cast<uint32_t*>(p)[i] = w[i % kWords];
-      }
+  __device__ __forceinline__ int at(int k) const {
+    const int v = k < 32 ? list[0] : k < 64 ? list[1] : k < 96 ? list[2] : list[3];
+    return __shfl_sync(0xffffffffu, v, k & 31);
   }
 };
 
-// A warp adds to kCols columns of a piece's rows, 16 rows an MMA. The MMA's
-// columns are dealt out so that a lane's outputs of four MMAs are 8 consecutive
-// columns of two rows: column 2t + i of MMA j is column 8t + 2j + i of 32. Ranks
-// likewise: a lane's are 8t.. of 32 (two MMAs; 4t.. of 16 for ranks up to 16), so
-// that it reads both operands in 16 bytes. A warp's part of B stays in registers
-// from piece to piece while the id is the same; where it is small, the next
-// piece's is on its way. Windows of 32 rows; a CTA takes `windows` of them,
-// gridDim.z CTAs share a window's pieces.
-template <bool kBf16, int RT>
-struct ExpandCfg {
-  static constexpr int kCols = RT == 8 || (RT == 4 && !kBf16) ? 32 : 64;
-  static constexpr bool kAhead = RT <= 2;
-  static constexpr int kQuads = kCols / 32, kPairs = RT == 1 ? 1 : RT / 2, kWords = RT == 1 ? 2 : 4;
+// Instruction descriptor, kind::f16: D fp32, A and B bf16, both K-major
+__host__ __device__ constexpr uint32_t idesc_bf16_f32(int m, int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// Many rows of bf16 x. A CTA multiplies one part of K of 128 rows with the A of each
+// of their adapters: D, 128 rows x RP ranks in tensor memory, of 64 values of K a
+// step (x 16 KB and A by TMA); one accumulator after another where there are
+// several adapters (x comes again, from L2), every other one in a CTA of its own.
+// Two CTAs an SM.
+// Warps: 0 producer, 1 MMA issuer, 2..5 epilogue (32 rows each: a row a thread).
+template <int RP>
+struct ShrinkTc {
+  static constexpr int kX = 128 * 128, kA = RP * 128, kRing = RP == 128 ? 3 : 4, kSlots = 2;
+  static constexpr int kCols = kSlots * RP < 32 ? 32 : kSlots * RP;
+  static constexpr size_t kSmem = kRing * (kX + kA) + 1024;
 };
 
-template <bool kBf16, int RT>
-struct ExpandB {
-  using C = ExpandCfg<kBf16, RT>;
-  uint32_t w[C::kQuads][4][C::kPairs][C::kWords];
-  __device__ __forceinline__ void load(const LoraArgs& a, int id, int col0) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint16_t* pb = a.b + (int64_t)id * a.N * a.rank;
-#pragma unroll
-    for (int q = 0; q < C::kQuads; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int n = col0 + q * 32 + 8 * (g >> 1) + 2 * i + (g & 1);
-#pragma unroll
-        for (int p = 0; p < C::kPairs; ++p) {
-          const int r = p * 32 + t * (RT == 1 ? 4 : 8);
-          const bool in = n < a.N && r < a.rank;
-          const uint16_t* from = pb + (int64_t)n * a.rank + r;
-          if constexpr (RT == 1) {
-            const uint2 v = in ? __ldg(reinterpret_cast<const uint2*>(from)) : make_uint2(0, 0);
-            w[q][i][p][0] = v.x;
-            w[q][i][p][1] = v.y;
-          } else {
-            const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(from)) : make_uint4(0, 0, 0, 0);
-            w[q][i][p][0] = v.x;
-            w[q][i][p][1] = v.y;
-            w[q][i][p][2] = v.z;
-            w[q][i][p][3] = v.w;
-          }
+template <int RP>
+__global__ void __launch_bounds__(192, 2)
+    lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
+                          const LoraArgs a, uint32_t* err) {
+  using C = ShrinkTc<RP>;
+  griddep_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[C::kRing], empty[C::kRing], d_full[C::kSlots], d_empty[C::kSlots], drain;
+  __shared__ uint32_t tmem_slot, tmem_busy;
+  uint8_t* sx = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sa = sx + C::kRing * C::kX;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = blockIdx.x;
+  const int64_t m0 = (int64_t)blockIdx.y * 128;
+  const int all = (a.K + 63) / 64, k0 = all * part / kManyParts, k1 = all * (part + 1) / kManyParts;  // steps
+  TileIds T;
+  T.load(a, m0);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], 4);
+    }
+    mbar_init(&drain, 1);
+    tmem_busy = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    if (elect_one()) {
+      tma_prefetch_desc(&tmX);
+      tma_prefetch_desc(&tmA);
+    }
+    __syncwarp();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, C::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  T.find();
+
+  if (warp == 0) {
+    bool ok = true;
+    int s = 0, loads = 0;
+    uint32_t phase = 1;
+    for (int i = blockIdx.z; i < T.count && ok; i += gridDim.z) {
+      const int id = T.at(i);
+      for (int k = k0; k < k1; ++k) {
+        ok = mbar_wait_warp(&empty[s], phase, err);
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&full[s], C::kX + C::kA);
+          tma_load_2d(sx + s * C::kX, &tmX, &full[s], k * 64, (int)m0);
+          tma_load_3d(sa + s * C::kA, &tmA, &full[s], k * 64, 0, id);
         }
+        __syncwarp();
+        ++loads;
+        if (++s == C::kRing) { s = 0; phase ^= 1; }
       }
-  }
-};
-
-// a lane's ranks of a row of h
-template <int kWords>
-__device__ __forceinline__ void load_h(const uint32_t* p, bool in, uint32_t (&v)[kWords]) {
-  if constexpr (kWords == 2) {
-    const uint2 x = in ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
-    v[0] = x.x;
-    v[1] = x.y;
+    }
+    // every load has landed before the CTA exits
+    for (int i = max(0, loads - C::kRing); i < loads; ++i)
+      mbar_wait_warp(&full[i % C::kRing], (uint32_t)(i / C::kRing) & 1u, err);
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, RP);
+    bool ok = true;
+    int s = 0, d = 0;
+    uint32_t phase = 0, phaseD = 1;
+    for (int i = blockIdx.z; i < T.count && ok; i += gridDim.z) {
+      ok = mbar_wait_warp(&d_empty[d], phaseD, err);
+      if (!ok) break;
+      for (int k = k0; k < k1; ++k) {
+        ok = mbar_wait_warp(&full[s], phase, err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t xa = smem_u32(sx + s * C::kX), aa = smem_u32(sa + s * C::kA);
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_f16_ss(tmem + d * RP, smem_desc_sw128(xa + j * 32), smem_desc_sw128(aa + j * 32), idesc,
+                       k > k0 || j > 0);
+          mma_commit(&empty[s]);
+          if (k + 1 == k1) mma_commit(&d_full[d]);
+        }
+        __syncwarp();
+        if (++s == C::kRing) { s = 0; phase ^= 1; }
+      }
+      if (k0 == k1) {
+        if (elect_one()) mma_commit(&d_full[d]);  // (nothing to sum: the epilogue knows)
+        __syncwarp();
+      }
+      if (++d == C::kSlots) { d = 0; phaseD ^= 1; }
+    }
+    if (!ok) {
+      if (elect_one()) mma_commit(&drain);
+      __syncwarp();
+      if (!mbar_wait_warp(&drain, 0, err)) atomicExch(&tmem_busy, 1u);
+    }
   } else {
-    const uint4 x = in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
-    v[0] = x.x;
-    v[1] = x.y;
-    v[2] = x.z;
-    v[3] = x.w;
+    const int quarter = warp & 3;
+    const int64_t m = m0 + quarter * 32 + lane;
+    const int mine = adapter_of(a, m);
+    float4* to = reinterpret_cast<float4*>(a.h + ((int64_t)part * a.M + m) * RP);
+    bool ok = true;
+    int d = 0;
+    uint32_t phaseD = 0;
+    for (int i = blockIdx.z; i < T.count && ok; i += gridDim.z) {
+      const int id = T.at(i);
+      ok = mbar_wait_warp(&d_full[d], phaseD, err);
+      if (!ok) break;
+      if (__any_sync(0xffffffffu, mine == id)) {
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < RP; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + d * RP + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(v[j]));
+          if (mine == id) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              to[c / 4 + j] = k0 == k1 ? make_float4(0, 0, 0, 0)
+                                       : make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                                     __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+          }
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&d_empty[d]);
+      if (++d == C::kSlots) { d = 0; phaseD ^= 1; }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1 && tmem_busy == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
   }
 }
 
-template <bool kBf16, int RT>
-__global__ void __launch_bounds__(32 * kExpandWarps) lora_expand_kernel(const LoraArgs a, const int vec,
-                                                                        const int windows) {
-  using C = ExpandCfg<kBf16, RT>;
-  constexpr int RP = RT * 16, kEs = kBf16 ? 2 : 4;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int col0 = ((int)blockIdx.x * kExpandWarps + warp) * C::kCols;
+// Adds up the parts' sums in order, scales them and splits them into two bf16
+// numbers; a thread four ranks of a row. (Ranks that only pad: 0, also where x is
+// infinite.) Rows without an adapter are left: nothing reads their products.
+__global__ void __launch_bounds__(256) lora_join_kernel(const LoraArgs a) {
+  griddep_launch_dependents();
+  const int fours = a.rp / 4;
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, m = e / fours;
+  const int r = (int)(e - m * fours) * 4, id = adapter_of(a, m);
+  const float scale = id >= 0 && a.scaling ? __ldg(a.scaling + id) : 1.0f;
+  griddep_wait();
+  if (id < 0) return;
+  float4 v = make_float4(0, 0, 0, 0), p[kManyParts];
+#pragma unroll
+  for (int i = 0; i < kManyParts; ++i)
+    p[i] = *reinterpret_cast<const float4*>(a.h + ((int64_t)i * a.M + m) * a.rp + r);
+#pragma unroll
+  for (int i = 0; i < kManyParts; ++i) {
+    v.x += p[i].x;
+    v.y += p[i].y;
+    v.z += p[i].z;
+    v.w += p[i].w;
+  }
+  v = r < a.rank ? make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale) : make_float4(0, 0, 0, 0);
+  const uint2 hi = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+  auto rest = [](float f, float h) { return isfinite(h) ? f - h : 0.0f; };  // (an infinity's would be NaN)
+  const uint2 lo = make_uint2(bf16x2(rest(v.x, bf16_lo(hi.x)), rest(v.y, bf16_hi(hi.x))),
+                              bf16x2(rest(v.z, bf16_lo(hi.y)), rest(v.w, bf16_hi(hi.y))));
+  uint2* to = reinterpret_cast<uint2*>(a.parts) + e;
+  to[0] = hi;
+  to[a.M * fours] = lo;
+}
+
+// Many rows. Bound by reading base and writing out, so both go by TMA, tile by
+// tile (128 rows x 128 bytes), through one ring: the epilogue adds to a tile where
+// it lies in shared memory and stores it from there. A tile's second product is a
+// tcgen05 MMA of 128 rows x kN columns: A operand h (large and small parts, in
+// shared memory as long as the CTA stays with its 128 rows), B operand kN rows of
+// B, into one of four accumulators in tensor memory. Where a tile's rows have
+// several adapters, it is multiplied with each, and every row (a lane of tensor
+// memory, a thread) adds the one that is its own. The tiles, columns fastest, are
+// cut into `sections`, and each of them evenly over the CTAs: shares of some dozen
+// tiles of the same rows, from different places, so that rows of several adapters
+// are everybody's. Rows of base or out that do not lie on
+// 16-byte pieces (`aligned` false) are read and written element by element.
+// Warps: 0 producer, 1 MMA issuer, 2..5 and 6..9 epilogue (32 rows each): a tile's
+// waits, loads, additions and store follow one another, so the two sets take turns.
+template <bool kBf16, int kHalves>  // 64 ranks each
+struct ExpandMany {
+  static constexpr int kN = kBf16 ? 64 : 32;  // columns of a tile: 128 bytes of a row
+  static constexpr int kBase = 128 * 128, kB = kN * 128 * kHalves, kH = 128 * 128;
+  static constexpr int kBaseRing = kHalves == 2 ? 7 : 8, kBRing = kHalves == 2 ? 3 : 4, kSlots = 4;
+  static constexpr int kHBytes = 2 * kHalves * kH, kHRing = kHalves == 2 ? 1 : 2;
+  static constexpr int kThreads = 64 + 32 * 8;
+  static constexpr size_t kSmem = kBaseRing * kBase + kBRing * kB + kHRing * kHBytes + 1024;
+};
+
+template <bool kBf16, int kHalves>
+__global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
+    lora_expand_many_kernel(const __grid_constant__ CUtensorMap tmBase, const __grid_constant__ CUtensorMap tmB,
+                            const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmH, const LoraArgs a,
+                            const int aligned, const int sections, uint32_t* err) {
+  using C = ExpandMany<kBf16, kHalves>;
+  constexpr int kN = C::kN;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t base_full[C::kBaseRing], base_empty[C::kBaseRing];
+  __shared__ uint64_t b_full[C::kBRing], b_empty[C::kBRing], d_full[C::kSlots], d_empty[C::kSlots], drain;
+  __shared__ uint64_t h_full[C::kHRing], h_empty[C::kHRing];
+  __shared__ uint32_t tmem_slot, tmem_busy;
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sx = base;                                  // tiles of base [slot]
+  uint8_t* sb = sx + C::kBaseRing * C::kBase;          // B [slot][half]
+  uint8_t* sh = sb + C::kBRing * C::kB;                // h [slot][large, small][half]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int CT = (a.N + kN - 1) / kN;
+  const int64_t tiles = (a.M + 127) / 128 * CT, cells = (int64_t)sections * gridDim.x;
   const bool keep = a.base == a.out && a.ldb == a.ldo;  // rows without an adapter are in place
-  bool waited = false;
-  if (col0 < a.N) {
-    int64_t m0 = (int64_t)blockIdx.y * windows * 32;
-    const int64_t end = min(m0 + (int64_t)windows * 32, a.M);
-    LoraPieces pieces(a, m0, 32);
-    int number = 0;
-    // the next piece, of this window or a later one
-    auto advance = [&](int64_t& m, int& id, uint32_t& rows) {
-      for (;;) {
-        while (pieces.next(number, blockIdx.z, gridDim.z, id, rows))
-          if (id >= 0 || !keep) {
-            m = m0;
-            return true;
-          }
-        m0 += 32;
-        if (m0 >= end) return false;
-        pieces = LoraPieces(a, m0, 32);
-        number = 0;
-      }
-    };
-    int id, id_next, held = -1;
-    int64_t m, m_next;
-    uint32_t rows, rows_next;
-    ExpandB<kBf16, RT> b, b_next;
-    bool more = advance(m, id, rows);
-    if (more && id >= 0) {
-      b.load(a, id, col0);
-      held = id;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kBaseRing; ++i) {
+      mbar_init(&base_full[i], 1);
+      mbar_init(&base_empty[i], 4);
     }
-    while (more) {
-      more = advance(m_next, id_next, rows_next);
-      if (C::kAhead && more && id_next >= 0 && id_next != held) b_next.load(a, id_next, col0);
-      const int count = __popc(rows);
+    for (int i = 0; i < C::kBRing; ++i) {
+      mbar_init(&b_full[i], 1);
+      mbar_init(&b_empty[i], 1);
+    }
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], 4);
+    }
+    for (int i = 0; i < C::kHRing; ++i) {
+      mbar_init(&h_full[i], 1);
+      mbar_init(&h_empty[i], 1);
+    }
+    mbar_init(&drain, 1);
+    tmem_busy = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    if (elect_one()) {
+      tma_prefetch_desc(&tmBase);
+      tma_prefetch_desc(&tmB);
+      tma_prefetch_desc(&tmOut);
+    }
+    __syncwarp();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, C::kSlots * kN);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  // the CTA's tiles, those of the same rows together: their first row, their
+  // adapters, the tiles of columns c0 up to c1. Rows that have no adapter and are in
+  // place are passed over. (The next rows' ids are on their way.)
+  TileIds T, ahead;
+  int64_t cell = blockIdx.x, next = tiles * cell / cells, end = tiles * (cell + 1) / cells, m0 = 0;
+  int c0 = 0, c1 = 0, mine = -1;  // mine: of row 32 (warp % 4) + lane
+  auto skip_empty = [&]() {  // to the next cell while this one is done
+    while (next >= end && cell + gridDim.x < cells) {
+      cell += gridDim.x;
+      next = tiles * cell / cells;
+      end = tiles * (cell + 1) / cells;
+    }
+    return next < end;
+  };
+  if (skip_empty()) ahead.load(a, next / CT * 128);
+  auto advance = [&]() {
+    while (skip_empty()) {
+      const int64_t rt = next / CT, stop = min(end, (rt + 1) * CT);
+      m0 = rt * 128;
+      c0 = (int)(next - rt * CT);
+      c1 = (int)(stop - rt * CT);
+      next = stop;
+      T = ahead;
+      if (skip_empty()) ahead.load(a, next / CT * 128);
+      mine = (warp & 3) == 0 ? T.v[0] : (warp & 3) == 1 ? T.v[1] : (warp & 3) == 2 ? T.v[2] : T.v[3];
+      T.find();
+      if (T.count || !keep) return true;
+    }
+    return false;
+  };
+
+  if (warp == 0) {
+    bool ok = true;
+    int s = 0, sB = 0, sH = 0, loads = 0, loadsB = 0, loadsH = 0;
+    uint32_t phase = 1, phaseB = 1, phaseH = 1;
+    griddep_wait();
+    while (ok && advance()) {
+      if (T.count) {
+        ok = mbar_wait_warp(&h_empty[sH], phaseH, err);
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&h_full[sH], C::kHBytes);
 #pragma unroll
-      for (int tile = 0; tile < 2; ++tile) {
-        if (16 * tile >= count) break;
-        int row[2];  // this lane's rows of the piece: numbers g and g + 8 of the tile
-        Cols8<kBf16> raw[C::kQuads][2];
+          for (int o = 0; o < 2; ++o)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int n = 16 * tile + g + 8 * h;
-          row[h] = n < count ? nth_bit(rows, n) : -1;
-#pragma unroll
-          for (int q = 0; q < C::kQuads; ++q) {
-            const int n0 = col0 + q * 32 + 8 * t;
-            if (row[h] >= 0)
-              raw[q][h].load(reinterpret_cast<const char*>(a.base) + ((m + row[h]) * a.ldb + n0) * kEs, a.N - n0, vec);
+            for (int h = 0; h < kHalves; ++h)
+              tma_load_3d(sh + sH * C::kHBytes + (o * kHalves + h) * C::kH, &tmH, &h_full[sH], h * 64, (int)m0, o);
+        }
+        __syncwarp();
+        ++loadsH;
+        if (++sH == C::kHRing) { sH = 0; phaseH ^= 1; }
+      }
+      for (int c = c0; c < c1 && ok; ++c) {
+        if (aligned) {
+          ok = mbar_wait_warp(&base_empty[s], phase, err);
+          if (!ok) break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&base_full[s], C::kBase);
+            tma_load_2d(sx + s * C::kBase, &tmBase, &base_full[s], c * kN, (int)m0);
           }
+          __syncwarp();
+          ++loads;
+          if (++s == C::kBaseRing) { s = 0; phase ^= 1; }
         }
-        if (!waited) {  // (nothing above is shrink's work; out may be what a kernel before it reads)
-          griddep_wait();
-          waited = true;
+        for (int k = 0; k < T.count; ++k) {
+          const int id = T.at(k);
+          ok = mbar_wait_warp(&b_empty[sB], phaseB, err);
+          if (!ok) break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&b_full[sB], C::kB);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+              tma_load_3d(sb + sB * C::kB + h * kN * 128, &tmB, &b_full[sB], h * 64, c * kN, id);
+          }
+          __syncwarp();
+          ++loadsB;
+          if (++sB == C::kBRing) { sB = 0; phaseB ^= 1; }
         }
-        if (id >= 0) {  // (a row without an adapter keeps base's bits)
-          float acc[C::kQuads][4][4];
+      }
+    }
+    // every load has landed before the CTA exits
+    for (int i = max(0, loadsH - C::kHRing); i < loadsH; ++i)
+      mbar_wait_warp(&h_full[i % C::kHRing], (uint32_t)(i / C::kHRing) & 1u, err);
+    for (int i = max(0, loads - C::kBaseRing); i < loads; ++i)
+      mbar_wait_warp(&base_full[i % C::kBaseRing], (uint32_t)(i / C::kBaseRing) & 1u, err);
+    for (int i = max(0, loadsB - C::kBRing); i < loadsB; ++i)
+      mbar_wait_warp(&b_full[i % C::kBRing], (uint32_t)(i / C::kBRing) & 1u, err);
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, kN);
+    const int steps = (a.rank + 15) / 16;
+    bool ok = true;
+    int sB = 0, d = 0, sH = 0;
+    uint32_t phaseB = 0, phaseD = 1, phaseH = 0;
+    while (ok && advance()) {
+      if (!T.count) continue;
+      ok = mbar_wait_warp(&h_full[sH], phaseH, err);
+      const uint32_t ha = smem_u32(sh + sH * C::kHBytes);
+      for (int c = c0; c < c1 && ok; ++c)
+        for (int i = 0; i < T.count; ++i) {
+          ok = mbar_wait_warp2(&b_full[sB], phaseB, &d_empty[d], phaseD, err);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ba = smem_u32(sb + sB * C::kB);
+          if (elect_one()) {
+            for (int o = 1; o >= 0; --o)  // the small parts first
+              for (int k = 0; k < steps; ++k)
+                mma_f16_ss(tmem + d * kN, smem_desc_sw128(ha + (o * kHalves + (k >> 2)) * C::kH + (k & 3) * 32),
+                           smem_desc_sw128(ba + (k >> 2) * kN * 128 + (k & 3) * 32), idesc, o == 0 || k > 0);
+            mma_commit(&d_full[d]);
+            mma_commit(&b_empty[sB]);
+            if (c + 1 == c1 && i + 1 == T.count) mma_commit(&h_empty[sH]);
+          }
+          __syncwarp();
+          if (++sB == C::kBRing) { sB = 0; phaseB ^= 1; }
+          if (++d == C::kSlots) { d = 0; phaseD ^= 1; }
+        }
+      if (++sH == C::kHRing) { sH = 0; phaseH ^= 1; }
+    }
+    // (after a wait that gave up, MMAs issued so far may still run; bounded)
+    if (!ok) {
+      if (elect_one()) mma_commit(&drain);
+      __syncwarp();
+      if (!mbar_wait_warp(&drain, 0, err)) atomicExch(&tmem_busy, 1u);
+    }
+  } else {
+    const int quarter = warp & 3;
+    const uint32_t set = (warp - 2) >> 2;
+    bool ok = true;
+    int last = -1;
+    uint32_t* const stage = reinterpret_cast<uint32_t*>(sx) + set * 128 * (kN + 1);  // (not `aligned`)
+    uint32_t n = 0, units = 0;  // tiles, and products of a tile with one adapter, so far
+    griddep_wait();  // (out may be what a kernel before reads, too)
+    while (ok && advance()) {
+      const int64_t w0 = m0 + quarter * 32;
+      for (int c = c0; c < c1 && ok; ++c, ++n) {
+        if ((n & 1) != set) {
+          units += T.count;
+          continue;
+        }
+        const uint32_t s = n % C::kBaseRing;
+        if (aligned) ok = mbar_wait_warp(&base_full[s], n / C::kBaseRing & 1, err);
+        if (!ok) break;
+        uint8_t* const row = sx + s * C::kBase + (quarter * 32 + lane) * 128;
+        for (int k = 0; k < T.count; ++k, ++units) {
+          const int id = T.at(k);
+          const uint32_t d = units % C::kSlots;
+          ok = mbar_wait_warp(&d_full[d], units / C::kSlots & 1, err);
+          if (!ok) break;
+          if (__any_sync(0xffffffffu, mine == id)) {
+            tc_fence_after();
+            uint32_t v[kN / 32][32];
 #pragma unroll
-          for (int q = 0; q < C::kQuads; ++q)
+            for (int i = 0; i < kN / 32; ++i)
+              tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + d * kN + i * 32, v[i]);
+            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < kN / 32; ++i)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) acc[q][i][c] = 0.0f;
+              for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(v[i][j]));
+            tc_fence_before();
+            if (mine == id && !aligned) {
+              // the products alone, as they will be read: row after row, a word on
+              // from row to row
 #pragma unroll
-          for (int p = 0; p < C::kPairs; ++p) {
-            uint32_t h[2][2][C::kWords];  // [large, small parts][row]
+              for (int i = 0; i < kN; ++i)
+                stage[(quarter * 32 + lane) * (kN + 1) + i] = v[i / 32][i % 32];
+            } else if (mine == id) {  // (a row without an adapter keeps base's bits)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t* ph = a.h + (m + row[i]) * RP + (p * 32 + t * 2 * C::kWords) / 2;
-              load_h(ph, row[i] >= 0, h[0][i]);
-              load_h(ph + RP / 2, row[i] >= 0, h[1][i]);
+              for (int i = 0; i < 8; ++i) {
+                uint4* p = reinterpret_cast<uint4*>(row + ((i ^ (lane & 7)) * 16));
+                uint4 x = *p;
+                if constexpr (kBf16) {
+                  auto add = [&](uint32_t u, int j) {
+                    return bf16x2(bf16_lo(u) + __uint_as_float(v[j / 32][j % 32]),
+                                  bf16_hi(u) + __uint_as_float(v[(j + 1) / 32][(j + 1) % 32]));
+                  };
+                  x = make_uint4(add(x.x, 8 * i), add(x.y, 8 * i + 2), add(x.z, 8 * i + 4), add(x.w, 8 * i + 6));
+                } else {
+                  auto add = [&](uint32_t u, int j) {
+                    return __float_as_uint(__uint_as_float(u) + __uint_as_float(v[0][j]));
+                  };
+                  x = make_uint4(add(x.x, 4 * i), add(x.y, 4 * i + 1), add(x.z, 4 * i + 2), add(x.w, 4 * i + 3));
+                }
+                *p = x;
+              }
             }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&d_empty[d]);
+        }
+        if (!ok) break;
+        if (!aligned) {
+          // base and out in whole rows of the tile, element by element
+          __syncwarp();
+          const uint32_t with = __ballot_sync(0xffffffffu, mine >= 0);
+          const int rows = (int)min((int64_t)32, a.M - w0);
+#pragma unroll 1
+          for (int r0 = 0; r0 < rows; r0 += 8) {
+            uint32_t x[8][kN / 32];
 #pragma unroll
-            for (int k = 0; k < C::kWords / 2; ++k)
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
-              for (int o = 1; o >= 0; --o) {
-                const uint32_t f[4] = {h[o][0][2 * k], h[o][1][2 * k], h[o][0][2 * k + 1], h[o][1][2 * k + 1]};
+              for (int j = 0; j < kN / 32; ++j) {
+                const int n = c * kN + j * 32 + lane;
+                x[i][j] = r0 + i < rows && n < a.N ? load_raw<kBf16>(a.base, (w0 + r0 + i) * a.ldb + n) : 0;
+              }
 #pragma unroll
-                for (int q = 0; q < C::kQuads; ++q)
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    mma_bf16_16816(acc[q][i], f, b.w[q][i][p][2 * k], b.w[q][i][p][2 * k + 1]);
+              for (int j = 0; j < kN / 32; ++j) {
+                const int n = c * kN + j * 32 + lane;
+                if (r0 + i >= rows || n >= a.N) continue;
+                const bool has = with >> (r0 + i) & 1;
+                if (has)
+                  x[i][j] = add_raw<kBf16>(
+                      x[i][j], __uint_as_float(stage[(quarter * 32 + r0 + i) * (kN + 1) + j * 32 + lane]));
+                if (has || !keep) store_raw<kBf16>(a.out, (w0 + r0 + i) * a.ldo + n, x[i][j]);
               }
           }
-#pragma unroll
-          for (int q = 0; q < C::kQuads; ++q)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) raw[q][h].add(i, acc[q][i][2 * h], acc[q][i][2 * h + 1]);
+          __syncwarp();
+          continue;
         }
-#pragma unroll
-        for (int q = 0; q < C::kQuads; ++q)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int n0 = col0 + q * 32 + 8 * t;
-            if (row[h] >= 0)
-              raw[q][h].store(reinterpret_cast<char*>(a.out) + ((m + row[h]) * a.ldo + n0) * kEs, a.N - n0, vec);
-          }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (w0 < a.M) tma_store_2d(&tmOut, sx + s * C::kBase + quarter * 4096, c * kN, (int)w0);
+          bulk_commit_group();
+          // the slot before this one goes back when its store has read it
+          asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          if (last >= 0) mbar_arrive(&base_empty[last]);
+        }
+        last = (int)s;
       }
-      if (more && id_next >= 0 && id_next != held) {
-        if (C::kAhead) b = b_next;
-        else b.load(a, id_next, col0);
-        held = id_next;
-      }
-      id = id_next;
-      m = m_next;
-      rows = rows_next;
     }
+    if (lane == 0) bulk_wait_all();
   }
-  // (this kernel's end stands for shrink's, too)
-  if (!waited) griddep_wait();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1 && tmem_busy == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kSlots * kN);
+  }
 }
 
-template <bool kBf16, int RT>
-static cudaError_t launch_shrink(const LoraArgs& a, cudaStream_t st) {
-  if (a.M > 128) {
-    const int64_t windows = ceil_div(a.M, 32);
-    // with few windows several clusters share the pieces of one
-    int64_t z = 4 * num_sms() / (windows * kGroups);
-    z = z < 1 ? 1 : z > 32 ? 32 : z;
-    auto kern = lora_shrink_many_kernel<kBf16, RT>;
+template <int RT>
+static cudaError_t launch_shrink_many(const LoraArgs& a, bool x_bf16, uint32_t* err, cudaStream_t st) {
+  if (x_bf16) {
+    constexpr int RP = RT * 16;
+    using C = ShrinkTc<RP>;
+    static_assert(C::kSmem <= 113 * 1024, "shared memory of two CTAs");
+    CUtensorMap tx, ta;
+    if (!make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.K, a.M, a.ldx * 2, 64, 128,
+                      CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tmap_3d(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.a, a.K, a.rank, a.count, (int64_t)a.K * 2,
+                      (int64_t)a.rank * a.K * 2, 64, RP, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorNotSupported;
+    auto kern = lora_shrink_tc_kernel<RP>;
     static std::atomic<uint64_t> attr_set{0};
-    const cudaError_t e = smem_attr_once_per_device(kern, ManyCfg<kBf16, RT>::kSmem, attr_set);
+    const cudaError_t e = smem_attr_once_per_device(kern, (int)C::kSmem, attr_set);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(kGroups, (unsigned)windows, (unsigned)z), 32 * kManyWarps, ManyCfg<kBf16, RT>::kSmem, st>>>(a);
+    kern<<<dim3(kManyParts, (unsigned)ceil_div(a.M, 128), 2), 192, C::kSmem, st>>>(tx, ta, a, err);
     return cudaGetLastError();
   }
-  const int windows = (int)ceil_div(a.M, 8), most = a.M < 8 ? (int)a.M : 8;
-  lora_shrink_few_kernel<kBf16, RT><<<dim3(kGroups, windows, most), 32 * kShares, 0, st>>>(a);
+  const int64_t windows = ceil_div(a.M, 32);
+  // with few windows several CTAs share the pieces of one
+  int64_t z = 4 * num_sms() / (windows * kManyParts);
+  z = z < 1 ? 1 : z > 32 ? 32 : z;
+  auto kern = lora_shrink_many_kernel<RT>;
+  static std::atomic<uint64_t> attr_set{0};
+  const cudaError_t e = smem_attr_once_per_device(kern, ManyCfg<RT>::kSmem, attr_set);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(kManyParts, (unsigned)windows, (unsigned)z), 32 * kManyWarps, ManyCfg<RT>::kSmem, st>>>(a);
   return cudaGetLastError();
 }
 
-template <bool kXBf16, bool kBf16, int RT>
-static cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st) {
-  const cudaError_t e = launch_shrink<kXBf16, RT>(a, st);
-  if (e != cudaSuccess) return e;
+template <bool kBf16, int kHalves>
+static cudaError_t launch_expand_many(const LoraArgs& a, uint32_t* err, cudaStream_t st) {
+  using C = ExpandMany<kBf16, kHalves>;
+  static_assert(C::kSmem <= 227 * 1024 && C::kBaseRing * C::kBase >= 2 * 128 * (C::kN + 1) * 4, "shared memory per CTA");
   constexpr int es = kBf16 ? 2 : 4;
+  const auto type = kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   auto at16 = [](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * es)) % 16 == 0; };
-  const int vec = at16(a.base, a.ldb) && at16(a.out, a.ldo);
-  const int64_t gx = ceil_div(a.N, ExpandCfg<kBf16, RT>::kCols * kExpandWarps), all = ceil_div(a.M, 32);
-  // four windows to a CTA where that leaves enough CTAs (they read the same rows
-  // of B); with few windows their pieces are dealt out
-  const int windows = gx * all >= 32 * num_sms() ? 4 : 1;
-  const int64_t gy = ceil_div(all, windows);
-  int64_t gz = 4 * num_sms() / (gx * gy);
-  gz = gz < 1 ? 1 : gz > 32 ? 32 : gz;
-  gz = gz < a.M ? gz : a.M;
-  return launch_kernel(lora_expand_kernel<kBf16, RT>, dim3((unsigned)gx, (unsigned)gy, (unsigned)gz),
-                       dim3(32 * kExpandWarps), 0, st, true, a, vec, windows);
+  // (a TMA store clips a row at 16-byte granularity: where a row does not end on
+  // such a boundary it would overwrite what lies behind it)
+  const bool aligned = at16(a.base, a.ldb) && at16(a.out, a.ldo) && (int64_t)a.N * es % 16 == 0;
+  CUtensorMap tx, tb, to, th;
+  memset(&tx, 0, sizeof(tx));
+  memset(&to, 0, sizeof(to));
+  if ((aligned &&
+       (!make_tmap_2d(&tx, type, a.base, a.N, a.M, a.ldb * es, C::kN, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tmap_2d(&to, type, a.out, a.N, a.M, a.ldo * es, C::kN, 32, CU_TENSOR_MAP_SWIZZLE_128B))) ||
+      !make_tmap_3d(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.b, a.rank, a.N, a.count, (int64_t)a.rank * 2,
+                    (int64_t)a.N * a.rank * 2, 64, C::kN, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_3d(&th, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.parts, a.rp, a.M, 2, (int64_t)a.rp * 2,
+                    a.M * a.rp * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorNotSupported;
+  auto kern = lora_expand_many_kernel<kBf16, kHalves>;
+  static std::atomic<uint64_t> attr_set{0};
+  const cudaError_t e = smem_attr_once_per_device(kern, (int)C::kSmem, attr_set);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ceil_div(a.M, 128) * ceil_div(a.N, C::kN), ctas = tiles < num_sms() ? tiles : num_sms();
+  int64_t sections = tiles / (ctas * 12);
+  sections = sections < 1 ? 1 : sections > 8 ? 8 : sections;
+  return launch_kernel(kern, dim3((unsigned)ctas), dim3(C::kThreads), C::kSmem, st, true, tx, tb, to, th, a,
+                       (int)aligned, (int)sections, err);
 }
 
-template <bool kXBf16, bool kBf16>
-static cudaError_t launch_lora_any(const LoraArgs& a, cudaStream_t st) {
-  if (a.rank <= 16) return launch_lora<kXBf16, kBf16, 1>(a, st);
-  if (a.rank <= 32) return launch_lora<kXBf16, kBf16, 2>(a, st);
-  if (a.rank <= 64) return launch_lora<kXBf16, kBf16, 4>(a, st);
-  return launch_lora<kXBf16, kBf16, 8>(a, st);
+template <bool kBf16, int C>
+static cudaError_t launch_expand_few(const LoraArgs& a, uint32_t* err, cudaStream_t st) {
+  const size_t smem = (size_t)(kExpandWarps * kExpandRing * 32 * C * 2 + kFewRows * 4) * a.rank;
+  auto kern = lora_expand_few_kernel<kBf16, C>;
+  static std::atomic<uint64_t> attr_set{0};
+  const cudaError_t e = smem_attr_once_per_device(kern, (kExpandWarps * kExpandRing * 64 + kFewRows * 4) * 128, attr_set);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3((unsigned)ceil_div(a.N, kExpandWarps * 32 * C), (unsigned)ceil_div(a.M, kFewRows)),
+                       dim3(32 * kExpandWarps), smem, st, true, a, err);
 }
 
-// ranks that a row of the workspace holds
-int lora_padded_rank(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+template <bool kBf16>
+static cudaError_t launch_shrink_few(const LoraArgs& a, cudaStream_t st) {
+  const dim3 grid((unsigned)few_parts(a.K), (unsigned)a.M);
+  const int r = (a.rank + kFewWarps - 1) / kFewWarps;  // ranks a warp
+  if (r <= 1) lora_shrink_few_kernel<kBf16, 1><<<grid, 32 * kFewWarps, 0, st>>>(a);
+  else if (r <= 2) lora_shrink_few_kernel<kBf16, 2><<<grid, 32 * kFewWarps, 0, st>>>(a);
+  else if (r <= 4) lora_shrink_few_kernel<kBf16, 4><<<grid, 32 * kFewWarps, 0, st>>>(a);
+  else if (r <= 8) lora_shrink_few_kernel<kBf16, 8><<<grid, 32 * kFewWarps, 0, st>>>(a);
+  else lora_shrink_few_kernel<kBf16, 16><<<grid, 32 * kFewWarps, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+static int64_t padded(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+
+// bytes of the parts' sums of M rows; with many rows, of their two parts before them
+int64_t lora_workspace(int64_t M, int64_t K, int64_t rank) {
+  if (M <= kLoraFew) return few_parts((int)K) * M * rank * 4;
+  return (kManyParts * 4 + 4) * M * padded(rank);
+}
 
 cudaError_t launch_add_lora(const void* base, bool bf16, int64_t ldb, const void* x, bool x_bf16, int64_t M,
                             int64_t K, int64_t ldx, const void* A, const void* B, int64_t count, int64_t rank,
                             int64_t N, const int64_t* ids, const float* scaling, void* out, int64_t ldo, void* ws,
-                            cudaStream_t st) {
-  const LoraArgs a{x, reinterpret_cast<const uint16_t*>(A), reinterpret_cast<const uint16_t*>(B), ids, scaling, base,
-                   out, reinterpret_cast<uint32_t*>(ws), ldx, ldb, ldo, M, (int)K, (int)N, (int)rank, (int)count};
-  if (x_bf16) return bf16 ? launch_lora_any<true, true>(a, st) : launch_lora_any<true, false>(a, st);
-  return bf16 ? launch_lora_any<false, true>(a, st) : launch_lora_any<false, false>(a, st);
+                            uint32_t* err, cudaStream_t st) {
+  LoraArgs a{x, reinterpret_cast<const uint16_t*>(A), reinterpret_cast<const uint16_t*>(B), ids, scaling, base,
+             out, reinterpret_cast<float*>(ws), reinterpret_cast<uint32_t*>(ws), ldx, ldb, ldo, M, (int)K, (int)N,
+             (int)rank, (int)count, (int)rank};
+  if (M <= kLoraFew) {
+    const cudaError_t e = x_bf16 ? launch_shrink_few<true>(a, st) : launch_shrink_few<false>(a, st);
+    if (e != cudaSuccess) return e;
+    if (rank <= 32) return bf16 ? launch_expand_few<true, 2>(a, err, st) : launch_expand_few<false, 2>(a, err, st);
+    return bf16 ? launch_expand_few<true, 1>(a, err, st) : launch_expand_few<false, 1>(a, err, st);
+  }
+  a.rp = (int)padded(rank);
+  a.h += M * a.rp;  // (behind the two parts, 2 bytes a rank each)
+  cudaError_t e = a.rp == 16   ? launch_shrink_many<1>(a, x_bf16, err, st)
+                  : a.rp == 32 ? launch_shrink_many<2>(a, x_bf16, err, st)
+                  : a.rp == 64 ? launch_shrink_many<4>(a, x_bf16, err, st)
+                               : launch_shrink_many<8>(a, x_bf16, err, st);
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(lora_join_kernel, dim3((unsigned)ceil_div(M * (a.rp / 4), 256)), dim3(256), 0, st, true, a);
+  if (e != cudaSuccess) return e;
+  if (rank <= 64) return bf16 ? launch_expand_many<true, 1>(a, err, st) : launch_expand_many<false, 1>(a, err, st);
+  return bf16 ? launch_expand_many<true, 2>(a, err, st) : launch_expand_many<false, 2>(a, err, st);
 }
 
 }  // namespace qg

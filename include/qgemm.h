@@ -411,14 +411,14 @@ qg_status qg_gemm_fp8_grouped(const uint8_t* q, const float* scale, int64_t lds,
 /*   a, b     bf16 [adapters][rank][K], [adapters][N][rank], 16-byte aligned;      */
 /*            adapters of a smaller rank are filled up with zeros.                  */
 /*   ids      [M] int64; scaling [adapters] fp32, or NULL for 1.                    */
-/*   workspace  qg_add_lora_workspace_bytes(M, rank) bytes (0: invalid sizes),      */
+/*   workspace  qg_add_lora_workspace_bytes(M, K, rank) bytes (0: invalid sizes),   */
 /*            256-byte aligned, owned by the caller; calls that may run at once      */
 /*            need one each.                                                         */
 /* K % 16 == 0, K <= 65536; rank % 8 == 0, 8 <= rank <= QG_LORA_MAX_RANK;            */
 /* 1 <= M <= 2^20, 1 <= N <= 2^24, 1 <= adapters <= 2^20.                            */
 /* ------------------------------------------------------------------------ */
 #define QG_LORA_MAX_RANK 128
-size_t qg_add_lora_workspace_bytes(int64_t M, int64_t rank);
+size_t qg_add_lora_workspace_bytes(int64_t M, int64_t K, int64_t rank);
 qg_status qg_add_lora(const void* base, qg_dtype dtype, int64_t ldb, const void* x, qg_dtype x_dtype,
                       int64_t M, int64_t K, int64_t ldx, const uint16_t* a, const uint16_t* b,
                       int64_t adapters, int64_t rank, int64_t N, const int64_t* ids,

@@ -1,11 +1,14 @@
 """GPU tests of the low-rank adapters against 64 bits.
 
-Bound. h: a warp's share of K goes through 2 * ceil(ceil(K/32) / 64) MMAs (three times
-that for fp32 x), each adding 16 exact products to its sum, every addition off by at
-most one unit, 2^-23 of the sum of |terms|; then 16 sums in fp32. scaling * h: 2^-24, and
-2^-17 for its two bf16 parts. The second product likewise: 2 * ceil(rank / 16) MMAs of
-16. The sum with base rounds once to fp32 and once to the output: half a step,
-2^-8 (bf16) or 2^-24.
+Bound: every addition of products in fp32 is off by at most one unit, 2^-23 of the sum
+of |terms|, so a chain of c of them by c * 2^-23.
+h, more than 128 rows of bf16: one of eight parts of K, in steps of 64, then 8 sums. Of
+fp32: one of 64 shares of K, in steps of 32 with three products a value, then 16 sums.
+Up to 128 rows: 64 products a lane at most (K in parts of 1024, K / 1024 of them), 5 sums
+of lanes and K / 1024 of parts.
+scaling * h: 2^-24, and 2^-17 for its two bf16 parts. The second product: twice rank up
+to 16 products. The sum with base rounds once to fp32 and once to the output: half a
+step, 2^-8 (bf16) or 2^-24.
 """
 import pytest
 import torch
@@ -41,9 +44,14 @@ def inputs(seed, m, k, n, rank, count, x=BF16, out=BF16, pad=0):
 
 
 def check(got, base, x, a, b, ids, scaling):
-    k, rank, count = x.shape[1], a.shape[1], a.shape[0]
-    mmas = 2 * -(-(-(-k // 32)) // 64) * (1 if x.dtype == BF16 else 3)
-    c1, c2 = 16 * mmas + 16, 2 * 16 * -(-rank // 16)
+    m, k, rank, count = x.shape[0], x.shape[1], a.shape[1], a.shape[0]
+    if m <= 128:
+        c1 = 64 + 5 + -(-k // 1024)
+    elif x.dtype == BF16:
+        c1 = 64 * -(-(-(-k // 64)) // 8) + 8
+    else:
+        c1 = 3 * 32 * -(-(-(-k // 32)) // 64) + 16
+    c2 = 2 * 16 * -(-rank // 16)
     half = 2.0 ** -8 if got.dtype == BF16 else 2.0 ** -24
     assert got.shape == base.shape and got.dtype == base.dtype
     for i in range(-1, count):
@@ -99,14 +107,38 @@ def test_strides_and_in_place(n):
 
 @pytest.mark.parametrize("x", [BF16, F32])
 def test_bits_of_a_row_do_not_depend_on_the_others(x):
-    base, xs, a, b, ids, scaling = inputs(1, 500, 1296, 300, 24, 6, x)
-    want = qg.add_lora(base, xs, a, b, ids, scaling)
-    for rows in (slice(7, 8), slice(30, 70), slice(3, 499)):
-        got = qg.add_lora(base[rows], xs[rows], a, b, ids[rows].contiguous(), scaling)
-        assert torch.equal(got, want[rows])
-    turn = torch.randperm(500, device=DEV)
-    got = qg.add_lora(base[turn], xs[turn], a, b, ids[turn], scaling)
-    assert torch.equal(got, want[turn])
+    # (of calls of up to 128 rows, and of calls of more)
+    base, xs, a, b, ids, scaling = inputs(1, 500, 1296, 304, 24, 6, x)
+    for many in (False, True):
+        last = 500 if many else 128
+        want = qg.add_lora(base[:last], xs[:last], a, b, ids[:last], scaling)
+        for rows in (slice(3, 499), slice(100, 400)) if many else (slice(7, 8), slice(30, 70)):
+            got = qg.add_lora(base[rows], xs[rows], a, b, ids[rows].contiguous(), scaling)
+            assert torch.equal(got, want[rows])
+        turn = torch.randperm(last, device=DEV)
+        got = qg.add_lora(base[turn], xs[turn], a, b, ids[turn], scaling)
+        assert torch.equal(got, want[turn])
+
+
+@pytest.mark.parametrize("x,out,rank", [(BF16, BF16, 64), (BF16, F32, 128), (F32, BF16, 8), (BF16, BF16, 72)])
+@pytest.mark.parametrize("m,n", [(129, 64), (200, 1000), (384, 5120), (1000, 328), (2049, 136)])
+def test_many_rows(m, n, x, out, rank):
+    # runs of rows, some without an adapter; a tile of rows of one adapter, of several, of none
+    base, xs, a, b, ids, scaling = inputs(m + n, m, 528, n, rank, 9, x, out)
+    runs = torch.randint(-2, 9, (m // 60 + 1,), device=DEV).repeat_interleave(60)[:m].contiguous()
+    for which in (runs, ids, torch.full_like(ids, 3), torch.full_like(ids, -1)):
+        got = qg.add_lora(base, xs, a, b, which, scaling)
+        check(got, base, xs, a, b, which.clamp(min=-1), scaling)
+        mine = base.clone()
+        assert qg.add_lora(mine, xs, a, b, which, scaling, out=mine) is mine
+        assert torch.equal(mine, got)
+
+
+def test_many_rows_of_many_adapters():
+    # more adapters in 128 rows than accumulators or slots
+    base, xs, a, b, _, scaling = inputs(8, 300, 272, 200, 16, 128)
+    ids = torch.arange(300, device=DEV) * 37 % 128
+    check(qg.add_lora(base, xs, a, b, ids, scaling), base, xs, a, b, ids, scaling)
 
 
 def test_rows_without_an_adapter_keep_their_bits():
