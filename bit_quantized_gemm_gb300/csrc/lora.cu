@@ -4,8 +4,8 @@
 //   out[m][n] = base[m][n] + sum_r (scaling[id] * h[m][r]) * B[id][n][r]
 // A row whose id is not one of the adapters keeps base's bits.
 //
-// `shrink` leaves h as sums over parts of K, which are added up in order and
-// scaled; `expand` adds the second product to base. The parts are cut by K alone,
+// `shrink` sums h over parts of K, which are added up in order and scaled; `expand`
+// adds the second product to base. The parts are cut by K alone,
 // so a row's bits do not depend on the other rows, but for the choice of the kernels:
 //   up to 128 rows (decode), bound by reading the adapters that the rows use: a
 //   row at a time on the fp32 units, a few products for every value read;
@@ -40,8 +40,8 @@ struct LoraArgs {
   const float* scaling;   // [count] or null
   const void* base;
   void* out;
-  float* h;               // [parts][M][rp], rp ranks a row (many rows: up to 16, 32, 64 or 128)
-  uint32_t* parts;        // many rows: scaling * h as [large, small parts][M][rp / 2] pairs of bf16
+  float* h;               // sums [part of K][M][rp], rp ranks a row (many rows: up to 16, 32, 64 or 128)
+  uint32_t* parts;        // many rows: scaling * h as [large, small numbers][M][rp / 2] pairs of bf16
   int64_t ldx, ldb, ldo, M;
   int K, N, rank, count, rp;
 };
@@ -375,7 +375,7 @@ struct ManyCfg {
 };
 
 template <int RT>
-__global__ void __launch_bounds__(32 * kManyWarps) lora_shrink_many_kernel(const LoraArgs a) {
+__global__ void __launch_bounds__(32 * kManyWarps) lora_shrink_f32_kernel(const LoraArgs a) {
   griddep_launch_dependents();
   using C = ManyCfg<RT>;
   constexpr int RP = RT * 16, kThreads = 32 * kManyWarps;
@@ -525,44 +525,69 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int m, int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// Many rows of bf16 x. A CTA multiplies one part of K of 128 rows with the A of each
-// of their adapters: D, 128 rows x RP ranks in tensor memory, of 64 values of K a
-// step (x 16 KB and A by TMA); one accumulator after another where there are
-// several adapters (x comes again, from L2), every other one in a CTA of its own.
-// Two CTAs an SM.
+// four ranks of a row of scaling * h as two bf16 numbers each. (Ranks that only
+// pad: 0, also where x is infinite.)
+__device__ __forceinline__ void put_parts(const LoraArgs& a, int64_t m, int r, float4 v, float scale) {
+  v = r < a.rank ? make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale) : make_float4(0, 0, 0, 0);
+  const uint2 hi = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+  auto rest = [](float f, float h) { return isfinite(h) ? f - h : 0.0f; };  // (an infinity's would be NaN)
+  const uint2 lo = make_uint2(bf16x2(rest(v.x, bf16_lo(hi.x)), rest(v.y, bf16_hi(hi.x))),
+                              bf16x2(rest(v.z, bf16_lo(hi.y)), rest(v.w, bf16_hi(hi.y))));
+  uint2* to = reinterpret_cast<uint2*>(a.parts) + (m * a.rp + r) / 4;
+  to[0] = hi;
+  to[a.M * (a.rp / 4)] = lo;
+}
+
+// Many rows of bf16 x. A cluster of eight CTAs, one a part of K, multiplies 128 rows
+// with the A of each of their adapters: D, 128 rows x RP ranks in tensor memory, of
+// 64 values of K a step (x 16 KB and A by TMA), for up to four adapters at once. The
+// parts' sums meet in shared memory, where every CTA adds up 16 rows, in order. Two
+// CTAs an SM (one for ranks above 64). Of 10.5 us (4096 x 5120, rank 64) the steps
+// are 3.6; the CTAs of a launch of this size start over 3 us, the ids take 0.9 and the
+// meeting of the cluster 2.7.
 // Warps: 0 producer, 1 MMA issuer, 2..5 epilogue (32 rows each: a row a thread).
 template <int RP>
 struct ShrinkTc {
-  static constexpr int kX = 128 * 128, kA = RP * 128, kRing = RP == 128 ? 3 : 4, kSlots = 2;
-  static constexpr int kCols = kSlots * RP < 32 ? 32 : kSlots * RP;
-  static constexpr size_t kSmem = kRing * (kX + kA) + 1024;
+  static constexpr int kX = 128 * 128, kA = RP * 128, kRing = 3, kARing = RP == 128 ? 4 : 3, kPitch = RP + 4;
+  static constexpr int kBatch = 4, kCols = kBatch * RP;
+  static constexpr size_t kSmem = kRing * kX + kARing * kA + 128 * kPitch * 4 + 1024;
 };
 
 template <int RP>
-__global__ void __launch_bounds__(192, 2)
+__global__ void __cluster_dims__(kManyParts, 1, 1) __launch_bounds__(192, RP == 128 ? 1 : 2)
     lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
                           const LoraArgs a, uint32_t* err) {
   using C = ShrinkTc<RP>;
   griddep_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[C::kRing], empty[C::kRing], d_full[C::kSlots], d_empty[C::kSlots], drain;
+  __shared__ uint64_t x_full[C::kRing], x_empty[C::kRing], a_full[C::kARing], a_empty[C::kARing], d_full, drain;
   __shared__ uint32_t tmem_slot, tmem_busy;
+  __shared__ int ids[128];  // the adapters of the rows
   uint8_t* sx = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sa = sx + C::kRing * C::kX;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = blockIdx.x;
+  float* sum = reinterpret_cast<float*>(sa + C::kARing * C::kA);  // [row][rank], kPitch apart
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = (int)cluster_ctarank();
   const int64_t m0 = (int64_t)blockIdx.y * 128;
   const int all = (a.K + 63) / 64, k0 = all * part / kManyParts, k1 = all * (part + 1) / kManyParts;  // steps
   TileIds T;
   T.load(a, m0);
+  const int q = warp & 3, mine = q == 0 ? T.v[0] : q == 1 ? T.v[1] : q == 2 ? T.v[2] : T.v[3];  // of row 32 q + lane
+  T.find();
+  if (T.count == 0) return;  // (every thread of the cluster)
+  if (warp == 0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ids[j * 32 + lane] = T.list[j];
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kRing; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&x_full[i], 1);
+      mbar_init(&x_empty[i], 1);
     }
-    for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], 4);
+    for (int i = 0; i < C::kARing; ++i) {
+      mbar_init(&a_full[i], 1);
+      mbar_init(&a_empty[i], 1);
     }
+    mbar_init(&d_full, 1);
     mbar_init(&drain, 1);
     tmem_busy = 0;
     fence_barrier_init();
@@ -582,100 +607,122 @@ __global__ void __launch_bounds__(192, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  T.find();
-
-  if (warp == 0) {
-    bool ok = true;
-    int s = 0, loads = 0;
-    uint32_t phase = 1;
-    for (int i = blockIdx.z; i < T.count && ok; i += gridDim.z) {
-      const int id = T.at(i);
-      for (int k = k0; k < k1; ++k) {
-        ok = mbar_wait_warp(&empty[s], phase, err);
+  bool ok = true;
+  // of the producer and of the issuer: slots, phases (a fresh slot is free), loads so far
+  int s = 0, sA = 0, loads = 0, loadsA = 0;
+  uint32_t phase = warp == 0, phaseA = warp == 0, phaseD = 0;
+  for (int first = 0; first < T.count; first += C::kBatch) {
+    const int batch = min(C::kBatch, T.count - first);
+    if (warp == 0) {
+      for (int k = k0; k < k1 && ok; ++k) {
+        ok = mbar_wait_warp(&x_empty[s], phase, err);
         if (!ok) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&full[s], C::kX + C::kA);
-          tma_load_2d(sx + s * C::kX, &tmX, &full[s], k * 64, (int)m0);
-          tma_load_3d(sa + s * C::kA, &tmA, &full[s], k * 64, 0, id);
+          mbar_arrive_expect_tx(&x_full[s], C::kX);
+          tma_load_2d(sx + s * C::kX, &tmX, &x_full[s], k * 64, (int)m0);
         }
         __syncwarp();
         ++loads;
         if (++s == C::kRing) { s = 0; phase ^= 1; }
-      }
-    }
-    // every load has landed before the CTA exits
-    for (int i = max(0, loads - C::kRing); i < loads; ++i)
-      mbar_wait_warp(&full[i % C::kRing], (uint32_t)(i / C::kRing) & 1u, err);
-  } else if (warp == 1) {
-    constexpr uint32_t idesc = idesc_bf16_f32(128, RP);
-    bool ok = true;
-    int s = 0, d = 0;
-    uint32_t phase = 0, phaseD = 1;
-    for (int i = blockIdx.z; i < T.count && ok; i += gridDim.z) {
-      ok = mbar_wait_warp(&d_empty[d], phaseD, err);
-      if (!ok) break;
-      for (int k = k0; k < k1; ++k) {
-        ok = mbar_wait_warp(&full[s], phase, err);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t xa = smem_u32(sx + s * C::kX), aa = smem_u32(sa + s * C::kA);
-        if (elect_one()) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f16_ss(tmem + d * RP, smem_desc_sw128(xa + j * 32), smem_desc_sw128(aa + j * 32), idesc,
-                       k > k0 || j > 0);
-          mma_commit(&empty[s]);
-          if (k + 1 == k1) mma_commit(&d_full[d]);
+        for (int i = 0; i < batch; ++i) {
+          const int id = T.at(first + i);
+          ok = mbar_wait_warp(&a_empty[sA], phaseA, err);
+          if (!ok) break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&a_full[sA], C::kA);
+            tma_load_3d(sa + sA * C::kA, &tmA, &a_full[sA], k * 64, 0, id);
+          }
+          __syncwarp();
+          ++loadsA;
+          if (++sA == C::kARing) { sA = 0; phaseA ^= 1; }
         }
-        __syncwarp();
+      }
+    } else if (warp == 1) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, RP);
+      for (int k = k0; k < k1 && ok; ++k) {
+        ok = mbar_wait_warp(&x_full[s], phase, err);
+        const uint32_t xa = smem_u32(sx + s * C::kX);
+        for (int i = 0; i < batch && ok; ++i) {
+          ok = mbar_wait_warp(&a_full[sA], phaseA, err);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t aa = smem_u32(sa + sA * C::kA);
+          if (elect_one()) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_f16_ss(tmem + i * RP, smem_desc_sw128(xa + j * 32), smem_desc_sw128(aa + j * 32), idesc,
+                         k > k0 || j > 0);
+            mma_commit(&a_empty[sA]);
+            if (i + 1 == batch) mma_commit(&x_empty[s]);
+            if (i + 1 == batch && k + 1 == k1) mma_commit(&d_full);
+          }
+          __syncwarp();
+          if (++sA == C::kARing) { sA = 0; phaseA ^= 1; }
+        }
         if (++s == C::kRing) { s = 0; phase ^= 1; }
       }
-      if (k0 == k1) {
-        if (elect_one()) mma_commit(&d_full[d]);  // (nothing to sum: the epilogue knows)
-        __syncwarp();
-      }
-      if (++d == C::kSlots) { d = 0; phaseD ^= 1; }
-    }
-    if (!ok) {
-      if (elect_one()) mma_commit(&drain);
-      __syncwarp();
-      if (!mbar_wait_warp(&drain, 0, err)) atomicExch(&tmem_busy, 1u);
-    }
-  } else {
-    const int quarter = warp & 3;
-    const int64_t m = m0 + quarter * 32 + lane;
-    const int mine = adapter_of(a, m);
-    float4* to = reinterpret_cast<float4*>(a.h + ((int64_t)part * a.M + m) * RP);
-    bool ok = true;
-    int d = 0;
-    uint32_t phaseD = 0;
-    for (int i = blockIdx.z; i < T.count && ok; i += gridDim.z) {
-      const int id = T.at(i);
-      ok = mbar_wait_warp(&d_full[d], phaseD, err);
-      if (!ok) break;
-      if (__any_sync(0xffffffffu, mine == id)) {
+    } else {
+      if (k0 < k1) {
+        if (ok) ok = mbar_wait_warp(&d_full, phaseD, err);
+        phaseD ^= 1;
         tc_fence_after();
+      }
+      for (int i = 0; i < batch; ++i) {
+        const int id = T.at(first + i);
+        if (!__any_sync(0xffffffffu, mine == id)) continue;
 #pragma unroll
         for (int c = 0; c < RP; c += 16) {
           uint32_t v[16];
-          tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + d * RP + c, v);
+          tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + i * RP + c, v);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(v[j]));
           if (mine == id) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              to[c / 4 + j] = k0 == k1 ? make_float4(0, 0, 0, 0)
-                                       : make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                                     __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+            for (int j = 0; j < 4; ++j)  // (a part without steps: nothing has been summed)
+              *reinterpret_cast<uint4*>(sum + (q * 32 + lane) * C::kPitch + c + 4 * j) =
+                  k0 < k1 ? make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]) : make_uint4(0, 0, 0, 0);
           }
         }
-        tc_fence_before();
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&d_empty[d]);
-      if (++d == C::kSlots) { d = 0; phaseD ^= 1; }
+      tc_fence_before();
     }
+    cluster_sync();  // the sums are there, the accumulators have been read
+    tc_fence_after();
+    for (int e = threadIdx.x; e < 16 * (RP / 4); e += 192) {
+      const int row = part * 16 + e / (RP / 4), r = e % (RP / 4) * 4, id = adapter_of(a, m0 + row);
+      bool here = false;  // whether its sums are of this batch
+      for (int i = 0; i < batch; ++i) here |= id == ids[first + i];
+      if (id < 0 || !here) continue;
+      float4 v = make_float4(0, 0, 0, 0), p[kManyParts];
+#pragma unroll
+      for (int c = 0; c < kManyParts; ++c)
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(p[c].x), "=f"(p[c].y), "=f"(p[c].z), "=f"(p[c].w)
+                     : "r"(map_to_cta(sum + row * C::kPitch + r, c))
+                     : "memory");
+#pragma unroll
+      for (int c = 0; c < kManyParts; ++c) {
+        v.x += p[c].x;
+        v.y += p[c].y;
+        v.z += p[c].z;
+        v.w += p[c].w;
+      }
+      put_parts(a, m0 + row, r, v, a.scaling ? __ldg(a.scaling + id) : 1.0f);
+    }
+    cluster_sync();  // the sums have been read
+  }
+  if (warp == 0) {
+    // every load has landed before the CTA exits
+    for (int i = max(0, loads - C::kRing); i < loads; ++i)
+      mbar_wait_warp(&x_full[i % C::kRing], (uint32_t)(i / C::kRing) & 1u, err);
+    for (int i = max(0, loadsA - C::kARing); i < loadsA; ++i)
+      mbar_wait_warp(&a_full[i % C::kARing], (uint32_t)(i / C::kARing) & 1u, err);
+  } else if (warp == 1 && !ok) {
+    // (after a wait that gave up, MMAs issued so far may still run; bounded)
+    if (elect_one()) mma_commit(&drain);
+    __syncwarp();
+    if (!mbar_wait_warp(&drain, 0, err)) atomicExch(&tmem_busy, 1u);
   }
   tc_fence_before();
   __syncthreads();
@@ -685,9 +732,8 @@ __global__ void __launch_bounds__(192, 2)
   }
 }
 
-// Adds up the parts' sums in order, scales them and splits them into two bf16
-// numbers; a thread four ranks of a row. (Ranks that only pad: 0, also where x is
-// infinite.) Rows without an adapter are left: nothing reads their products.
+// The same end for the parts' sums that lora_shrink_f32_kernel leaves; a thread
+// four ranks of a row. Rows without an adapter are left: nothing reads their products.
 __global__ void __launch_bounds__(256) lora_join_kernel(const LoraArgs a) {
   griddep_launch_dependents();
   const int fours = a.rp / 4;
@@ -707,14 +753,7 @@ __global__ void __launch_bounds__(256) lora_join_kernel(const LoraArgs a) {
     v.z += p[i].z;
     v.w += p[i].w;
   }
-  v = r < a.rank ? make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale) : make_float4(0, 0, 0, 0);
-  const uint2 hi = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
-  auto rest = [](float f, float h) { return isfinite(h) ? f - h : 0.0f; };  // (an infinity's would be NaN)
-  const uint2 lo = make_uint2(bf16x2(rest(v.x, bf16_lo(hi.x)), rest(v.y, bf16_hi(hi.x))),
-                              bf16x2(rest(v.z, bf16_lo(hi.y)), rest(v.w, bf16_hi(hi.y))));
-  uint2* to = reinterpret_cast<uint2*>(a.parts) + e;
-  to[0] = hi;
-  to[a.M * fours] = lo;
+  put_parts(a, m, r, v, scale);
 }
 
 // Many rows. Bound by reading base and writing out, so both go by TMA, tile by
@@ -741,11 +780,18 @@ struct ExpandMany {
   static constexpr size_t kSmem = kBaseRing * kBase + kBRing * kB + kHRing * kHBytes + 1024;
 };
 
+// how the tiles are dealt out: `sections` times the number of CTAs cells of `tiles`
+// tiles, the first `rest` cells one more
+struct ExpandShares {
+  int sections;
+  uint32_t tiles, rest;
+};
+
 template <bool kBf16, int kHalves>
 __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
     lora_expand_many_kernel(const __grid_constant__ CUtensorMap tmBase, const __grid_constant__ CUtensorMap tmB,
                             const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmH, const LoraArgs a,
-                            const int aligned, const int sections, uint32_t* err) {
+                            const int aligned, const ExpandShares share, uint32_t* err) {
   using C = ExpandMany<kBf16, kHalves>;
   constexpr int kN = C::kN;
   extern __shared__ uint8_t smem_raw[];
@@ -758,8 +804,7 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
   uint8_t* sb = sx + C::kBaseRing * C::kBase;          // B [slot][half]
   uint8_t* sh = sb + C::kBRing * C::kB;                // h [slot][large, small][half]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int CT = (a.N + kN - 1) / kN;
-  const int64_t tiles = (a.M + 127) / 128 * CT, cells = (int64_t)sections * gridDim.x;
+  const uint32_t CT = (a.N + kN - 1) / kN;
   const bool keep = a.base == a.out && a.ldb == a.ldo;  // rows without an adapter are in place
 
   if (threadIdx.x == 0) {
@@ -804,26 +849,35 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
   // adapters, the tiles of columns c0 up to c1. Rows that have no adapter and are in
   // place are passed over. (The next rows' ids are on their way.)
   TileIds T, ahead;
-  int64_t cell = blockIdx.x, next = tiles * cell / cells, end = tiles * (cell + 1) / cells, m0 = 0;
-  int c0 = 0, c1 = 0, mine = -1;  // mine: of row 32 (warp % 4) + lane
-  auto skip_empty = [&]() {  // to the next cell while this one is done
-    while (next >= end && cell + gridDim.x < cells) {
-      cell += gridDim.x;
-      next = tiles * cell / cells;
-      end = tiles * (cell + 1) / cells;
+  int section = 0, c0 = 0, c1 = 0, mine = -1;  // mine: of row 32 (warp % 4) + lane
+  uint32_t next = 0, end = 0;
+  int64_t m0 = 0;
+  // (a CTA's place in a section moves on by a quarter from one to the next: rows of
+  // several adapters often lie at regular distances)
+  auto enter = [&]() {
+    const uint32_t place = (blockIdx.x + section * (gridDim.x / 4 + 1)) % gridDim.x;
+    const uint32_t cell = section * gridDim.x + place;
+    next = cell * share.tiles + min(cell, share.rest);
+    end = next + share.tiles + (cell < share.rest);
+  };
+  enter();
+  auto skip_empty = [&]() {  // to the next section while this one is done
+    while (next >= end && section + 1 < share.sections) {
+      ++section;
+      enter();
     }
     return next < end;
   };
-  if (skip_empty()) ahead.load(a, next / CT * 128);
+  if (skip_empty()) ahead.load(a, (int64_t)(next / CT) * 128);
   auto advance = [&]() {
     while (skip_empty()) {
-      const int64_t rt = next / CT, stop = min(end, (rt + 1) * CT);
-      m0 = rt * 128;
+      const uint32_t rt = next / CT, stop = min(end, (rt + 1) * CT);
+      m0 = (int64_t)rt * 128;
       c0 = (int)(next - rt * CT);
       c1 = (int)(stop - rt * CT);
       next = stop;
       T = ahead;
-      if (skip_empty()) ahead.load(a, next / CT * 128);
+      if (skip_empty()) ahead.load(a, (int64_t)(next / CT) * 128);
       mine = (warp & 3) == 0 ? T.v[0] : (warp & 3) == 1 ? T.v[1] : (warp & 3) == 2 ? T.v[2] : T.v[3];
       T.find();
       if (T.count || !keep) return true;
@@ -1049,7 +1103,7 @@ static cudaError_t launch_shrink_many(const LoraArgs& a, bool x_bf16, uint32_t* 
   if (x_bf16) {
     constexpr int RP = RT * 16;
     using C = ShrinkTc<RP>;
-    static_assert(C::kSmem <= 113 * 1024, "shared memory of two CTAs");
+    static_assert(C::kSmem <= (RP == 128 ? 227 : 113) * 1024, "shared memory");
     CUtensorMap tx, ta;
     if (!make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.K, a.M, a.ldx * 2, 64, 128,
                       CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -1060,14 +1114,14 @@ static cudaError_t launch_shrink_many(const LoraArgs& a, bool x_bf16, uint32_t* 
     static std::atomic<uint64_t> attr_set{0};
     const cudaError_t e = smem_attr_once_per_device(kern, (int)C::kSmem, attr_set);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(kManyParts, (unsigned)ceil_div(a.M, 128), 2), 192, C::kSmem, st>>>(tx, ta, a, err);
+    kern<<<dim3(kManyParts, (unsigned)ceil_div(a.M, 128)), 192, C::kSmem, st>>>(tx, ta, a, err);
     return cudaGetLastError();
   }
   const int64_t windows = ceil_div(a.M, 32);
   // with few windows several CTAs share the pieces of one
   int64_t z = 4 * num_sms() / (windows * kManyParts);
   z = z < 1 ? 1 : z > 32 ? 32 : z;
-  auto kern = lora_shrink_many_kernel<RT>;
+  auto kern = lora_shrink_f32_kernel<RT>;
   static std::atomic<uint64_t> attr_set{0};
   const cudaError_t e = smem_attr_once_per_device(kern, ManyCfg<RT>::kSmem, attr_set);
   if (e != cudaSuccess) return e;
@@ -1101,10 +1155,13 @@ static cudaError_t launch_expand_many(const LoraArgs& a, uint32_t* err, cudaStre
   const cudaError_t e = smem_attr_once_per_device(kern, (int)C::kSmem, attr_set);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ceil_div(a.M, 128) * ceil_div(a.N, C::kN), ctas = tiles < num_sms() ? tiles : num_sms();
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  // (a change of rows costs about as much as two tiles)
   int64_t sections = tiles / (ctas * 12);
   sections = sections < 1 ? 1 : sections > 8 ? 8 : sections;
+  const ExpandShares share{(int)sections, (uint32_t)(tiles / (ctas * sections)), (uint32_t)(tiles % (ctas * sections))};
   return launch_kernel(kern, dim3((unsigned)ctas), dim3(C::kThreads), C::kSmem, st, true, tx, tb, to, th, a,
-                       (int)aligned, (int)sections, err);
+                       (int)aligned, share, err);
 }
 
 template <bool kBf16, int C>
@@ -1158,7 +1215,8 @@ cudaError_t launch_add_lora(const void* base, bool bf16, int64_t ldb, const void
                   : a.rp == 64 ? launch_shrink_many<4>(a, x_bf16, err, st)
                                : launch_shrink_many<8>(a, x_bf16, err, st);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(lora_join_kernel, dim3((unsigned)ceil_div(M * (a.rp / 4), 256)), dim3(256), 0, st, true, a);
+  if (!x_bf16)
+    e = launch_kernel(lora_join_kernel, dim3((unsigned)ceil_div(M * (a.rp / 4), 256)), dim3(256), 0, st, true, a);
   if (e != cudaSuccess) return e;
   if (rank <= 64) return bf16 ? launch_expand_many<true, 1>(a, err, st) : launch_expand_many<false, 1>(a, err, st);
   return bf16 ? launch_expand_many<true, 2>(a, err, st) : launch_expand_many<false, 2>(a, err, st);
