@@ -16,7 +16,7 @@
 // follow one another, so that weights come from HBM once.
 #include <cuda.h>
 
-#include "qg_common.cuh"
+#include "gemm_grouped.cuh"
 
 namespace qg {
 
@@ -26,6 +26,11 @@ bool make_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, 
 bool make_tmap_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t cols,
                   int64_t rows, int64_t mats, int64_t pitch, int64_t mat_pitch, uint32_t box_cols,
                   uint32_t box_rows, CUtensorMapSwizzle swizzle);
+
+cudaError_t launch_gemm_fp8_grouped_large(const uint8_t* q, const float* scale, int64_t lds, int64_t M, int64_t K,
+                                          const int64_t* offsets, int64_t E, const uint8_t* w, int64_t ldw,
+                                          int64_t lde, const float* w_scale, int64_t N, void* out, bool out_f32,
+                                          int64_t ldo, uint32_t* err, cudaStream_t st);
 
 struct Fp8GroupedArgs {
   const int64_t* offsets;  // [E + 1]
@@ -63,57 +68,6 @@ struct GroupedBars {
   uint32_t tmem_base, tmem_busy;
 };
 
-// The tiles of a call: expert e has ceil(count / BM) tiles of rows (before[e]
-// of them lie ahead of its own) times NT tiles of weight rows, the rows' tiles
-// of one weight tile after one another.
-struct GroupedTiles {
-  const int *first, *before;  // [E], [E + 1], in shared memory
-  int E, NT;
-  // Filled by one warp. Offsets outside 0..M are taken as 0 or M, an expert
-  // whose end lies before its start as one without rows.
-  static __device__ void fill(const int64_t* offsets, int E, int M, int BM, int* first, int* count, int* before) {
-    const int lane = threadIdx.x & 31;
-    int base = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + lane;
-      int lo = 0, n = 0;
-      if (e < E) {
-        lo = (int)min(max(offsets[e], (int64_t)0), (int64_t)M);
-        n = max((int)min(max(offsets[e + 1], (int64_t)0), (int64_t)M) - lo, 0);
-      }
-      const int t = (n + BM - 1) / BM;
-      int s = t;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += v;
-      }
-      if (e < E) {
-        first[e] = lo;
-        count[e] = n;
-        before[e] = base + s - t;
-      }
-      base += __shfl_sync(0xffffffffu, s, 31);
-    }
-    if (lane == 0) before[E] = base;
-  }
-  __device__ int total() const { return before[E] * NT; }
-  // the expert of tile t, its tile of rows and of weight rows; by a whole warp
-  __device__ void at(int t, int& e, int& mi, int& ni) const {
-    const int lane = threadIdx.x & 31, row = t / NT;  // row: its tiles of rows are counted alike
-    int lo = 0;
-    for (int span = 1024; span > 1; span >>= 5) {
-      const int i = min(lo + lane * (span >> 5), E);
-      lo += (__popc(__ballot_sync(0xffffffffu, before[i] <= row)) - 1) * (span >> 5);
-      lo = min(lo, E - 1);
-    }
-    e = lo;
-    const int k = before[e + 1] - before[e], idx = t - before[e] * NT;
-    ni = idx / k;
-    mi = idx - ni * k;
-  }
-};
-
 template <int R, int BM>
 __global__ void __launch_bounds__(GroupedCfg<R, BM>::kThreads)
     gemm_fp8_grouped_kernel(const __grid_constant__ CUtensorMap tmW,
@@ -130,9 +84,8 @@ __global__ void __launch_bounds__(GroupedCfg<R, BM>::kThreads)
   uint8_t* sw = base;                            // weight tiles [stage][G]
   uint8_t* sq = sw + stages * G * C::kW;         // rows' tiles [stage][G]
   uint8_t* ss = sq + stages * G * C::kQ;         // rows' scales [stage][G][BM + 4]
-  int* first = reinterpret_cast<int*>(ss + stages * C::kS);  // [E]
-  int* count = first + a.E;                                  // [E]
-  int* before = count + a.E;                                 // [E + 1]
+  int* first = reinterpret_cast<int*>(ss + stages * C::kS);  // [E + 1]
+  int* before = first + a.E + 1;                             // [E + 1]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -160,7 +113,7 @@ __global__ void __launch_bounds__(GroupedCfg<R, BM>::kThreads)
     tmem_alloc(&S.tmem_base, C::kCols);
     tmem_relinquish();
   }
-  if (warp == 2) GroupedTiles::fill(a.offsets, a.E, a.M, BM, first, count, before);
+  if (warp == 2) GroupedTiles::fill(a.offsets, a.E, a.M, BM, first, before);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -256,7 +209,7 @@ __global__ void __launch_bounds__(GroupedCfg<R, BM>::kThreads)
     bool ok = true;
     for (int tile = blockIdx.x; tile < tiles && ok; tile += step) {
       const float* wsp = scales(e, ni);
-      const int m0 = first[e] + mi * BM, rows = min(BM, count[e] - mi * BM), n0 = ni * R;
+      const int m0 = first[e] + mi * BM, rows = min(BM, first[e + 1] - m0), n0 = ni * R;
       float w_cur = w_first;
       float w_nxt = 32 + lane < KB ? ldg_f32_pinned(wsp + 32 + lane) : 0.0f;
       if (tile + step < tiles) {
@@ -362,11 +315,11 @@ static cudaError_t launch_grouped(const uint8_t* q, const float* scale, int64_t 
   // one CTA per SM, with the whole shared memory for its ring
   const int64_t most = ((a.M < a.E ? a.M : a.E) + a.M / BM) * ceil_div(a.N, R);
   const unsigned grid = (unsigned)(most < num_sms() ? most : num_sms());
-  const int lists = (3 * a.E + 1) * 4;
-  int stages = (223 * 1024 - lists) / (int)C::kStage;
+  const int list = GroupedTiles::bytes(a.E);
+  int stages = (223 * 1024 - list) / (int)C::kStage;
   stages = stages > kGroupedMaxStages ? kGroupedMaxStages : stages;
   a.stages = stages;
-  const size_t smem = (size_t)stages * C::kStage + lists + 1024;
+  const size_t smem = (size_t)stages * C::kStage + list + 1024;
   auto kern = gemm_fp8_grouped_kernel<R, BM>;
   static std::atomic<uint64_t> attr_set{0};
   const cudaError_t e = smem_attr_once_per_device(kern, 224 * 1024, attr_set);
@@ -387,7 +340,7 @@ cudaError_t launch_gemm_fp8_grouped(const uint8_t* q, const float* scale, int64_
   if (mean <= 12) return launch_grouped<128, 16>(q, scale, lds, K, w, ldw, lde, a, st);
   if (mean <= 32) return launch_grouped<128, 32>(q, scale, lds, K, w, ldw, lde, a, st);
   if (mean <= 64) return launch_grouped<128, 64>(q, scale, lds, K, w, ldw, lde, a, st);
-  return launch_grouped<128, 128>(q, scale, lds, K, w, ldw, lde, a, st);
+  return launch_gemm_fp8_grouped_large(q, scale, lds, M, K, offsets, E, w, ldw, lde, w_scale, N, out, out_f32, ldo, err, st);
 }
 
 }  // namespace qg

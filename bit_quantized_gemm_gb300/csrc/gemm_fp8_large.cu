@@ -38,10 +38,13 @@
 
 #include <cstring>
 
-#include "qg_common.cuh"
+#include "gemm_grouped.cuh"
 
 namespace qg {
 
+bool make_tmap_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t cols,
+                  int64_t rows, int64_t mats, int64_t pitch, int64_t mat_pitch, uint32_t box_cols,
+                  uint32_t box_rows, CUtensorMapSwizzle swizzle);
 bool make_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t cols,
                   int64_t rows, int64_t pitch, uint32_t box_cols, uint32_t box_rows,
                   CUtensorMapSwizzle swizzle);
@@ -64,10 +67,13 @@ struct Fp8LargeArgs {
   int tile_group;        // token tiles per group of the persistent tile order
   int tma_out, pdl;
   uint32_t* err;
+  // grouped by expert
+  const int64_t* offsets;  // [E + 1]
+  int E;
 };
 
 // Geometry of a tile
-template <bool kPair, int W, bool kF32>
+template <bool kPair, int W, bool kF32, bool kGrouped>
 struct Fp8LargeCfg {
   static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int kTileM = 128 * kCtas;
@@ -92,7 +98,10 @@ struct Fp8LargeCfg {
   // ring stages of G blocks of K share their barriers; a stage also brings the
   // token scales of its blocks
   static constexpr int G = 2;
-  static constexpr int kScaleBytes = G * 512;
+  // a row of scales has to start on a multiple of four tokens: where an expert's
+  // first row decides, four more are loaded
+  static constexpr int kScaleRow = kGrouped ? 132 : 128, kScaleLoad = G * kScaleRow * 4;
+  static constexpr int kScaleBytes = (kScaleLoad + 127) / 128 * 128;
   static constexpr uint32_t kStage = G * (kABytes + kBBytes);
   // s * ws of a block: [buffer][row block of the tile][token]
   static constexpr int kScaleRows = W > 128 ? 2 : 1;
@@ -104,13 +113,13 @@ struct Fp8LargeCfg {
   static_assert(W % 64 == 0 && W <= 256 && kCols % kRound == 0 && kStages >= 3, "tile");
 };
 
-template <bool kPair, int W, bool kF32>
-__global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
+template <bool kPair, int W, bool kF32, bool kGrouped>
+__global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32, kGrouped>::kThreads, 1)
     gemm_fp8_large_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmW,
                           const __grid_constant__ CUtensorMap tmS,
                           const __grid_constant__ CUtensorMap tmO, const Fp8LargeArgs a) {
-  using C = Fp8LargeCfg<kPair, W, kF32>;
+  using C = Fp8LargeCfg<kPair, W, kF32, kGrouped>;
   constexpr int kSlots = C::kSlots, G = C::G;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[C::kStages], empty[C::kStages], sfull[C::kStages];
@@ -128,7 +137,9 @@ __global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
   const uint32_t rank = kPair ? cluster_ctarank() : 0;
   const int KB = a.KB, NS = (KB + G - 1) / G;
   const int MT = (a.M + C::kTileM - 1) / C::kTileM, NT = (a.N + W - 1) / W;
-  const int tiles = MT * NT;
+  int tiles = MT * NT;
+  int* const lists = reinterpret_cast<int*>(sf + C::kProducts / 4);  // grouped: the experts' rows and tiles
+  const GroupedTiles T{lists, lists + a.E + 1, a.E, NT};
   const int first = (int)blockIdx.x / C::kCtas, step = (int)gridDim.x / C::kCtas;
 
   if (threadIdx.x == 0) {
@@ -160,20 +171,40 @@ __global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
       tmem_relinquish();
     }
   }
+  if constexpr (kGrouped) {
+    if (warp == 2) GroupedTiles::fill(a.offsets, a.E, a.M, C::kTileM, lists, lists + a.E + 1);
+  }
   tc_fence_before();
   if constexpr (kPair) cluster_sync();
   else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  if constexpr (kGrouped) tiles = T.total();
 
-  auto coords = [&](int tile, int& mt, int& nt) {
+  // a tile's expert (grouped), its first token and the token after its last, its
+  // number among the tiles of weight rows
+  struct Place {
+    int e, m, end, nt;
+  };
+  auto place = [&](int tile) {
+    Place p;
+    if constexpr (kGrouped) {
+      int mi;
+      T.at(tile, p.e, mi, p.nt);
+      p.m = T.first[p.e] + mi * C::kTileM;
+      p.end = T.first[p.e + 1];
+      return p;
+    }
     // groups of tile_group token tiles, the token tile fastest: the tiles in
     // flight share weight rows and a bounded set of tokens in L2
     const int per = a.tile_group * NT, g = tile / per;
     const int gm = min(a.tile_group, MT - g * a.tile_group);
     const int idx = tile - g * per;
-    mt = g * a.tile_group + idx % gm;
-    nt = idx / gm;
+    p.e = 0;
+    p.m = (g * a.tile_group + idx % gm) * C::kTileM;
+    p.end = a.M;
+    p.nt = idx / gm;
+    return p;
   };
 
   if (C::kEpiRegs != C::kRestRegs && warp < 4)
@@ -186,9 +217,8 @@ __global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
     int s = 0, loads = 0;
     uint32_t phase = 1;
     for (int tile = first; tile < tiles && ok; tile += step) {
-      int mt, nt;
-      coords(tile, mt, nt);
-      const int m = mt * C::kTileM + (int)rank * 128, n = nt * W + (int)rank * C::kWRows;
+      const Place p = place(tile);
+      const int m = p.m + (int)rank * 128, n = p.nt * W + (int)rank * C::kWRows;
       for (int i = 0; i < NS; ++i) {
         ok = mbar_wait_warp(&empty[s], phase, a.err);
         if (!ok) break;
@@ -201,17 +231,23 @@ __global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
           // both CTAs' bytes complete on the leader's barrier
           if (rank == 0)
             mbar_arrive_expect_tx(&full[s], blocks * C::kCtas * (C::kABytes + C::kBBytes));
-          mbar_arrive_expect_tx(&sfull[s], C::kScaleBytes);
-          tma_load_2d(ss + s * C::kScaleBytes, &tmS, &sfull[s], m, G * i);
+          mbar_arrive_expect_tx(&sfull[s], C::kScaleLoad);
+          tma_load_2d(ss + s * C::kScaleBytes, &tmS, &sfull[s], kGrouped ? m & ~3 : m, G * i);
           const uint32_t bar = kPair ? map_to_cta(&full[s], 0) : 0;
           for (int j = 0; j < blocks; ++j) {
             const int k = (G * i + j) * 128;
             if constexpr (kPair) {
               tma_load_2d_pair(sa + (G * s + j) * C::kABytes, &tmQ, bar, k, m);
-              tma_load_2d_pair(sb + (G * s + j) * C::kBBytes, &tmW, bar, k, n);
+              if constexpr (kGrouped)
+                tma_load_3d_pair(sb + (G * s + j) * C::kBBytes, &tmW, bar, k, n, p.e);
+              else
+                tma_load_2d_pair(sb + (G * s + j) * C::kBBytes, &tmW, bar, k, n);
             } else {
               tma_load_2d(sa + (G * s + j) * C::kABytes, &tmQ, &full[s], k, m);
-              tma_load_2d(sb + (G * s + j) * C::kBBytes, &tmW, &full[s], k, n);
+              if constexpr (kGrouped)
+                tma_load_3d(sb + (G * s + j) * C::kBBytes, &tmW, &full[s], k, n, p.e);
+              else
+                tma_load_2d(sb + (G * s + j) * C::kBBytes, &tmW, &full[s], k, n);
             }
           }
         }
@@ -311,25 +347,27 @@ __global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
     int s = 0;
     uint32_t phase = 0, used = ~0u;  // used: bit per buffer, phase of the next wait
     float w_first[C::kScaleRows];    // the weight scales of a tile's first 32 blocks
-    auto w_row = [&](int tile, int r) {
-      int mt, nt;
-      coords(tile, mt, nt);
-      return a.w_scale + (int64_t)min((nt * W >> 7) + r, a.NB - 1) * KB;
+    auto w_row = [&](const Place& p, int r) {
+      return a.w_scale + (kGrouped ? (int64_t)p.e * a.NB * KB : 0) + (int64_t)min((p.nt * W >> 7) + r, a.NB - 1) * KB;
     };
+    Place here{}, after{};
+    if (tiles_here) after = place(first);
 #pragma unroll
     for (int r = 0; r < C::kScaleRows; ++r)
-      w_first[r] = tiles_here && lane < KB ? ldg_f32_pinned(w_row(first, r) + lane) : 0.0f;
+      w_first[r] = tiles_here && lane < KB ? ldg_f32_pinned(w_row(after, r) + lane) : 0.0f;
     for (int ti = 0; ti < tiles_here && ok; ++ti) {
-      const int tile = first + ti * step;
+      here = after;
+      if (ti + 1 < tiles_here) after = place(first + (ti + 1) * step);
+      const int odd = kGrouped ? here.m & 3 : 0;  // (of either CTA: its tokens are 128 apart)
       const float* wp[C::kScaleRows];
       float w_cur[C::kScaleRows], w_nxt[C::kScaleRows];
 #pragma unroll
       for (int r = 0; r < C::kScaleRows; ++r) {
-        wp[r] = w_row(tile, r);
+        wp[r] = w_row(here, r);
         w_cur[r] = w_first[r];
         w_nxt[r] = 32 + lane < KB ? ldg_f32_pinned(wp[r] + 32 + lane) : 0.0f;
         if (ti + 1 < tiles_here)
-          w_first[r] = lane < KB ? ldg_f32_pinned(w_row(tile + step, r) + lane) : 0.0f;
+          w_first[r] = lane < KB ? ldg_f32_pinned(w_row(after, r) + lane) : 0.0f;
       }
 #pragma unroll (2 * kSlots / U)
       for (int b = 0; b < KB; b += U) {
@@ -341,8 +379,13 @@ __global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
         float4 p[U][C::kScaleRows];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const float4 v =
-              *reinterpret_cast<const float4*>(ss + s * C::kScaleBytes + (own + u) * 512 + lane * 16);
+          const float* ps =
+              reinterpret_cast<const float*>(ss + s * C::kScaleBytes + (own + u) * C::kScaleRow * 4) + lane * 4;
+          float4 v;
+          if constexpr (kGrouped)
+            v = make_float4(ps[odd], ps[odd + 1], ps[odd + 2], ps[odd + 3]);
+          else
+            v = *reinterpret_cast<const float4*>(ps);
 #pragma unroll
           for (int r = 0; r < C::kScaleRows; ++r) {
             const float w = __shfl_sync(0xffffffffu, w_cur[r], (b + u) & 31);
@@ -392,10 +435,11 @@ __global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
     uint32_t used = 0;  // bit per buffer: phase of its next wait
     bool ok = true;
     for (int tile = first; tile < tiles && ok; tile += step) {
-      int mt, nt;
-      coords(tile, mt, nt);
-      const int mrow0 = mt * C::kTileM + (int)rank * 128 + quarter * 32;  // this warp's first token
-      const int nc0 = nt * W + part * C::kCols;                          // and first column
+      const Place p = place(tile);
+      const int mrow0 = p.m + (int)rank * 128 + quarter * 32;  // this warp's first token
+      const int nc0 = p.nt * W + part * C::kCols;              // and first column
+      // (a store of 32 rows stops at the last of all rows, not at the expert's)
+      const bool tma_out = a.tma_out && (!kGrouped || mrow0 + 32 <= p.end);
       float acc[C::kCols];
 #pragma unroll
       for (int j = 0; j < C::kCols; ++j) acc[j] = 0.0f;
@@ -484,44 +528,56 @@ __global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
         for (int i = 0; i < 4; ++i) {
           uint4 o;
           if constexpr (kF32) {
-            const float* p = acc + c0 + 4 * i;
-            o = make_uint4(__float_as_uint(p[0]), __float_as_uint(p[1]), __float_as_uint(p[2]),
-                           __float_as_uint(p[3]));
+            const float* f = acc + c0 + 4 * i;
+            o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                           __float_as_uint(f[3]));
           } else {
-            const float* p = acc + c0 + 8 * i;
+            const float* f = acc + c0 + 8 * i;
             uint32_t* w4 = reinterpret_cast<uint32_t*>(&o);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(p[2 * j], p[2 * j + 1]);
+              const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
               w4[j] = *reinterpret_cast<const uint32_t*>(&h);
             }
           }
           *reinterpret_cast<uint4*>(stage + lane * C::kRowBytes + ((i ^ sw) * 16)) = o;
         }
-        if (a.tma_out) {
+        if (tma_out) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && mrow0 < a.M && nc0 + c0 < a.N) {
             tma_store_2d(&tmO, stage, nc0 + c0, mrow0);
             bulk_commit_group();
           }
+        } else if (kGrouped && a.tma_out) {
+          // an expert's last rows: 16 bytes a lane, eight rows at a time
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2), col = (lane & 3) * (16 / C::kEsize);
+            if (mrow0 + r >= p.end || nc0 + c0 + col >= a.N) continue;
+            const uint4 o = *reinterpret_cast<const uint4*>(stage + r * C::kRowBytes + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+            *reinterpret_cast<uint4*>(reinterpret_cast<char*>(a.out) +
+                                      ((int64_t)(mrow0 + r) * a.ldo + nc0 + c0 + col) * C::kEsize) = o;
+          }
+          __syncwarp();
         } else {
           __syncwarp();
           // 32 columns of a row at a time, or 16 of two rows
           constexpr int kRows = 32 / C::kRound;
-          const int rows = min(32, a.M - mrow0), cols = min(C::kRound, a.N - nc0 - c0);
+          const int rows = min(32, p.end - mrow0), cols = min(C::kRound, a.N - nc0 - c0);
           const int col = lane % C::kRound, byte = col * C::kEsize;
 #pragma unroll 4
           for (int r0 = 0; r0 < rows; r0 += kRows) {
             const int r = r0 + lane / C::kRound;
-            const uint8_t* p =
+            const uint8_t* from =
                 stage + r * C::kRowBytes + (((byte >> 4) ^ ((r >> 1) & 3)) << 4) + (byte & 15);
             const int64_t o = (int64_t)(mrow0 + r) * a.ldo + nc0 + c0 + col;
             if (r >= rows || col >= cols) continue;
             if constexpr (kF32)
-              reinterpret_cast<float*>(a.out)[o] = *reinterpret_cast<const float*>(p);
+              reinterpret_cast<float*>(a.out)[o] = *reinterpret_cast<const float*>(from);
             else
-              reinterpret_cast<uint16_t*>(a.out)[o] = *reinterpret_cast<const uint16_t*>(p);
+              reinterpret_cast<uint16_t*>(a.out)[o] = *reinterpret_cast<const uint16_t*>(from);
           }
           __syncwarp();
         }
@@ -551,17 +607,20 @@ __global__ void __launch_bounds__(Fp8LargeCfg<kPair, W, kF32>::kThreads, 1)
   }
 }
 
-template <bool kPair, int W, bool kF32>
-static cudaError_t launch_large(const uint8_t* q, int64_t K, const uint8_t* w, int64_t ldw,
+// (experts' weights lie lde bytes apart where the product is grouped)
+template <bool kPair, int W, bool kF32, bool kGrouped>
+static cudaError_t launch_large(const uint8_t* q, int64_t K, const uint8_t* w, int64_t ldw, int64_t lde,
                                 Fp8LargeArgs a, cudaStream_t st) {
-  using C = Fp8LargeCfg<kPair, W, kF32>;
-  static_assert(C::kSmem <= 226 * 1024, "shared memory per CTA");
+  using C = Fp8LargeCfg<kPair, W, kF32, kGrouped>;
+  static_assert(C::kSmem + (kGrouped ? GroupedTiles::bytes(1024) : 0) <= 226 * 1024, "shared memory per CTA");
   CUtensorMap tq, tw, ts, to;
   if (!make_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, a.M, K, 128, 128,
                     CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, K, a.N, ldw, 128, C::kWRows,
-                    CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&ts, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.scale, a.M, a.KB, a.lds * 4, 128,
+      !(kGrouped ? make_tmap_3d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, K, a.N, a.E, ldw, lde, 128, C::kWRows,
+                                CU_TENSOR_MAP_SWIZZLE_128B)
+                 : make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, K, a.N, ldw, 128, C::kWRows,
+                                CU_TENSOR_MAP_SWIZZLE_128B)) ||
+      !make_tmap_2d(&ts, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.scale, a.M, a.KB, a.lds * 4, C::kScaleRow,
                     C::G, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorNotSupported;
   memset(&to, 0, sizeof(to));
@@ -572,9 +631,11 @@ static cudaError_t launch_large(const uint8_t* q, int64_t K, const uint8_t* w, i
                            a.out, a.N, a.M, a.ldo * (kF32 ? 4 : 2), C::kRound, 32,
                            CU_TENSOR_MAP_SWIZZLE_64B);
   a.tile_group = 2048 / C::kTileM;
-  auto kern = gemm_fp8_large_kernel<kPair, W, kF32>;
+  // (grouped: the list of tiles behind everything else)
+  const size_t smem = C::kSmem + (kGrouped ? GroupedTiles::bytes(a.E) : 0);
+  auto kern = gemm_fp8_large_kernel<kPair, W, kF32, kGrouped>;
   static std::atomic<uint64_t> attr_set{0};
-  cudaError_t e = smem_attr_once_per_device(kern, (int)C::kSmem, attr_set);
+  cudaError_t e = smem_attr_once_per_device(kern, (int)C::kSmem + (kGrouped ? GroupedTiles::bytes(1024) : 0), attr_set);
   if (e != cudaSuccess) return e;
   // the register split takes from what the block was launched with
   static const int regs = [&] {
@@ -583,12 +644,14 @@ static cudaError_t launch_large(const uint8_t* q, int64_t K, const uint8_t* w, i
   }();
   if (C::kEpiRegs != C::kRestRegs && regs < C::kLaunchRegs)
     return cudaErrorInvalidConfiguration;
-  const int64_t tiles = ceil_div(a.M, C::kTileM) * ceil_div(a.N, W);
+  // (grouped: at most; the device knows the number)
+  const int64_t tiles = (kGrouped ? a.M / C::kTileM + (a.M < a.E ? a.M : a.E) : ceil_div(a.M, C::kTileM)) *
+                        ceil_div(a.N, W);
   const int64_t slots = num_sms() / C::kCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((tiles < slots ? tiles : slots) * C::kCtas));
   cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -616,15 +679,16 @@ struct Fp8LargeChoice {
 };
 static const Fp8LargeChoice kChoices[] = {{true, 256, 481}, {true, 128, 252}, {false, 128, 276}, {false, 64, 236}};
 
-// the tile of the smallest estimated time: waves x ns per block
-static int fp8_large_choice(int64_t M, int64_t N, int sms) {
+// the tile of the smallest estimated time: waves x ns per block. (Rows of `experts`:
+// the last tile of each is taken as half full.)
+static int fp8_large_choice(int64_t M, int64_t N, int sms, int64_t experts) {
   int best = 3;
   double best_t = 1e300;
   for (int i = 0; i < 4; ++i) {
     const Fp8LargeChoice& c = kChoices[i];
     const int ctas = c.pair ? 2 : 1;
     if (sms < ctas) continue;
-    const int64_t tiles = ceil_div(M, 128 * ctas) * ceil_div(N, c.w);
+    const int64_t tiles = (ceil_div(M, 128 * ctas) + experts / 2) * ceil_div(N, c.w);
     const double t = (double)ceil_div(tiles, sms / ctas) * c.step;
     if (t < best_t) { best_t = t; best = i; }
   }
@@ -633,20 +697,31 @@ static int fp8_large_choice(int64_t M, int64_t N, int sms) {
 
 void fp8_tile(int64_t M, int64_t N, int sms, int* tokens, int* rows) {
   if (M <= kFp8SmallM) return fp8_small_tile(M, N, sms, tokens, rows);
-  const Fp8LargeChoice& c = kChoices[fp8_large_choice(M, N, sms)];
+  const Fp8LargeChoice& c = kChoices[fp8_large_choice(M, N, sms, 0)];
   *tokens = c.pair ? 256 : 128;
   *rows = c.w;
 }
 
-template <bool kF32>
-static cudaError_t launch_large_any(const uint8_t* q, int64_t K, const uint8_t* w, int64_t ldw,
+template <bool kF32, bool kGrouped>
+static cudaError_t launch_large_any(const uint8_t* q, int64_t K, const uint8_t* w, int64_t ldw, int64_t lde,
                                     const Fp8LargeArgs& a, cudaStream_t st) {
-  switch (fp8_large_choice(a.M, a.N, num_sms())) {
-    case 0: return launch_large<true, 256, kF32>(q, K, w, ldw, a, st);
-    case 1: return launch_large<true, 128, kF32>(q, K, w, ldw, a, st);
-    case 2: return launch_large<false, 128, kF32>(q, K, w, ldw, a, st);
-    default: return launch_large<false, 64, kF32>(q, K, w, ldw, a, st);
+  switch (fp8_large_choice(a.M, a.N, num_sms(), kGrouped ? a.E : 0)) {
+    case 0: return launch_large<true, 256, kF32, kGrouped>(q, K, w, ldw, lde, a, st);
+    case 1: return launch_large<true, 128, kF32, kGrouped>(q, K, w, ldw, lde, a, st);
+    case 2: return launch_large<false, 128, kF32, kGrouped>(q, K, w, ldw, lde, a, st);
+    default: return launch_large<false, 64, kF32, kGrouped>(q, K, w, ldw, lde, a, st);
   }
+}
+
+// gemm_fp8_grouped for many rows an expert
+cudaError_t launch_gemm_fp8_grouped_large(const uint8_t* q, const float* scale, int64_t lds, int64_t M, int64_t K,
+                                          const int64_t* offsets, int64_t E, const uint8_t* w, int64_t ldw,
+                                          int64_t lde, const float* w_scale, int64_t N, void* out, bool out_f32,
+                                          int64_t ldo, uint32_t* err, cudaStream_t st) {
+  const Fp8LargeArgs a{scale, w_scale, out, lds, ldo, (int)M, (int)N, (int)ceil_div(K, 128),
+                       (int)ceil_div(N, 128), 0, 0, 0, err, offsets, (int)E};
+  return out_f32 ? launch_large_any<true, true>(q, K, w, ldw, lde, a, st)
+                 : launch_large_any<false, true>(q, K, w, ldw, lde, a, st);
 }
 
 cudaError_t launch_gemm_fp8(const uint8_t* q, const float* scale, int64_t lds, int64_t M, int64_t K,
@@ -657,9 +732,9 @@ cudaError_t launch_gemm_fp8(const uint8_t* q, const float* scale, int64_t lds, i
     return launch_gemm_fp8_small(q, scale, lds, M, K, w, ldw, w_scale, N, out, out_f32, ldo, err,
                                  pdl, st);
   Fp8LargeArgs a{scale, w_scale, out, lds, ldo, (int)M, (int)N, (int)ceil_div(K, 128),
-                 (int)ceil_div(N, 128), 0, 0, pdl, err};
-  return out_f32 ? launch_large_any<true>(q, K, w, ldw, a, st)
-                 : launch_large_any<false>(q, K, w, ldw, a, st);
+                 (int)ceil_div(N, 128), 0, 0, pdl, err, nullptr, 0};
+  return out_f32 ? launch_large_any<true, false>(q, K, w, ldw, 0, a, st)
+                 : launch_large_any<false, false>(q, K, w, ldw, 0, a, st);
 }
 
 }  // namespace qg

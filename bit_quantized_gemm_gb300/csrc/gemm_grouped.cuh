@@ -1,0 +1,58 @@
+// gemm_grouped.cuh -- the tiles of a product grouped by expert, found on the device.
+#pragma once
+
+#include "qg_common.cuh"
+
+namespace qg {
+
+// Expert e owns rows first[e] up to first[e + 1] (the offsets, those outside 0..M
+// taken as 0 or M; an expert that ends before it begins has none). It has ceil(rows
+// / T) tiles of T rows (before[e] of them lie ahead of its own) times NT tiles of
+// weight rows, the rows' tiles of one weight tile after one another: weights come
+// from HBM once.
+struct GroupedTiles {
+  const int *first, *before;  // [E + 1] each, in shared memory
+  int E, NT;
+  // bytes of the two lists
+  static __host__ __device__ constexpr int bytes(int E) { return 2 * (E + 1) * 4; }
+  // filled by one warp
+  static __device__ void fill(const int64_t* offsets, int E, int M, int T, int* first, int* before) {
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+    for (int e0 = 0; e0 <= E; e0 += 32) {
+      const int e = e0 + lane;
+      auto row = [&](int i) { return (int)min(max(__ldg(offsets + min(i, E)), (int64_t)0), (int64_t)M); };
+      const int lo = row(e), n = e < E ? max(row(e + 1) - lo, 0) : 0;
+      const int t = (n + T - 1) / T;
+      int s = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += v;
+      }
+      if (e <= E) {
+        first[e] = lo;
+        before[e] = base + s - t;
+      }
+      base += __shfl_sync(0xffffffffu, s, 31);
+    }
+  }
+  __device__ int total() const { return before[E] * NT; }
+  // the expert of tile t, the number of its tile of rows and of weight rows; by a
+  // whole warp (a 32-way search)
+  __device__ void at(int t, int& e, int& mi, int& ni) const {
+    const int lane = threadIdx.x & 31, row = t / NT;  // row: the tiles of rows, counted over the experts
+    int lo = 0;
+    for (int span = 1024; span > 1; span >>= 5) {
+      const int i = min(lo + lane * (span >> 5), E);
+      lo += (__popc(__ballot_sync(0xffffffffu, before[i] <= row)) - 1) * (span >> 5);
+      lo = min(lo, E - 1);
+    }
+    e = lo;
+    const int k = before[e + 1] - before[e], idx = t - before[e] * NT;
+    ni = idx / k;
+    mi = idx - ni * k;
+  }
+};
+
+}  // namespace qg
