@@ -10,10 +10,15 @@
 //
 // Every CTA forms the list of tiles from the offsets (a scan over the experts,
 // then a 32-way search per tile) and takes every gridDim-th tile of it: no
-// kernel before this one, no workspace, nothing to wait for on the host. A tile
-// is R weight rows of one expert (the MMA's long operand, in tensor-memory
-// lanes) and up to BM of its rows (columns); the tiles of the same weights
-// follow one another, so that weights come from HBM once.
+// kernel before this one, no workspace, nothing to wait for on the host.
+//
+// Few rows an expert: bound by reading the weights once, as gemm_fp8 of few tokens,
+// and made alike: a tile is R weight rows of one expert (the MMA's long operand, in
+// tensor-memory lanes) and up to BM of its rows (columns), a persistent CTA's ring of
+// TMA loads runs on from tile to tile, blocks of 128 accumulate from zero in buffers
+// of their own. The tiles of the same weights follow one another, so that weights
+// come from HBM once. 512 rows of 64 experts, 2560 -> 2432: 64 us, 6.3 TB/s.
+// Many rows an expert: the prefill kernel's tiles (gemm_fp8_large.cu).
 #include <cuda.h>
 
 #include "gemm_grouped.cuh"
@@ -334,13 +339,19 @@ cudaError_t launch_gemm_fp8_grouped(const uint8_t* q, const float* scale, int64_
                                     uint32_t* err, cudaStream_t st) {
   const Fp8GroupedArgs a{offsets, w_scale, out, ldo, (int)M, (int)N, (int)E, (int)ceil_div(K, 128),
                          (int)ceil_div(N, 128), 0, out_f32, err};
-  const int64_t mean = M / E;
-  if (ceil_div(N, 64) * (M < E ? M : E) <= num_sms())
-    return launch_grouped<64, 16>(q, scale, lds, K, w, ldw, lde, a, st);
-  if (mean <= 12) return launch_grouped<128, 16>(q, scale, lds, K, w, ldw, lde, a, st);
+  // Tiles of 16 columns while all of them run at once (at most one more than the full
+  // ones for every expert with rows): weights in 64 rows, 1 row of 64 experts, 17408 ->
+  // 2560 18.7 us (128 rows 24.7), else in 128, 100 rows of 2 experts, 2560 -> 2432 7.9
+  // (32 columns 8.7; the prefill kernel 9.9). Then by the mean rows of an expert: 512
+  // rows of 64 experts 64.0, 65.6, 70.1; 2048 rows 78.8, 71.1, 73.8; 3000 rows 99, 83,
+  // 72.8; 160 rows of 8 13.8, 14.8, 14.1.
+  const int64_t tiles = (M < E ? M : E) + M / 16, mean = M / E;
+  if (ceil_div(N, 64) * tiles <= num_sms()) return launch_grouped<64, 16>(q, scale, lds, K, w, ldw, lde, a, st);
+  if (ceil_div(N, 128) * tiles <= num_sms() || mean <= 12)
+    return launch_grouped<128, 16>(q, scale, lds, K, w, ldw, lde, a, st);
   if (mean <= 32) return launch_grouped<128, 32>(q, scale, lds, K, w, ldw, lde, a, st);
-  if (mean <= 64) return launch_grouped<128, 64>(q, scale, lds, K, w, ldw, lde, a, st);
-  return launch_gemm_fp8_grouped_large(q, scale, lds, M, K, offsets, E, w, ldw, lde, w_scale, N, out, out_f32, ldo, err, st);
+  return launch_gemm_fp8_grouped_large(q, scale, lds, M, K, offsets, E, w, ldw, lde, w_scale, N, out, out_f32, ldo, err,
+                                       st);
 }
 
 }  // namespace qg

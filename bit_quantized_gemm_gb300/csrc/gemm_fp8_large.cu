@@ -34,6 +34,13 @@
 // Outputs are staged per warp in shared memory (32 rows of 64 bytes, swizzled)
 // and leave by TMA, or by coalesced element stores where the row length or the
 // pitch is not a multiple of 16 bytes.
+//
+// Grouped by expert (kGrouped), the tiles are those of each expert's rows, listed by
+// every CTA for itself, the weights a third dimension of their tensor map. An
+// expert's last rows leave in 16-byte stores (straight from the registers, all of
+// them: 161 us, 147 as it is). 16384 rows of 64 experts, 2560 -> 2432: 144-147 us, of
+// which 110 are the blocks of 128 x 128 tiles at 276 ns (a fifth of their rows lies
+// behind an expert's last) and the rest the tiles' ends.
 #include <cuda.h>
 
 #include <cstring>

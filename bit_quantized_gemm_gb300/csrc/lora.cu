@@ -225,7 +225,6 @@ __global__ void __launch_bounds__(32 * kExpandWarps) lora_expand_few_kernel(cons
   }
   __syncthreads();
   int used = -1;  // the slot in use, counted from the first
-  bool ok = true;
   for (int row = 0; row < rows && cols > 0; ++row) {
     load_base(row + 1, raw_next);
     if (with >> row & 1) {
@@ -235,7 +234,7 @@ __global__ void __launch_bounds__(32 * kExpandWarps) lora_expand_few_kernel(cons
           ask();
         }
         ++used;
-        if (ok) ok = mbar_wait_warp(&full[warp][used % kExpandRing], (uint32_t)(used / kExpandRing) & 1u, err);
+        mbar_wait_warp(&full[warp][used % kExpandRing], (uint32_t)(used / kExpandRing) & 1u, err);
       }
       const uint8_t* from = ring + (used % kExpandRing) * slot_bytes;
       const int eights = rank >> 3;
@@ -761,7 +760,7 @@ __global__ void __launch_bounds__(256) lora_join_kernel(const LoraArgs a) {
 // it lies in shared memory and stores it from there. A tile's second product is a
 // tcgen05 MMA of 128 rows x kN columns: A operand h (large and small parts, in
 // shared memory as long as the CTA stays with its 128 rows), B operand kN rows of
-// B, into one of four accumulators in tensor memory. Where a tile's rows have
+// B, into an accumulator in tensor memory. Where a tile's rows have
 // several adapters, it is multiplied with each, and every row (a lane of tensor
 // memory, a thread) adds the one that is its own. The tiles, columns fastest, are
 // cut into `sections`, and each of them evenly over the CTAs: shares of some dozen
@@ -774,9 +773,13 @@ template <bool kBf16, int kHalves>  // 64 ranks each
 struct ExpandMany {
   static constexpr int kN = kBf16 ? 64 : 32;  // columns of a tile: 128 bytes of a row
   static constexpr int kBase = 128 * 128, kB = kN * 128 * kHalves, kH = 128 * 128;
-  static constexpr int kBaseRing = kHalves == 2 ? 7 : 8, kBRing = kHalves == 2 ? 3 : 4, kSlots = 4;
+  static constexpr int kBaseRing = kHalves == 2 ? 6 : 8, kBRing = kHalves == 2 ? 3 : 4, kSlots = 4;
   static constexpr int kHBytes = 2 * kHalves * kH, kHRing = kHalves == 2 ? 1 : 2;
   static constexpr int kThreads = 64 + 32 * 8;
+  // A set waits for its own tiles alone, and a wait on a barrier tells a phase from
+  // the next one only: every slot of base and every accumulator is one set's (even
+  // rings; two accumulators each).
+  static_assert(kBaseRing % 2 == 0 && kSlots == 4, "slots of one set");
   static constexpr size_t kSmem = kBaseRing * kBase + kBRing * kB + kHRing * kHBytes + 1024;
 };
 
@@ -830,9 +833,12 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
   }
   if (warp == 0) {
     if (elect_one()) {
-      tma_prefetch_desc(&tmBase);
       tma_prefetch_desc(&tmB);
-      tma_prefetch_desc(&tmOut);
+      tma_prefetch_desc(&tmH);
+      if (aligned) {
+        tma_prefetch_desc(&tmBase);
+        tma_prefetch_desc(&tmOut);
+      }
     }
     __syncwarp();
   }
@@ -945,15 +951,20 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
     constexpr uint32_t idesc = idesc_bf16_f32(128, kN);
     const int steps = (a.rank + 15) / 16;
     bool ok = true;
-    int sB = 0, d = 0, sH = 0;
-    uint32_t phaseB = 0, phaseD = 1, phaseH = 0;
+    int sB = 0, sH = 0;
+    uint32_t phaseB = 0, phaseH = 0;
+    uint32_t n = 0, units0 = 0, units1 = 0;  // tiles; products for either set so far
     while (ok && advance()) {
-      if (!T.count) continue;
+      if (!T.count) {
+        n += c1 - c0;
+        continue;
+      }
       ok = mbar_wait_warp(&h_full[sH], phaseH, err);
       const uint32_t ha = smem_u32(sh + sH * C::kHBytes);
-      for (int c = c0; c < c1 && ok; ++c)
+      for (int c = c0; c < c1 && ok; ++c, ++n)
         for (int i = 0; i < T.count; ++i) {
-          ok = mbar_wait_warp2(&b_full[sB], phaseB, &d_empty[d], phaseD, err);
+          const uint32_t u = n & 1 ? units1++ : units0++, d = 2 * (n & 1) + (u & 1);
+          ok = mbar_wait_warp2(&b_full[sB], phaseB, &d_empty[d], (u >> 1 & 1) ^ 1, err);
           if (!ok) break;
           tc_fence_after();
           const uint32_t ba = smem_u32(sb + sB * C::kB);
@@ -968,7 +979,6 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
           }
           __syncwarp();
           if (++sB == C::kBRing) { sB = 0; phaseB ^= 1; }
-          if (++d == C::kSlots) { d = 0; phaseD ^= 1; }
         }
       if (++sH == C::kHRing) { sH = 0; phaseH ^= 1; }
     }
@@ -984,23 +994,20 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
     bool ok = true;
     int last = -1;
     uint32_t* const stage = reinterpret_cast<uint32_t*>(sx) + set * 128 * (kN + 1);  // (not `aligned`)
-    uint32_t n = 0, units = 0;  // tiles, and products of a tile with one adapter, so far
+    uint32_t n = 0, units = 0;  // tiles, and products for this set, so far
     griddep_wait();  // (out may be what a kernel before reads, too)
     while (ok && advance()) {
       const int64_t w0 = m0 + quarter * 32;
       for (int c = c0; c < c1 && ok; ++c, ++n) {
-        if ((n & 1) != set) {
-          units += T.count;
-          continue;
-        }
+        if ((n & 1) != set) continue;
         const uint32_t s = n % C::kBaseRing;
         if (aligned) ok = mbar_wait_warp(&base_full[s], n / C::kBaseRing & 1, err);
         if (!ok) break;
         uint8_t* const row = sx + s * C::kBase + (quarter * 32 + lane) * 128;
         for (int k = 0; k < T.count; ++k, ++units) {
           const int id = T.at(k);
-          const uint32_t d = units % C::kSlots;
-          ok = mbar_wait_warp(&d_full[d], units / C::kSlots & 1, err);
+          const uint32_t d = 2 * set + (units & 1);
+          ok = mbar_wait_warp(&d_full[d], units >> 1 & 1, err);
           if (!ok) break;
           if (__any_sync(0xffffffffu, mine == id)) {
             tc_fence_after();

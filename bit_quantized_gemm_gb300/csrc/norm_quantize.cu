@@ -132,7 +132,6 @@ constexpr int kNormRegs = kU == 4 ? 64 : kU == 2 ? (kBf16 ? 56 : 96) : kBf16 ? 4
 // have a row each). A warp holds kU units of 512 values.
 template <bool kBf16, bool kWBf16, bool kFp8, int kU>
 __global__ void __maxnreg__((kNormRegs<kBf16, kWBf16, kU>)) norm_quantize_kernel(const NormArgs a) {
-  griddep_launch_dependents();
   // sums by group and unit (at most kNormMaxUnits), int8 maxima by group and warp
   __shared__ float part[kNormMaxUnits], top[kNormMaxWarps];
   const int lane = threadIdx.x, warp = threadIdx.y, W = blockDim.y, group = threadIdx.z;
@@ -293,7 +292,6 @@ __global__ void __launch_bounds__(128) silu_mul_quantize_kernel(const void* __re
                                                                 int64_t units, int units_per_row,
                                                                 uint8_t* __restrict__ q, float* __restrict__ scale,
                                                                 int64_t lds) {
-  griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (unit >= units) return;

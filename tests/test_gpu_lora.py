@@ -121,7 +121,8 @@ def test_bits_of_a_row_do_not_depend_on_the_others(x):
 
 
 @pytest.mark.parametrize("x,out,rank", [(BF16, BF16, 64), (BF16, F32, 128), (F32, BF16, 8), (BF16, BF16, 72)])
-@pytest.mark.parametrize("m,n", [(129, 64), (200, 1000), (384, 5120), (1000, 328), (2049, 136)])
+@pytest.mark.parametrize("m,n", [(129, 64), (200, 1000), (384, 5120), (1000, 328), (2049, 136), (130, 1), (257, 63),
+                                 (999, 333), (300, 2051)])
 def test_many_rows(m, n, x, out, rank):
     # runs of rows, some without an adapter; a tile of rows of one adapter, of several, of none
     base, xs, a, b, ids, scaling = inputs(m + n, m, 528, n, rank, 9, x, out)
@@ -134,11 +135,16 @@ def test_many_rows(m, n, x, out, rank):
         assert torch.equal(mine, got)
 
 
-def test_many_rows_of_many_adapters():
-    # more adapters in 128 rows than accumulators or slots
-    base, xs, a, b, _, scaling = inputs(8, 300, 272, 200, 16, 128)
-    ids = torch.arange(300, device=DEV) * 37 % 128
+@pytest.mark.parametrize("n", [200, 10000, 10001])
+@pytest.mark.parametrize("count", [3, 4, 5, 9, 128])
+@pytest.mark.parametrize("out,rank", [(BF16, 16), (F32, 72)])
+def test_many_rows_of_many_adapters(n, count, out, rank):
+    # more adapters in 128 rows than accumulators or slots, in several tiles of a CTA
+    base, xs, a, b, _, scaling = inputs(8, 300, 272, n, rank, count, BF16, out)
+    ids = torch.arange(300, device=DEV) * 37 % count
     check(qg.add_lora(base, xs, a, b, ids, scaling), base, xs, a, b, ids, scaling)
+    runs = (torch.arange(300, device=DEV) // 23) % (count + 1) - 1
+    check(qg.add_lora(base, xs, a, b, runs, scaling), base, xs, a, b, runs, scaling)
 
 
 def test_rows_without_an_adapter_keep_their_bits():

@@ -156,6 +156,9 @@ def test_norm_bits_of_a_row(k, dtype):
     mine, out_q = res.clone(), torch.empty_like(q)
     a, b, c = qg.rmsnorm_quantize_act_fp8(x, w, residual=mine, out=(out_q, room[:, :m], mine))
     assert c is mine and torch.equal(mine, total) and torch.equal(out_q.view(torch.uint8), q.view(torch.uint8))
+    mine = x.clone()
+    a, b, c = qg.rmsnorm_quantize_act(mine, w, residual=res, out=(q8.clone(), s8.clone(), None, None, mine))[:3]
+    assert torch.equal(a, q8) and torch.equal(b, s8) and torch.equal(mine, total)
     assert torch.equal(room[:, :m], scale) and bool((room[:, m:] == 7.0).all())
 
 
