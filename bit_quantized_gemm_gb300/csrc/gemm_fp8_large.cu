@@ -38,9 +38,9 @@
 // Grouped by expert (kGrouped), the tiles are those of each expert's rows, listed by
 // every CTA for itself, the weights a third dimension of their tensor map. An
 // expert's last rows leave in 16-byte stores (straight from the registers, all of
-// them: 161 us, 147 as it is). 16384 rows of 64 experts, 2560 -> 2432: 144-147 us, of
-// which 110 are the blocks of 128 x 128 tiles at 276 ns (a fifth of their rows lies
-// behind an expert's last) and the rest the tiles' ends.
+// them: 161 us where it was 147). 16384 rows of 64 experts, 2560 -> 2432: 138 us. A
+// fifth of the tiles' rows lies behind an expert's last; of 6.6 us a tile of 128 x 128
+// the blocks take 5.0 (250 ns each: L2 delivers 13 TB/s then), the stores 1.3.
 #include <cuda.h>
 
 #include <cstring>
@@ -117,7 +117,7 @@ struct Fp8LargeCfg {
   static constexpr int kFit = (226 * 1024 - kFixed) / ((int)kStage + kScaleBytes);
   static constexpr int kStages = kFit > 4 ? 4 : kFit;
   static constexpr size_t kSmem = (size_t)kStages * (kStage + kScaleBytes) + kFixed;
-  static_assert(W % 64 == 0 && W <= 256 && kCols % kRound == 0 && kStages >= 3, "tile");
+  static_assert(W % 64 == 0 && W <= 256 && kCols % kRound == 0 && kStages >= (kGrouped ? 2 : 3), "tile");
 };
 
 template <bool kPair, int W, bool kF32, bool kGrouped>
@@ -684,18 +684,26 @@ struct Fp8LargeChoice {
   int w;
   double step;
 };
-static const Fp8LargeChoice kChoices[] = {{true, 256, 481}, {true, 128, 252}, {false, 128, 276}, {false, 64, 236}};
+// Grouped by expert there is a fifth, 128 x 256: as much of the weights a token as a
+// pair has, in tiles of half the tokens (a ring of two stages: of no use in the
+// other). us, 128 x 128 and 128 x 256: 16384 rows of 64 experts, 2560 -> 2432 143.6,
+// 138.1; of 32, 2560 -> 4864 225, 216; 1024 rows of 8, 2560 -> 2432 20.6, 18.2; 4096 rows
+// of 32 50.2, 57.2.
+static const Fp8LargeChoice kChoices[] = {
+    {true, 256, 481}, {true, 128, 252}, {false, 128, 276}, {false, 64, 236}, {false, 256, 482}};
 
 // the tile of the smallest estimated time: waves x ns per block. (Rows of `experts`:
-// the last tile of each is taken as half full.)
+// the last tile of each is taken as half full,
+// and each has one.)
 static int fp8_large_choice(int64_t M, int64_t N, int sms, int64_t experts) {
   int best = 3;
   double best_t = 1e300;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < (experts ? 5 : 4); ++i) {
     const Fp8LargeChoice& c = kChoices[i];
     const int ctas = c.pair ? 2 : 1;
     if (sms < ctas) continue;
-    const int64_t tiles = (ceil_div(M, 128 * ctas) + experts / 2) * ceil_div(N, c.w);
+    const int64_t full = ceil_div(M, 128 * ctas) + experts / 2, least = M < experts ? M : experts;
+    const int64_t tiles = (full > least ? full : least) * ceil_div(N, c.w);
     const double t = (double)ceil_div(tiles, sms / ctas) * c.step;
     if (t < best_t) { best_t = t; best = i; }
   }
@@ -716,6 +724,9 @@ static cudaError_t launch_large_any(const uint8_t* q, int64_t K, const uint8_t* 
     case 0: return launch_large<true, 256, kF32, kGrouped>(q, K, w, ldw, lde, a, st);
     case 1: return launch_large<true, 128, kF32, kGrouped>(q, K, w, ldw, lde, a, st);
     case 2: return launch_large<false, 128, kF32, kGrouped>(q, K, w, ldw, lde, a, st);
+    case 4:
+      if constexpr (kGrouped) return launch_large<false, 256, kF32, kGrouped>(q, K, w, ldw, lde, a, st);
+      return cudaErrorInvalidValue;
     default: return launch_large<false, 64, kF32, kGrouped>(q, K, w, ldw, lde, a, st);
   }
 }
