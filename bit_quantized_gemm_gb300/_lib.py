@@ -513,9 +513,9 @@ def _ptr_or_none(t):
 
 def rmsnorm_quantize_act_fp8(x, weight, eps=1e-6, residual=None, out=None, stream=None):
     """Norm of the rows of x (cuda [M, K] bf16/fp32, rows may be strided; K % 16 == 0), or of
-    x + residual, times weight (bf16/fp32 [K]), quantized as by quantize_act_fp8 -> (q float8_e4m3fn
-    [M, K], scale fp32 [ceil(K/128), M], x + residual in x's dtype or None). `out` may supply
-    preallocated (q, scale, sum); sum may be residual or x itself."""
+    x + residual, times weight (bf16/fp32 [K]), quantized in the layout of quantize_act_fp8, by products
+    with 1/s -> (q float8_e4m3fn [M, K], scale fp32 [ceil(K/128), M], x + residual in x's dtype or
+    None). `out` may supply preallocated (q, scale, sum); sum may be residual or x itself."""
     M, K, ldx, ldr, dev = _norm_inputs(x, weight, residual)
     _device(x, stream)
     if out is None:
@@ -541,7 +541,7 @@ def rmsnorm_quantize_act_fp8(x, weight, eps=1e-6, residual=None, out=None, strea
 
 def rmsnorm_quantize_act(x, weight, eps=1e-6, residual=None, block_sums=False, q16=False, out=None,
                          stream=None, int8=True):
-    """As rmsnorm_quantize_act_fp8, quantized as by quantize_act (K % 32 == 0) -> (q int8 [M, K] or
+    """As rmsnorm_quantize_act_fp8, in the layout of quantize_act (K % 32 == 0) -> (q int8 [M, K] or
     None, scale fp32 [M], block_sums int32 [M, K/32] or None, q16 fp16 [M, K] or None, x + residual
     or None). `out` may supply preallocated (q, scale, block_sums, q16, sum)."""
     M, K, ldx, ldr, dev = _norm_inputs(x, weight, residual)
@@ -575,7 +575,7 @@ def rmsnorm_quantize_act(x, weight, eps=1e-6, residual=None, block_sums=False, q
 
 def silu_mul_quantize_act_fp8(x, out=None, stream=None):
     """x: cuda [M, 2K] bf16/fp32 (rows may be strided; K % 16 == 0), K gates and K values up a row ->
-    silu(gate) * up quantized as by quantize_act_fp8: (q float8_e4m3fn [M, K], scale fp32
+    silu(gate) * up quantized as by rmsnorm_quantize_act_fp8: (q float8_e4m3fn [M, K], scale fp32
     [ceil(K/128), M]). `out` may supply preallocated (q, scale)."""
     M, K2, ldx = _rows(x, "x", _CODES)
     if K2 % 2:
@@ -663,7 +663,9 @@ def add_lora(base, x, a, b, ids, scaling=None, out=None, workspace=None, stream=
     the projection's output; x: cuda [M, K] bf16/fp32, its input (K % 16 == 0); rows of both may be
     strided; a, b: contiguous cuda bf16 [adapters, rank, K], [adapters, N, rank] (rank a multiple of 8,
     at most 128); ids: cuda int64 [M]; scaling: cuda fp32 [adapters] or None for 1 -> out [M, N] of
-    base's dtype. `out` may be base itself. Through `workspace` (allocated here when not given)."""
+    base's dtype. `out` may be base itself. Through `workspace` (allocated here when not given). A
+    row's bits do not depend on the other rows among calls of up to 128 rows, nor among calls of more
+    (tensor cores, where x of one adapter's rows in a row costs least)."""
     M, N, ldb = _rows(base, "base", _CODES)
     dev = _device(base, stream)
     m, K, ldx = _rows(x, "x", _CODES, dev)

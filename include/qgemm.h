@@ -335,23 +335,28 @@ qg_status qg_linear_fp8(const void* x, qg_dtype x_dtype, int64_t M, int64_t K, i
                         void* stream);
 
 /* ------------------------------------------------------------------------ */
-/* Root-mean-square norm of each row, with the residual's addition, into 8-bit */
-/* activations with their scales: what stands before a projection.            */
-/*   h = x + residual, rounded to x_dtype and written to sum (h = x without a  */
-/*       residual: residual and sum both NULL)                                 */
-/*   y = (h * (1 / sqrt(sum h^2 / K + eps))) * weight   (fp32 throughout)      */
-/* and y is quantized as qg_quantize_act_fp8 (the first call) or               */
-/* qg_quantize_act (the second) quantizes fp32 values; there is no rounding in  */
-/* between. The norm reads h as it is stored: a call on x and a residual gives  */
-/* the bits of a call on their sum. A row's bits do not depend on the other     */
-/* rows of its call. NaN and infinities spread by IEEE rules: a NaN makes a      */
-/* row's scales NaN; an infinity (r is 0 then) makes its block's scale NaN       */
-/* (int8: the row's, with q 0) and the row's products with it.                   */
-/*   x, residual, sum  [M][ld*] of x_dtype, rows of K values, 16-byte aligned,  */
-/*          ld* >= K, ld*elem_size % 16 == 0. sum may be x or residual itself.  */
-/*   weight [K] of weight_dtype, 16-byte aligned. eps >= 0.                     */
-/*   q, scale, lds (fp8), q, scale, block_sums, q16 (int8): as the two calls     */
-/*          named above write them. K as there (a multiple of 16; of 32).        */
+/* Root-mean-square norm of each row, with the residual's addition, into    */
+/* 8-bit activations with their scales: what stands before a projection.    */
+/*   h = x + residual, rounded to x_dtype and written to sum (h = x without */
+/*       a residual: residual and sum both NULL)                            */
+/*   y = (h * (1 / sqrt(sum h^2 / K + eps))) * weight   (fp32)              */
+/*   q = e4m3(y * fl(1/s)), s = max |y| * fl(1/448) over 128 values; or     */
+/*   q = rint(y * fl(1/s)), s = max |y| / 127 over the row (int8)           */
+/* with no rounding between y and q. (The quantizers above divide by s; a   */
+/* product differs beside ties alone.) The norm reads h as it is stored: a  */
+/* call on x and a residual gives the bits of a call on their sum. A row's  */
+/* bits do not depend on the other rows of its call. NaN and infinities     */
+/* spread by IEEE rules: a NaN makes a row's scales NaN; an infinity        */
+/* (1/sqrt is 0 then) makes its block's scale NaN (int8: the row's), and    */
+/* the row's products with it. int8: q is 0 where the scale is 0 or not     */
+/* finite.                                                                  */
+/*   x, residual, sum  [M][ld*] of x_dtype, rows of K values, 16-byte       */
+/*             aligned, ld* >= K, ld*elem_size % 16 == 0. sum may be x or   */
+/*             residual itself.                                             */
+/*   weight    [K] of weight_dtype, 16-byte aligned; eps >= 0.              */
+/*   q, scale, lds, block_sums, q16  as qg_quantize_act_fp8 and             */
+/*             qg_quantize_act write them (block_sums may be NULL, and one  */
+/*             of q and q16); K as there.                                   */
 /* ------------------------------------------------------------------------ */
 qg_status qg_rmsnorm_quantize_act_fp8(const void* x, const void* residual, qg_dtype x_dtype,
                                       int64_t M, int64_t K, int64_t ldx, int64_t ldr,
@@ -365,29 +370,33 @@ qg_status qg_rmsnorm_quantize_act(const void* x, const void* residual, qg_dtype 
                                   void* stream);
 
 /* ------------------------------------------------------------------------ */
-/* silu(gate) * up into e4m3 activations: what stands between the two          */
-/* projections of an MLP. Row m of x holds K gates, then K values up:          */
-/*   y = g / (1 + e^-g) * u  (fp32, off by less than (8 + |g|) 2^-23 of itself;  */
-/*       e^-|g| below 2^-126 counts as 0), quantized as qg_quantize_act_fp8.     */
-/*   x [M][ldx] of x_dtype, rows of 2K values, 16-byte aligned, ldx >= 2K,      */
-/*     ldx*elem_size % 16 == 0; q, scale, lds, K as for qg_quantize_act_fp8.     */
+/* silu(gate) * up into e4m3 activations: what stands between the two       */
+/* projections of an MLP. Row m of x holds K gates, then K values up:       */
+/*   y = g / (1 + e^-g) * u   (fp32, off by less than (8 + |g|) * 2^-23 of  */
+/*       itself; e^-|g| below 2^-126 counts as 0)                           */
+/* and y is quantized to e4m3 as by the norm above.                         */
+/*   x         [M][ldx] of x_dtype, rows of 2K values, 16-byte aligned, ldx */
+/*             >= 2K, ldx*elem_size % 16 == 0.                              */
+/*   q, scale, lds  as for qg_quantize_act_fp8; K as there.                 */
 /* ------------------------------------------------------------------------ */
 qg_status qg_silu_mul_quantize_act_fp8(const void* x, qg_dtype x_dtype, int64_t M, int64_t K,
                                        int64_t ldx, uint8_t* q, float* scale, int64_t lds,
                                        void* stream);
 
 /* ------------------------------------------------------------------------ */
-/* qg_gemm_fp8 with the weights of each row's expert. The rows are sorted by    */
-/* expert: expert e owns rows offsets[e] <= m < offsets[e+1]; other rows of out */
-/* are left as they were. A row's bits are those of qg_gemm_fp8 with its        */
-/* expert's weights.                                                            */
-/*   offsets  [experts+1] int64 on the device, ascending. Values outside 0..M   */
-/*            are taken as 0 or M, an expert that ends before it begins has no   */
-/*            rows; where two experts claim a row, either's result may stand.    */
-/*   w        [experts] matrices [N][ldw] of e4m3, lde bytes from one to the     */
-/*            next (a multiple of 16, no overlap).                               */
-/*   w_scale  [experts][ceil(N/128)][ceil(K/128)] fp32, 4-byte aligned.          */
-/*   1 <= experts <= 1024; all else as for qg_gemm_fp8.                          */
+/* qg_gemm_fp8 with the weights of each row's expert. The rows are sorted   */
+/* by expert: expert e owns rows offsets[e] <= m < offsets[e+1]; other rows */
+/* of out are left as they were. A row's bits are those of qg_gemm_fp8 with */
+/* its expert's weights, whatever the other rows are.                       */
+/*   offsets   [experts+1] int64 on the device, ascending; read there, so   */
+/*             that nothing waits for the host. Values outside 0..M are     */
+/*             taken as 0 or M, an expert that ends before it begins has no */
+/*             rows; where two experts claim a row, either's result may     */
+/*             stand.                                                       */
+/*   w         [experts] matrices [N][ldw] of e4m3, lde bytes from one to   */
+/*             the next (a multiple of 16, no overlap).                     */
+/*   w_scale   [experts][ceil(N/128)][ceil(K/128)] fp32, 4-byte aligned.    */
+/* 1 <= experts <= 1024; all else as for qg_gemm_fp8.                       */
 /* ------------------------------------------------------------------------ */
 qg_status qg_gemm_fp8_grouped(const uint8_t* q, const float* scale, int64_t lds, int64_t M, int64_t K,
                               const int64_t* offsets, int64_t experts, const uint8_t* w, int64_t ldw,
@@ -395,27 +404,32 @@ qg_status qg_gemm_fp8_grouped(const uint8_t* q, const float* scale, int64_t lds,
                               qg_dtype out_dtype, int64_t ldo, void* stream);
 
 /* ------------------------------------------------------------------------ */
-/* Low-rank adapters of many requests beside a shared projection:               */
-/*   h[m][r]   = sum_k x[m][k] * a[id][r][k]                     id = ids[m]     */
-/*   out[m][n] = base[m][n] + sum_r (scaling[id] * h[m][r]) * b[id][n][r]        */
-/* in fp32 (scaling * h as the sum of two bf16 numbers, off by 2^-17 of itself;  */
-/* fp32 x as the sum of three), rounded once to dtype. A row whose id is outside */
-/* 0..adapters-1 keeps base's bits. Rows may come in any order; rows of one       */
-/* adapter that follow one another cost least. A row's bits do not depend on the  */
-/* other rows of its call.                                                        */
-/*   base, out  [M][ldb], [M][ldo] of dtype, rows of N values, aligned to their   */
-/*            elements (fastest where rows start on 16 bytes). out may be base     */
-/*            itself (with ldo = ldb); it overlaps nothing else of the call.       */
-/*   x        [M][ldx] of x_dtype, rows of K values, 16-byte aligned, ldx >= K,    */
-/*            ldx*elem_size % 16 == 0.                                              */
-/*   a, b     bf16 [adapters][rank][K], [adapters][N][rank], 16-byte aligned;      */
-/*            adapters of a smaller rank are filled up with zeros.                  */
-/*   ids      [M] int64; scaling [adapters] fp32, or NULL for 1.                    */
-/*   workspace  qg_add_lora_workspace_bytes(M, K, rank) bytes (0: invalid sizes),   */
-/*            256-byte aligned, owned by the caller; calls that may run at once      */
-/*            need one each.                                                         */
-/* K % 16 == 0, K <= 65536; rank % 8 == 0, 8 <= rank <= QG_LORA_MAX_RANK;            */
-/* 1 <= M <= 2^20, 1 <= N <= 2^24, 1 <= adapters <= 2^20.                            */
+/* Low-rank adapters of many requests beside a shared projection:           */
+/*   h[m][r]   = sum_k x[m][k] * a[id][r][k]               id = ids[m]      */
+/*   out[m][n] = base[m][n] + sum_r (scaling[id] * h[m][r]) * b[id][n][r]   */
+/* in fp32, rounded once to dtype. A row whose id is outside 0..adapters-1  */
+/* keeps base's bits. Rows may come in any order; with more than 128 rows,  */
+/* rows of one adapter that follow one another cost least. Up to 128 rows   */
+/* the products run on the fp32 units; above that on the tensor cores,      */
+/* scaling * h as the sum of two bf16 numbers (off by 2^-17 of itself),     */
+/* fp32 x as the sum of three. Within either kind a row's bits do not       */
+/* depend on the other rows of its call.                                    */
+/*   base, out [M][ldb], [M][ldo] of dtype, rows of N values, aligned to    */
+/*             their elements (fastest where rows begin and end on 16       */
+/*             bytes). out may be base itself (with ldo = ldb); it overlaps */
+/*             nothing else of the call.                                    */
+/*   x         [M][ldx] of x_dtype, rows of K values, 16-byte aligned, ldx  */
+/*             >= K, ldx*elem_size % 16 == 0.                               */
+/*   a, b      bf16 [adapters][rank][K], [adapters][N][rank], 16-byte       */
+/*             aligned; adapters of a smaller rank are filled up with       */
+/*             zeros.                                                       */
+/*   ids       [M] int64.                                                   */
+/*   scaling   [adapters] fp32, or NULL for 1.                              */
+/*   workspace qg_add_lora_workspace_bytes(M, K, rank) bytes (0: invalid    */
+/*             sizes), 256-byte aligned, owned by the caller; calls that    */
+/*             may run at once need one each.                               */
+/* K % 16 == 0, K <= 65536; rank % 8 == 0, 8 <= rank <= QG_LORA_MAX_RANK; 1 */
+/* <= M <= 2^20, 1 <= N <= 2^24, 1 <= adapters <= 2^20.                     */
 /* ------------------------------------------------------------------------ */
 #define QG_LORA_MAX_RANK 128
 size_t qg_add_lora_workspace_bytes(int64_t M, int64_t K, int64_t rank);

@@ -2,8 +2,10 @@
 
 What a value y may be off by, relative to itself (half units of fp32, 2^-24):
   norm: the sum of squares is a chain of 16, a butterfly of 5, a chain of at most
-  4 and a butterfly of 5: 30, halved by the root; the quotient by K and + eps 2,
-  halved; root, reciprocal, two products 4. Together 20: below 2^-19.
+  4 and a butterfly of 5: 30, halved by the root; the quotient by K (2 ulp, 4 half
+  units) and + eps 1, halved; the refined reciprocal root 4 (1.5 times the square of
+  the hardware's 2^-22.9 vanishes; the step's own roundings), two products 2.
+  Together 24: below 2^-19.
   gate: (8 + |g|) * 2^-23, as the header states.
 The scale adds its constant's rounding and a product (int8: a quotient), 2 * 2^-24.
 A quantized value times its scale is then off from y by that, and by half a step:
