@@ -572,7 +572,9 @@ __global__ void __cluster_dims__(kManyParts, 1, 1) __launch_bounds__(192, RP == 
   T.load(a, m0);
   const int q = warp & 3, mine = q == 0 ? T.v[0] : q == 1 ? T.v[1] : q == 2 ? T.v[2] : T.v[3];  // of row 32 q + lane
   T.find();
-  if (T.count == 0) return;  // (every thread of the cluster)
+  const int per = (T.count + (int)gridDim.z - 1) / (int)gridDim.z;  // adapters of this cluster
+  const int i0 = per * (int)blockIdx.z, i1 = min(T.count, i0 + per);
+  if (i0 >= i1) return;  // (every thread of the cluster)
   if (warp == 0) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) ids[j * 32 + lane] = T.list[j];
@@ -610,8 +612,8 @@ __global__ void __cluster_dims__(kManyParts, 1, 1) __launch_bounds__(192, RP == 
   // of the producer and of the issuer: slots, phases (a fresh slot is free), loads so far
   int s = 0, sA = 0, loads = 0, loadsA = 0;
   uint32_t phase = warp == 0, phaseA = warp == 0, phaseD = 0;
-  for (int first = 0; first < T.count; first += C::kBatch) {
-    const int batch = min(C::kBatch, T.count - first);
+  for (int first = i0; first < i1; first += C::kBatch) {
+    const int batch = min(C::kBatch, i1 - first);
     if (warp == 0) {
       for (int k = k0; k < k1 && ok; ++k) {
         ok = mbar_wait_warp(&x_empty[s], phase, err);
@@ -639,18 +641,17 @@ __global__ void __cluster_dims__(kManyParts, 1, 1) __launch_bounds__(192, RP == 
     } else if (warp == 1) {
       constexpr uint32_t idesc = idesc_bf16_f32(128, RP);
       for (int k = k0; k < k1 && ok; ++k) {
+        const uint64_t xa = smem_desc_sw128(smem_u32(sx + s * C::kX));
         ok = mbar_wait_warp(&x_full[s], phase, err);
-        const uint32_t xa = smem_u32(sx + s * C::kX);
         for (int i = 0; i < batch && ok; ++i) {
+          const uint64_t aa = smem_desc_sw128(smem_u32(sa + sA * C::kA));
           ok = mbar_wait_warp(&a_full[sA], phaseA, err);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t aa = smem_u32(sa + sA * C::kA);
           if (elect_one()) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              mma_f16_ss(tmem + i * RP, smem_desc_sw128(xa + j * 32), smem_desc_sw128(aa + j * 32), idesc,
-                         k > k0 || j > 0);
+              mma_f16_ss(tmem + i * RP, xa + j * 2, aa + j * 2, idesc, k > k0 || j > 0);
             mma_commit(&a_empty[sA]);
             if (i + 1 == batch) mma_commit(&x_empty[s]);
             if (i + 1 == batch && k + 1 == k1) mma_commit(&d_full);
@@ -767,20 +768,27 @@ __global__ void __launch_bounds__(256) lora_join_kernel(const LoraArgs a) {
 // tiles of the same rows, from different places, so that rows of several adapters
 // are everybody's. Rows of base or out that do not lie on
 // 16-byte pieces (`aligned` false) are read and written element by element.
-// Warps: 0 producer, 1 MMA issuer, 2..5 and 6..9 epilogue (32 rows each): a tile's
-// waits, loads, additions and store follow one another, so the two sets take turns.
+// Warps: 0 producer, 1 and 10 issuers of MMAs, 2..5 and 6..9 epilogue (32 rows each): a
+// tile's waits, loads, additions and store follow one another, so the two sets take
+// turns, each with an issuer, accumulators and slots of B of its own. A product
+// takes its issuer 700 to 900 cycles, waits among them, so that two of them are what
+// tiles of several adapters need: 64 runs in 4096 rows, 5120 -> 17408, rank 64: 108 us,
+// 119 with one. A product alone in its tile takes the epilogue 1150 cycles, under the
+// time that the tile's bytes take. 4096 rows, 11 runs: 76.5 us, of one adapter 73.5: the
+// first kernel 10.5, a start and an end of 10, and base and out at 5.7 TB/s (a copy of
+// theirs through the same ring 48.8 us in all, through plain loads and stores 43.7).
 template <bool kBf16, int kHalves>  // 64 ranks each
 struct ExpandMany {
   static constexpr int kN = kBf16 ? 64 : 32;  // columns of a tile: 128 bytes of a row
   static constexpr int kBase = 128 * 128, kB = kN * 128 * kHalves, kH = 128 * 128;
-  static constexpr int kBaseRing = kHalves == 2 ? 6 : 8, kBRing = kHalves == 2 ? 3 : 4, kSlots = 4;
+  static constexpr int kBaseRing = kHalves == 2 ? 6 : 8, kBRing = 2, kSlots = 4;  // (B: of a set)
   static constexpr int kHBytes = 2 * kHalves * kH, kHRing = kHalves == 2 ? 1 : 2;
-  static constexpr int kThreads = 64 + 32 * 8;
+  static constexpr int kThreads = 96 + 32 * 8;
   // A set waits for its own tiles alone, and a wait on a barrier tells a phase from
   // the next one only: every slot of base and every accumulator is one set's (even
   // rings; two accumulators each).
   static_assert(kBaseRing % 2 == 0 && kSlots == 4, "slots of one set");
-  static constexpr size_t kSmem = kBaseRing * kBase + kBRing * kB + kHRing * kHBytes + 1024;
+  static constexpr size_t kSmem = kBaseRing * kBase + 2 * kBRing * kB + kHRing * kHBytes + 1024;
 };
 
 // how the tiles are dealt out: `sections` times the number of CTAs cells of `tiles`
@@ -799,13 +807,13 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
   constexpr int kN = C::kN;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t base_full[C::kBaseRing], base_empty[C::kBaseRing];
-  __shared__ uint64_t b_full[C::kBRing], b_empty[C::kBRing], d_full[C::kSlots], d_empty[C::kSlots], drain;
+  __shared__ uint64_t b_full[2 * C::kBRing], b_empty[2 * C::kBRing], d_full[C::kSlots], d_empty[C::kSlots], drain[2];
   __shared__ uint64_t h_full[C::kHRing], h_empty[C::kHRing];
   __shared__ uint32_t tmem_slot, tmem_busy;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sx = base;                                  // tiles of base [slot]
-  uint8_t* sb = sx + C::kBaseRing * C::kBase;          // B [slot][half]
-  uint8_t* sh = sb + C::kBRing * C::kB;                // h [slot][large, small][half]
+  uint8_t* sb = sx + C::kBaseRing * C::kBase;          // B [set][slot][half]
+  uint8_t* sh = sb + 2 * C::kBRing * C::kB;                // h [slot][large, small][half]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t CT = (a.N + kN - 1) / kN;
   const bool keep = a.base == a.out && a.ldb == a.ldo;  // rows without an adapter are in place
@@ -815,7 +823,7 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
       mbar_init(&base_full[i], 1);
       mbar_init(&base_empty[i], 4);
     }
-    for (int i = 0; i < C::kBRing; ++i) {
+    for (int i = 0; i < 2 * C::kBRing; ++i) {
       mbar_init(&b_full[i], 1);
       mbar_init(&b_empty[i], 1);
     }
@@ -825,9 +833,10 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
     }
     for (int i = 0; i < C::kHRing; ++i) {
       mbar_init(&h_full[i], 1);
-      mbar_init(&h_empty[i], 1);
+      mbar_init(&h_empty[i], 2);
     }
-    mbar_init(&drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     tmem_busy = 0;
     fence_barrier_init();
   }
@@ -893,10 +902,30 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
 
   if (warp == 0) {
     bool ok = true;
-    int s = 0, sB = 0, sH = 0, loads = 0, loadsB = 0, loadsH = 0;
-    uint32_t phase = 1, phaseB = 1, phaseH = 1;
-    griddep_wait();
+    int s = 0, sH = 0, loads = 0, loadsH = 0;
+    uint32_t phase = 1, phaseH = 1, n = 0;  // n: tiles so far
+    int loads0 = 0, loads1 = 0;  // of B, for either set
+    auto load_base = [&](int c) {
+      ok = mbar_wait_warp(&base_empty[s], phase, err);
+      if (!ok) return;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&base_full[s], C::kBase);
+        tma_load_2d(sx + s * C::kBase, &tmBase, &base_full[s], c * kN, (int)m0);
+      }
+      __syncwarp();
+      ++loads;
+      if (++s == C::kBaseRing) { s = 0; phase ^= 1; }
+    };
+    bool waited = false;
     while (ok && advance()) {
+      int from = c0;  // the tile of base that is next
+      if (!waited) {
+        // base is no work of the kernels before (and the slots are all free)
+        for (; aligned && ok && from < min(c1, c0 + C::kBaseRing); ++from) load_base(from);
+        griddep_wait();
+        waited = true;
+        if (!ok) break;
+      }
       if (T.count) {
         ok = mbar_wait_warp(&h_empty[sH], phaseH, err);
         if (!ok) break;
@@ -912,32 +941,27 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
         ++loadsH;
         if (++sH == C::kHRing) { sH = 0; phaseH ^= 1; }
       }
-      for (int c = c0; c < c1 && ok; ++c) {
-        if (aligned) {
-          ok = mbar_wait_warp(&base_empty[s], phase, err);
-          if (!ok) break;
-          if (elect_one()) {
-            mbar_arrive_expect_tx(&base_full[s], C::kBase);
-            tma_load_2d(sx + s * C::kBase, &tmBase, &base_full[s], c * kN, (int)m0);
-          }
-          __syncwarp();
-          ++loads;
-          if (++s == C::kBaseRing) { s = 0; phase ^= 1; }
-        }
-        for (int k = 0; k < T.count; ++k) {
+      for (int c = c0; c < c1 && ok; c += 2) {
+        const int both = min(2, c1 - c);
+        for (; aligned && ok && from < c + both; ++from) load_base(from);
+        for (int k = 0; k < T.count && ok; ++k) {
           const int id = T.at(k);
-          ok = mbar_wait_warp(&b_empty[sB], phaseB, err);
-          if (!ok) break;
-          if (elect_one()) {
-            mbar_arrive_expect_tx(&b_full[sB], C::kB);
+          for (int i = 0; i < both; ++i) {
+            const int set = (n + i) & 1, u = set ? loads1 : loads0, sB = set * C::kBRing + u % C::kBRing;
+            ok = mbar_wait_warp(&b_empty[sB], (u / C::kBRing & 1) ^ 1, err);
+            if (!ok) break;
+            if (elect_one()) {
+              mbar_arrive_expect_tx(&b_full[sB], C::kB);
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-              tma_load_3d(sb + sB * C::kB + h * kN * 128, &tmB, &b_full[sB], h * 64, c * kN, id);
+              for (int h = 0; h < kHalves; ++h)
+                tma_load_3d(sb + sB * C::kB + h * kN * 128, &tmB, &b_full[sB], h * 64, (c + i) * kN, id);
+            }
+            __syncwarp();
+            if (set) ++loads1;
+            else ++loads0;
           }
-          __syncwarp();
-          ++loadsB;
-          if (++sB == C::kBRing) { sB = 0; phaseB ^= 1; }
         }
+        n += both;
       }
     }
     // every load has landed before the CTA exits
@@ -945,48 +969,54 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
       mbar_wait_warp(&h_full[i % C::kHRing], (uint32_t)(i / C::kHRing) & 1u, err);
     for (int i = max(0, loads - C::kBaseRing); i < loads; ++i)
       mbar_wait_warp(&base_full[i % C::kBaseRing], (uint32_t)(i / C::kBaseRing) & 1u, err);
-    for (int i = max(0, loadsB - C::kBRing); i < loadsB; ++i)
+    for (int i = max(0, loads0 - C::kBRing); i < loads0; ++i)
       mbar_wait_warp(&b_full[i % C::kBRing], (uint32_t)(i / C::kBRing) & 1u, err);
-  } else if (warp == 1) {
+    for (int i = max(0, loads1 - C::kBRing); i < loads1; ++i)
+      mbar_wait_warp(&b_full[C::kBRing + i % C::kBRing], (uint32_t)(i / C::kBRing) & 1u, err);
+  } else if (warp == 1 || warp == 10) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, kN);
     const int steps = (a.rank + 15) / 16;
+    const uint32_t set = warp == 10;
     bool ok = true;
-    int sB = 0, sH = 0;
-    uint32_t phaseB = 0, phaseH = 0;
-    uint32_t n = 0, units0 = 0, units1 = 0;  // tiles; products for either set so far
+    int sH = 0;
+    uint32_t phaseH = 0;
+    uint32_t n = 0, units = 0;  // tiles; products for the set so far
     while (ok && advance()) {
       if (!T.count) {
         n += c1 - c0;
         continue;
       }
       ok = mbar_wait_warp(&h_full[sH], phaseH, err);
-      const uint32_t ha = smem_u32(sh + sH * C::kHBytes);
-      for (int c = c0; c < c1 && ok; ++c, ++n)
-        for (int i = 0; i < T.count; ++i) {
-          const uint32_t u = n & 1 ? units1++ : units0++, d = 2 * (n & 1) + (u & 1);
-          ok = mbar_wait_warp2(&b_full[sB], phaseB, &d_empty[d], (u >> 1 & 1) ^ 1, err);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t ba = smem_u32(sb + sB * C::kB);
-          if (elect_one()) {
-            for (int o = 1; o >= 0; --o)  // the small parts first
-              for (int k = 0; k < steps; ++k)
-                mma_f16_ss(tmem + d * kN, smem_desc_sw128(ha + (o * kHalves + (k >> 2)) * C::kH + (k & 3) * 32),
-                           smem_desc_sw128(ba + (k >> 2) * kN * 128 + (k & 3) * 32), idesc, o == 0 || k > 0);
-            mma_commit(&d_full[d]);
-            mma_commit(&b_empty[sB]);
-            if (c + 1 == c1 && i + 1 == T.count) mma_commit(&h_empty[sH]);
-          }
-          __syncwarp();
-          if (++sB == C::kBRing) { sB = 0; phaseB ^= 1; }
+      const uint64_t da = smem_desc_sw128(smem_u32(sh + sH * C::kHBytes));
+      const uint32_t mine = (uint32_t)(c1 - c0 + ((n & 1) == set)) / 2 * T.count;  // products of these tiles
+      n += c1 - c0;
+      for (uint32_t i = 0; i < mine && ok; ++i, ++units) {
+        const uint32_t d = 2 * set + (units & 1), sB = set * C::kBRing + units % C::kBRing;
+        const uint64_t db = smem_desc_sw128(smem_u32(sb + sB * C::kB));
+        ok = mbar_wait_warp2(&b_full[sB], units / C::kBRing & 1, &d_empty[d], (units >> 1 & 1) ^ 1, err);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int o = 1; o >= 0; --o)  // the small parts first
+#pragma unroll
+            for (int k = 0; k < 4 * kHalves; ++k)
+              if (k < steps)
+                mma_f16_ss(tmem + d * kN, da + (((o * kHalves + (k >> 2)) * C::kH + (k & 3) * 32) >> 4),
+                           db + (((k >> 2) * kN * 128 + (k & 3) * 32) >> 4), idesc, o == 0 || k > 0);
+          mma_commit(&d_full[d]);
         }
+        __syncwarp();
+      }
+      if (elect_one()) mma_commit(&h_empty[sH]);
+      __syncwarp();
       if (++sH == C::kHRing) { sH = 0; phaseH ^= 1; }
     }
     // (after a wait that gave up, MMAs issued so far may still run; bounded)
     if (!ok) {
-      if (elect_one()) mma_commit(&drain);
+      if (elect_one()) mma_commit(&drain[set]);
       __syncwarp();
-      if (!mbar_wait_warp(&drain, 0, err)) atomicExch(&tmem_busy, 1u);
+      if (!mbar_wait_warp(&drain[set], 0, err)) atomicExch(&tmem_busy, 1u);
     }
   } else {
     const int quarter = warp & 3;
@@ -995,8 +1025,10 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
     int last = -1;
     uint32_t* const stage = reinterpret_cast<uint32_t*>(sx) + set * 128 * (kN + 1);  // (not `aligned`)
     uint32_t n = 0, units = 0;  // tiles, and products for this set, so far
-    griddep_wait();  // (out may be what a kernel before reads, too)
+    bool waited = false;
     while (ok && advance()) {
+      if (!waited) griddep_wait();  // (out may be what a kernel before reads, too)
+      waited = true;
       const int64_t w0 = m0 + quarter * 32;
       for (int c = c0; c < c1 && ok; ++c, ++n) {
         if ((n & 1) != set) continue;
@@ -1009,6 +1041,8 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
           const uint32_t d = 2 * set + (units & 1);
           ok = mbar_wait_warp(&d_full[d], units >> 1 & 1, err);
           if (!ok) break;
+          // its part of B has been read
+          if (quarter == 0 && lane == 0) mbar_arrive(&b_empty[set * C::kBRing + units % C::kBRing]);
           if (__any_sync(0xffffffffu, mine == id)) {
             tc_fence_after();
             uint32_t v[kN / 32][32];
@@ -1121,7 +1155,13 @@ static cudaError_t launch_shrink_many(const LoraArgs& a, bool x_bf16, uint32_t* 
     static std::atomic<uint64_t> attr_set{0};
     const cudaError_t e = smem_attr_once_per_device(kern, (int)C::kSmem, attr_set);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(kManyParts, (unsigned)ceil_div(a.M, 128)), 192, C::kSmem, st>>>(tx, ta, a, err);
+    // with few rows several clusters share their adapters (129 rows of 64 adapters,
+    // 5120 -> 5120, rank 16: the call 50 us, 187 with one cluster a tile; 300 rows of 11
+    // runs, 5120 -> 17408, rank 64: 30, 43; of one adapter 20.4, 21)
+    const int64_t tiles = ceil_div(a.M, 128);
+    int64_t z = num_sms() * (RP == 128 ? 1 : 2) / (tiles * kManyParts);
+    z = z < 1 ? 1 : z > 16 ? 16 : z;
+    kern<<<dim3(kManyParts, (unsigned)tiles, (unsigned)z), 192, C::kSmem, st>>>(tx, ta, a, err);
     return cudaGetLastError();
   }
   const int64_t windows = ceil_div(a.M, 32);
