@@ -664,8 +664,8 @@ def add_lora(base, x, a, b, ids, scaling=None, out=None, workspace=None, stream=
     strided; a, b: contiguous cuda bf16 [adapters, rank, K], [adapters, N, rank] (rank a multiple of 8,
     at most 128); ids: cuda int64 [M]; scaling: cuda fp32 [adapters] or None for 1 -> out [M, N] of
     base's dtype. `out` may be base itself. Through `workspace` (allocated here when not given). A
-    row's bits do not depend on the other rows among calls of up to 128 rows, nor among calls of more
-    (tensor cores, where x of one adapter's rows in a row costs least)."""
+    row's bits do not depend on the other rows among calls of few rows (up to 128 of ranks up to 32, 32
+    of ranks up to 64, 16 of higher ranks), nor among calls of more, which tensor cores compute."""
     M, N, ldb = _rows(base, "base", _CODES)
     dev = _device(base, stream)
     m, K, ldx = _rows(x, "x", _CODES, dev)

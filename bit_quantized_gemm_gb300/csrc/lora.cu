@@ -7,8 +7,8 @@
 // `shrink` sums h over parts of K, which are added up in order and scaled; `expand`
 // adds the second product to base. The parts are cut by K alone,
 // so a row's bits do not depend on the other rows, but for the choice of the kernels:
-//   up to 128 rows (decode), bound by reading the adapters that the rows use: a
-//   row at a time on the fp32 units, a few products for every value read;
+//   few rows (decode), bound by reading the adapters that the rows use: a row at a
+//   time on the fp32 units, a few products for every value read;
 //   more rows, bound by x, base and out: products on the tensor cores, where
 //   scaling * h goes in as the sum of two bf16 numbers (off by 2^-17 of itself:
 //   as good as an fp32 h), everything by TMA.
@@ -30,7 +30,13 @@ bool make_tmap_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base, 
                   int64_t rows, int64_t mats, int64_t pitch, int64_t mat_pitch, uint32_t box_cols,
                   uint32_t box_rows, CUtensorMapSwizzle swizzle);
 
-constexpr int kLoraFew = 128;                      // rows that are taken one at a time
+// Rows that are taken one at a time. GPU us of a call with one adapter and with one of 16
+// each row, one at a time | by tensor cores: 5120 -> 5120, rank 32, 64 rows 11.1, 15.0 |
+// 12.4, 26.6, 128 rows 14.6, 17.7 | 13.5, 27.7; rank 64, 32 rows 13.7, 17.1 | 13.3, 25.3,
+// 64 rows 17.0, 20.5 | 13.6, 27.5; 5120 -> 17408, 32 rows 21.5, 28.3 | 15.0, 27.6, 64
+// rows 35, 42 | 16, 30; 2560 -> 9728, rank 128, 16 rows 14.2, 17.5 | 15.1, 22.7, 32 rows
+// 26, 30 | 16, 27.
+static int64_t few_rows(int64_t rank) { return rank <= 32 ? 128 : rank <= 64 ? 32 : 16; }
 constexpr int kManyParts = 8;                      // parts of K of many rows
 
 struct LoraArgs {
@@ -78,17 +84,18 @@ __device__ __forceinline__ uint32_t add_raw(uint32_t v, float y) {
 }
 
 // -------------------------------------------------------------------- few rows
-// A CTA sums one part of K (up to 1024 values) of one row, a warp the ranks warp,
-// warp + 8, ...: 8 values a lane at a time, up to kU times, all loads of R ranks
-// ahead of the first product.
+// A CTA sums one part of K (up to 1024 values) of one row for 8 R ranks, a warp the
+// ranks warp and warp + 8: 8 values a lane at a time, up to kU times, all loads ahead of
+// the first product.
 constexpr int kFewWarps = 8, kFewPart = 128;  // eights of a part
 __host__ __device__ inline int few_parts(int K) { return (K / 8 + kFewPart - 1) / kFewPart; }
 
 template <bool kBf16, int R>
 __global__ void __launch_bounds__(32 * kFewWarps) lora_shrink_few_kernel(const LoraArgs a) {
   griddep_launch_dependents();
-  constexpr int kU = R <= 2 ? 4 : R == 4 ? 2 : 1;
+  constexpr int kU = 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = blockIdx.x, parts = gridDim.x;
+  const int r0 = (int)blockIdx.z * R * kFewWarps + warp;  // its first rank
   const int64_t m = blockIdx.y;
   const int id = adapter_of(a, m);
   if (id < 0) return;
@@ -110,7 +117,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) lora_shrink_few_kernel(const L
         x[u][j] = e < e1 ? __ldg(reinterpret_cast<const uint4*>(px) + (kBf16 ? 1 : 2) * e + j) : zero;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const int r = i * kFewWarps + warp;
+        const int r = r0 + i * kFewWarps;
         w[u][i] = e < e1 && r < a.rank ? __ldg(reinterpret_cast<const uint4*>(pa + (int64_t)r * a.K) + e) : zero;
       }
     }
@@ -143,7 +150,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) lora_shrink_few_kernel(const L
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int r = i * kFewWarps + warp;
+    const int r = r0 + i * kFewWarps;
     if (r >= a.rank) break;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
@@ -151,14 +158,14 @@ __global__ void __launch_bounds__(32 * kFewWarps) lora_shrink_few_kernel(const L
   }
 }
 
-// A warp adds to 32 C columns of kFewRows rows, one after another, a lane to
-// column lane (+ 32). B's part for a row (contiguous: columns x rank) comes
+// A warp adds to 32 C columns of up to kFewRows rows (`group`), one after another, a
+// lane to column lane (+ 32). B's part for a row (contiguous: columns x rank) comes
 // through a ring of the warp's own by bulk copies, once for rows that follow one
 // another with one id. A lane reads its column's ranks eight at a time, starting
 // with another eight than its neighbours, so that their reads do not conflict.
 constexpr int kExpandWarps = 4, kExpandRing = 4, kFewRows = 8;
 template <bool kBf16, int C>
-__global__ void __launch_bounds__(32 * kExpandWarps) lora_expand_few_kernel(const LoraArgs a, uint32_t* err) {
+__global__ void __launch_bounds__(32 * kExpandWarps) lora_expand_few_kernel(const LoraArgs a, int group, uint32_t* err) {
   extern __shared__ __align__(128) uint8_t smem[];  // [warp][slot][column][rank], then h [row][rank]
   __shared__ uint64_t full[kExpandWarps][kExpandRing];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = a.rank;
@@ -167,8 +174,8 @@ __global__ void __launch_bounds__(32 * kExpandWarps) lora_expand_few_kernel(cons
   float* const h = reinterpret_cast<float*>(smem + kExpandWarps * kExpandRing * slot_bytes);
   const int col0 = ((int)blockIdx.x * kExpandWarps + warp) * 32 * C;
   const int cols = min(32 * C, a.N - col0);  // (none: a warp behind the last column)
-  const int64_t m0 = (int64_t)blockIdx.y * kFewRows;
-  const int rows = (int)min((int64_t)kFewRows, a.M - m0);
+  const int64_t m0 = (int64_t)blockIdx.y * group;
+  const int rows = (int)min((int64_t)group, a.M - m0);
   const bool keep = a.base == a.out && a.ldb == a.ldo;  // rows without an adapter are in place
   const int mine = lane < rows ? adapter_of(a, m0 + lane) : -1;
   // a row brings B unless the last row before it that has an adapter has the same
@@ -1218,28 +1225,39 @@ static cudaError_t launch_expand_few(const LoraArgs& a, uint32_t* err, cudaStrea
   static std::atomic<uint64_t> attr_set{0};
   const cudaError_t e = smem_attr_once_per_device(kern, (kExpandWarps * kExpandRing * 64 + kFewRows * 4) * 128, attr_set);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((unsigned)ceil_div(a.N, kExpandWarps * 32 * C), (unsigned)ceil_div(a.M, kFewRows)),
-                       dim3(32 * kExpandWarps), smem, st, true, a, err);
+  // fewer rows a CTA while all of them run at once, with room for as many again (GPU us
+  // of a call, eight rows and by this rule: 16 rows of 16 adapters, 17408 -> 5120, rank 16
+  // 15.5, 9.0; 64 rows 19.8, 13.3)
+  const int64_t columns = ceil_div(a.N, kExpandWarps * 32 * C), fit = 112 * 1024 / smem;
+  const int64_t ctas = num_sms() * (fit < 1 ? 1 : fit > 4 ? 4 : fit);
+  int group = kFewRows;
+  while (group > 1 && columns * ceil_div(a.M, group) < ctas) group /= 2;
+  return launch_kernel(kern, dim3((unsigned)columns, (unsigned)ceil_div(a.M, group)), dim3(32 * kExpandWarps), smem, st,
+                       true, a, group, err);
 }
 
 template <bool kBf16>
 static cudaError_t launch_shrink_few(const LoraArgs& a, cudaStream_t st) {
-  const dim3 grid((unsigned)few_parts(a.K), (unsigned)a.M);
-  const int r = (a.rank + kFewWarps - 1) / kFewWarps;  // ranks a warp
-  if (r <= 1) lora_shrink_few_kernel<kBf16, 1><<<grid, 32 * kFewWarps, 0, st>>>(a);
-  else if (r <= 2) lora_shrink_few_kernel<kBf16, 2><<<grid, 32 * kFewWarps, 0, st>>>(a);
-  else if (r <= 4) lora_shrink_few_kernel<kBf16, 4><<<grid, 32 * kFewWarps, 0, st>>>(a);
-  else if (r <= 8) lora_shrink_few_kernel<kBf16, 8><<<grid, 32 * kFewWarps, 0, st>>>(a);
-  else lora_shrink_few_kernel<kBf16, 16><<<grid, 32 * kFewWarps, 0, st>>>(a);
+  auto launch = [&](auto kern, int R) {
+    const dim3 grid((unsigned)few_parts(a.K), (unsigned)a.M, (unsigned)ceil_div(a.rank, R * kFewWarps));
+    kern<<<grid, 32 * kFewWarps, 0, st>>>(a);
+  };
+  // (two ranks a warp: of four the loads go out in two turns, 4 rows, 5120 -> 5120, rank
+  // 64 11.3 us, and 7.8)
+  if (a.rank <= kFewWarps) launch(lora_shrink_few_kernel<kBf16, 1>, 1);
+  else launch(lora_shrink_few_kernel<kBf16, 2>, 2);
   return cudaGetLastError();
 }
 
 static int64_t padded(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
 // bytes of the parts' sums of M rows; with many rows, of their two parts before them
+// (and never less than fewer rows need)
 int64_t lora_workspace(int64_t M, int64_t K, int64_t rank) {
-  if (M <= kLoraFew) return few_parts((int)K) * M * rank * 4;
-  return (kManyParts * 4 + 4) * M * padded(rank);
+  const int64_t few = few_rows(rank), sums = few_parts((int)K) * (M < few ? M : few) * rank * 4;
+  if (M <= few) return sums;
+  const int64_t many = (kManyParts * 4 + 4) * M * padded(rank);
+  return many > sums ? many : sums;
 }
 
 cudaError_t launch_add_lora(const void* base, bool bf16, int64_t ldb, const void* x, bool x_bf16, int64_t M,
@@ -1249,7 +1267,7 @@ cudaError_t launch_add_lora(const void* base, bool bf16, int64_t ldb, const void
   LoraArgs a{x, reinterpret_cast<const uint16_t*>(A), reinterpret_cast<const uint16_t*>(B), ids, scaling, base,
              out, reinterpret_cast<float*>(ws), reinterpret_cast<uint32_t*>(ws), ldx, ldb, ldo, M, (int)K, (int)N,
              (int)rank, (int)count, (int)rank};
-  if (M <= kLoraFew) {
+  if (M <= few_rows(rank)) {
     const cudaError_t e = x_bf16 ? launch_shrink_few<true>(a, st) : launch_shrink_few<false>(a, st);
     if (e != cudaSuccess) return e;
     if (rank <= 32) return bf16 ? launch_expand_few<true, 2>(a, err, st) : launch_expand_few<false, 2>(a, err, st);

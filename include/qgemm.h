@@ -408,12 +408,13 @@ qg_status qg_gemm_fp8_grouped(const uint8_t* q, const float* scale, int64_t lds,
 /*   h[m][r]   = sum_k x[m][k] * a[id][r][k]               id = ids[m]      */
 /*   out[m][n] = base[m][n] + sum_r (scaling[id] * h[m][r]) * b[id][n][r]   */
 /* in fp32, rounded once to dtype. A row whose id is outside 0..adapters-1  */
-/* keeps base's bits. Rows may come in any order; with more than 128 rows,  */
-/* rows of one adapter that follow one another cost least. Up to 128 rows   */
-/* the products run on the fp32 units; above that on the tensor cores,      */
-/* scaling * h as the sum of two bf16 numbers (off by 2^-17 of itself),     */
-/* fp32 x as the sum of three. Within either kind a row's bits do not       */
-/* depend on the other rows of its call.                                    */
+/* keeps base's bits. Rows may come in any order; with many, rows of one    */
+/* adapter that follow one another cost least. Few rows (up to 128 of ranks */
+/* up to 32, 32 of ranks up to 64, 16 of higher ranks) are taken one at a   */
+/* time by the fp32 units, more by the tensor cores: scaling * h as the sum */
+/* of two bf16 numbers (off by 2^-17 of itself), fp32 x as the sum of       */
+/* three. A row's bits do not depend on the other rows of its call among    */
+/* calls of few rows, nor among calls of more.                              */
 /*   base, out [M][ldb], [M][ldo] of dtype, rows of N values, aligned to    */
 /*             their elements (fastest where rows begin and end on 16       */
 /*             bytes). out may be base itself (with ldo = ldb); it overlaps */
@@ -426,8 +427,9 @@ qg_status qg_gemm_fp8_grouped(const uint8_t* q, const float* scale, int64_t lds,
 /*   ids       [M] int64.                                                   */
 /*   scaling   [adapters] fp32, or NULL for 1.                              */
 /*   workspace qg_add_lora_workspace_bytes(M, K, rank) bytes (0: invalid    */
-/*             sizes), 256-byte aligned, owned by the caller; calls that    */
-/*             may run at once need one each.                               */
+/*             sizes; not less than fewer rows need), 256-byte aligned,     */
+/*             owned by the caller; calls that may run at once need one     */
+/*             each.                                                        */
 /* K % 16 == 0, K <= 65536; rank % 8 == 0, 8 <= rank <= QG_LORA_MAX_RANK; 1 */
 /* <= M <= 2^20, 1 <= N <= 2^24, 1 <= adapters <= 2^20.                     */
 /* ------------------------------------------------------------------------ */

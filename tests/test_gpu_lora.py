@@ -2,9 +2,9 @@
 
 Bound: every addition of products in fp32 is off by at most one unit, 2^-23 of the sum
 of |terms|, so a chain of c of them by c * 2^-23.
-h, more than 128 rows of bf16: one of eight parts of K, in steps of 64, then 8 sums. Of
+h, by tensor cores, bf16 rows: one of eight parts of K, in steps of 64, then 8 sums. Of
 fp32: one of 64 shares of K, in steps of 32 with three products a value, then 16 sums.
-Up to 128 rows: 64 products a lane at most (K in parts of 1024, K / 1024 of them), 5 sums
+A row at a time (few_rows): 64 products a lane at most (K in parts of 1024, K / 1024 of them), 5 sums
 of lanes and K / 1024 of parts.
 scaling * h: 2^-24, and 2^-17 for its two bf16 parts. The second product: twice rank up
 to 16 products. The sum with base rounds once to fp32 and once to the output: half a
@@ -43,9 +43,14 @@ def inputs(seed, m, k, n, rank, count, x=BF16, out=BF16, pad=0):
     return base, xs, a, b, ids, scaling
 
 
+def few_rows(rank):
+    """Rows up to which they are taken one at a time."""
+    return 128 if rank <= 32 else 32 if rank <= 64 else 16
+
+
 def check(got, base, x, a, b, ids, scaling):
     m, k, rank, count = x.shape[0], x.shape[1], a.shape[1], a.shape[0]
-    if m <= 128:
+    if m <= few_rows(rank):
         c1 = 64 + 5 + -(-k // 1024)
     elif x.dtype == BF16:
         c1 = 64 * -(-(-(-k // 64)) // 8) + 8
@@ -74,7 +79,8 @@ def check(got, base, x, a, b, ids, scaling):
 CASES = [
     (1, 16, 1, 8, 1), (1, 17408, 5120, 16, 3), (5, 272, 100, 16, 2), (16, 2560, 333, 8, 20), (31, 528, 256, 24, 4),
     (64, 5120, 1000, 16, 64), (33, 1040, 257, 32, 5), (100, 640, 129, 64, 3), (65, 2064, 520, 128, 9),
-    (300, 256, 72, 40, 7), (700, 1280, 2000, 64, 2), (40, 65536, 64, 16, 3),
+    (300, 256, 72, 40, 7), (700, 1280, 2000, 64, 2), (40, 65536, 64, 16, 3), (128, 2560, 2000, 32, 9),
+    (32, 5120, 777, 64, 6), (33, 5120, 777, 64, 6), (16, 1296, 2048, 128, 4), (17, 1296, 2048, 128, 4), (3, 17408, 640, 72, 2),
 ]
 
 
@@ -106,13 +112,16 @@ def test_strides_and_in_place(n):
 
 
 @pytest.mark.parametrize("x", [BF16, F32])
-def test_bits_of_a_row_do_not_depend_on_the_others(x):
-    # (of calls of up to 128 rows, and of calls of more)
-    base, xs, a, b, ids, scaling = inputs(1, 500, 1296, 304, 24, 6, x)
+@pytest.mark.parametrize("rank,n", [(24, 304), (64, 304), (128, 2000)])
+def test_bits_of_a_row_do_not_depend_on_the_others(x, rank, n):
+    # (of calls of few rows, and of calls of more)
+    few = few_rows(rank)
+    base, xs, a, b, ids, scaling = inputs(1, 500, 1296, n, rank, 6, x)
     for many in (False, True):
-        last = 500 if many else 128
+        last = 500 if many else few
         want = qg.add_lora(base[:last], xs[:last], a, b, ids[:last], scaling)
-        for rows in (slice(3, 499), slice(100, 400)) if many else (slice(7, 8), slice(30, 70)):
+        for rows in ((slice(3, 499), slice(100, 400), slice(9, 10 + few)) if many
+                     else (slice(7, 8), slice(few // 4, few // 2), slice(1, few))):
             got = qg.add_lora(base[rows], xs[rows], a, b, ids[rows].contiguous(), scaling)
             assert torch.equal(got, want[rows])
         turn = torch.randperm(last, device=DEV)

@@ -111,11 +111,16 @@ def test_adapter_refusals(L, kw, status):
 
 def test_adapter_workspace(L):
     up = lambda v: -(-v // 256) * 256  # noqa: E731
-    # up to 128 rows: an fp32 sum for each part of K of 1024; above: eight, and two bf16 numbers
-    for M, K, r in [(1, 16, 8), (64, 5120, 16), (128, 17408, 128), (7, 1040, 24)]:
+    # few rows: an fp32 sum for each part of K of 1024; more: eight, and two bf16 numbers
+    for M, K, r in [(1, 16, 8), (64, 5120, 16), (128, 17408, 32), (7, 1040, 24), (32, 5120, 64), (16, 5120, 128)]:
         assert L.qg_add_lora_workspace_bytes(M, K, r) == up(-(-K // 1024) * M * r * 4)
-    for M, K, r, padded in [(129, 16, 8, 16), (4096, 5120, 24, 32), (200, 5120, 72, 128)]:
+    for M, K, r, padded in [(129, 16, 8, 16), (4096, 5120, 24, 32), (200, 5120, 72, 128), (33, 1024, 40, 64)]:
         assert L.qg_add_lora_workspace_bytes(M, K, r) == up(M * padded * 36)
+    # a workspace of many rows is one of fewer
+    for K in (16, 5120, 65536):
+        for r in (8, 32, 40, 64, 72, 128):
+            need = [L.qg_add_lora_workspace_bytes(M, K, r) for M in (1, 2, 15, 16, 17, 32, 33, 128, 129, 500, 2**20)]
+            assert need == sorted(need) and need[0] > 0
     for M, K, r in [(0, 256, 16), (2**20 + 1, 256, 16), (4, 24, 16), (4, 256, 12), (4, 256, 136), (4, 0, 16)]:
         assert L.qg_add_lora_workspace_bytes(M, K, r) == 0
 
