@@ -259,8 +259,10 @@ static cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
 template <bool kBf16, bool kWBf16, bool kFp8>
 static cudaError_t launch_norm_k(const NormArgs& a, cudaStream_t st) {
   // one unit a warp up to 20 warps (4096 x 9728 bf16: 48.1 us, 58.6 in two units),
-  // two up to 17 (4096 x 14336 int8: 91 us, 104 in one)
-  if (a.K <= 512 * 20) return launch_norm<kBf16, kWBf16, kFp8, 1>(a, st);
+  // two up to 17 (4096 x 14336 int8: 91 us, 104 in one); with an SM for every row one up
+  // to 32 (16 x 14128 bf16, residual: 3.7 us, 4.6 in two)
+  if (a.K <= 512 * 20 || (a.K <= 512 * 32 && a.M <= num_sms()))
+    return launch_norm<kBf16, kWBf16, kFp8, 1>(a, st);
   if (a.K <= 512 * 2 * 17) return launch_norm<kBf16, kWBf16, kFp8, 2>(a, st);
   return launch_norm<kBf16, kWBf16, kFp8, 4>(a, st);
 }

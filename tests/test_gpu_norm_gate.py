@@ -77,7 +77,7 @@ def check_int8(q, scale, y, off):
 
 
 SIZES = [(1, 16), (3, 144), (1, 5120), (64, 2560), (7, 496), (130, 8192), (33, 8208), (2, 17408), (9, 17424),
-         (1000, 272), (2, 65536), (3, 32784), (700, 1040)]
+         (1000, 272), (2, 65536), (3, 32784), (700, 1040), (5, 11200), (200, 11200), (3, 16384)]
 
 
 @pytest.mark.parametrize("m,k", SIZES)
@@ -136,10 +136,11 @@ def test_norm_of_exact_values_has_the_quantizers_bits():
         assert torch.equal(q, want) and torch.equal(scale, ws) and torch.equal(bs, wbs) and torch.equal(h, wh)
 
 
-@pytest.mark.parametrize("k", [256, 5120, 17408])
+@pytest.mark.parametrize("k", [256, 5120, 11216, 16384, 17408])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_norm_bits_of_a_row(k, dtype):
-    # alone, in batches, on their stored sum, in place: the same bits
+    # alone, in batches, on their stored sum, in place: the same bits (K of the int8 norm: a multiple of 32)
+    k = k // 32 * 32
     g = gen(k)
     x, res = rows(g, 1700, k, dtype), rows(g, 1700, k, dtype, 0, 3.0)
     w = torch.randn(k, generator=g, device=DEV)
