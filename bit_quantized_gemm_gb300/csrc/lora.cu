@@ -10,8 +10,9 @@
 //   few rows (decode), bound by reading the adapters that the rows use: a row at a
 //   time on the fp32 units, a few products for every value read;
 //   more rows, bound by x, base and out: products on the tensor cores, where
-//   scaling * h goes in as the sum of two bf16 numbers (off by 2^-17 of itself:
-//   as good as an fp32 h), everything by TMA.
+//   scaling * h goes in as the sum of two bf16 numbers (off by 2^-17 of itself, far
+//   less than a bf16 output's rounding) or, for fp32 outputs, of three (2^-24),
+//   everything by TMA.
 // Each kernel is a programmatic dependent of the one before it. Rows may come in
 // any order. Many rows are taken in tiles of 128, in which the different ids are
 // found by votes; each costs a pass over the tile.
@@ -47,9 +48,10 @@ struct LoraArgs {
   const void* base;
   void* out;
   float* h;               // sums [part of K][M][rp], rp ranks a row (many rows: up to 16, 32, 64 or 128)
-  uint32_t* parts;        // many rows: scaling * h as [large, small numbers][M][rp / 2] pairs of bf16
+  uint32_t* parts;        // many rows: scaling * h as [large to small numbers][M][rp / 2] pairs of bf16
   int64_t ldx, ldb, ldo, M;
   int K, N, rank, count, rp;
+  int numbers;            // many rows: bf16 numbers that scaling * h is the sum of
 };
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -531,17 +533,17 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int m, int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// four ranks of a row of scaling * h as two bf16 numbers each. (Ranks that only
-// pad: 0, also where x is infinite.)
+// four ranks of a row of scaling * h as two or three bf16 numbers each. (Ranks that
+// only pad: 0, also where x is infinite.)
 __device__ __forceinline__ void put_parts(const LoraArgs& a, int64_t m, int r, float4 v, float scale) {
   v = r < a.rank ? make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale) : make_float4(0, 0, 0, 0);
-  const uint2 hi = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
   auto rest = [](float f, float h) { return isfinite(h) ? f - h : 0.0f; };  // (an infinity's would be NaN)
-  const uint2 lo = make_uint2(bf16x2(rest(v.x, bf16_lo(hi.x)), rest(v.y, bf16_hi(hi.x))),
-                              bf16x2(rest(v.z, bf16_lo(hi.y)), rest(v.w, bf16_hi(hi.y))));
   uint2* to = reinterpret_cast<uint2*>(a.parts) + (m * a.rp + r) / 4;
-  to[0] = hi;
-  to[a.M * (a.rp / 4)] = lo;
+  for (int i = 0; i < a.numbers; ++i, to += a.M * (a.rp / 4)) {
+    const uint2 n = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+    *to = n;
+    v = make_float4(rest(v.x, bf16_lo(n.x)), rest(v.y, bf16_hi(n.x)), rest(v.z, bf16_lo(n.y)), rest(v.w, bf16_hi(n.y)));
+  }
 }
 
 // Many rows of bf16 x. A cluster of eight CTAs, one a part of K, multiplies 128 rows
@@ -766,7 +768,7 @@ __global__ void __launch_bounds__(256) lora_join_kernel(const LoraArgs a) {
 // Many rows. Bound by reading base and writing out, so both go by TMA, tile by
 // tile (128 rows x 128 bytes), through one ring: the epilogue adds to a tile where
 // it lies in shared memory and stores it from there. A tile's second product is a
-// tcgen05 MMA of 128 rows x kN columns: A operand h (large and small parts, in
+// tcgen05 MMA of 128 rows x kN columns: A operand h (its two or three numbers, in
 // shared memory as long as the CTA stays with its 128 rows), B operand kN rows of
 // B, into an accumulator in tensor memory. Where a tile's rows have
 // several adapters, it is multiplied with each, and every row (a lane of tensor
@@ -788,8 +790,9 @@ template <bool kBf16, int kHalves>  // 64 ranks each
 struct ExpandMany {
   static constexpr int kN = kBf16 ? 64 : 32;  // columns of a tile: 128 bytes of a row
   static constexpr int kBase = 128 * 128, kB = kN * 128 * kHalves, kH = 128 * 128;
-  static constexpr int kBaseRing = kHalves == 2 ? 6 : 8, kBRing = 2, kSlots = 4;  // (B: of a set)
-  static constexpr int kHBytes = 2 * kHalves * kH, kHRing = kHalves == 2 ? 1 : 2;
+  static constexpr int kNumbers = kBf16 ? 2 : 3;  // of h
+  static constexpr int kBaseRing = kHalves == 2 || !kBf16 ? 6 : 8, kBRing = 2, kSlots = 4;  // (B: of a set)
+  static constexpr int kHBytes = kNumbers * kHalves * kH, kHRing = kHalves == 2 ? 1 : 2;
   static constexpr int kThreads = 96 + 32 * 8;
   // A set waits for its own tiles alone, and a wait on a barrier tells a phase from
   // the next one only: every slot of base and every accumulator is one set's (even
@@ -820,7 +823,7 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sx = base;                                  // tiles of base [slot]
   uint8_t* sb = sx + C::kBaseRing * C::kBase;          // B [set][slot][half]
-  uint8_t* sh = sb + 2 * C::kBRing * C::kB;                // h [slot][large, small][half]
+  uint8_t* sh = sb + 2 * C::kBRing * C::kB;                // h [slot][number][half]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t CT = (a.N + kN - 1) / kN;
   const bool keep = a.base == a.out && a.ldb == a.ldo;  // rows without an adapter are in place
@@ -939,7 +942,7 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
         if (elect_one()) {
           mbar_arrive_expect_tx(&h_full[sH], C::kHBytes);
 #pragma unroll
-          for (int o = 0; o < 2; ++o)
+          for (int o = 0; o < C::kNumbers; ++o)
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
               tma_load_3d(sh + sH * C::kHBytes + (o * kHalves + h) * C::kH, &tmH, &h_full[sH], h * 64, (int)m0, o);
@@ -1005,12 +1008,12 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int o = 1; o >= 0; --o)  // the small parts first
+          for (int o = C::kNumbers - 1; o >= 0; --o)  // the small numbers first
 #pragma unroll
             for (int k = 0; k < 4 * kHalves; ++k)
               if (k < steps)
                 mma_f16_ss(tmem + d * kN, da + (((o * kHalves + (k >> 2)) * C::kH + (k & 3) * 32) >> 4),
-                           db + (((k >> 2) * kN * 128 + (k & 3) * 32) >> 4), idesc, o == 0 || k > 0);
+                           db + (((k >> 2) * kN * 128 + (k & 3) * 32) >> 4), idesc, o + 1 < C::kNumbers || k > 0);
           mma_commit(&d_full[d]);
         }
         __syncwarp();
@@ -1204,7 +1207,7 @@ static cudaError_t launch_expand_many(const LoraArgs& a, uint32_t* err, cudaStre
         !make_tmap_2d(&to, type, a.out, a.N, a.M, a.ldo * es, C::kN, 32, CU_TENSOR_MAP_SWIZZLE_128B))) ||
       !make_tmap_3d(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.b, a.rank, a.N, a.count, (int64_t)a.rank * 2,
                     (int64_t)a.N * a.rank * 2, 64, C::kN, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_3d(&th, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.parts, a.rp, a.M, 2, (int64_t)a.rp * 2,
+      !make_tmap_3d(&th, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.parts, a.rp, a.M, C::kNumbers, (int64_t)a.rp * 2,
                     a.M * a.rp * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorNotSupported;
   auto kern = lora_expand_many_kernel<kBf16, kHalves>;
@@ -1254,12 +1257,12 @@ static cudaError_t launch_shrink_few(const LoraArgs& a, cudaStream_t st) {
 
 static int64_t padded(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
-// bytes of the parts' sums of M rows; with many rows, of their two parts before them
-// (and never less than fewer rows need)
+// bytes of the parts' sums of M rows; with many rows, of up to three bf16 numbers of
+// each sum before them (and never less than fewer rows need)
 int64_t lora_workspace(int64_t M, int64_t K, int64_t rank) {
   const int64_t few = few_rows(rank), sums = few_parts((int)K) * (M < few ? M : few) * rank * 4;
   if (M <= few) return sums;
-  const int64_t many = (kManyParts * 4 + 4) * M * padded(rank);
+  const int64_t many = (kManyParts * 4 + 6) * M * padded(rank);
   return many > sums ? many : sums;
 }
 
@@ -1269,7 +1272,7 @@ cudaError_t launch_add_lora(const void* base, bool bf16, int64_t ldb, const void
                             uint32_t* err, cudaStream_t st) {
   LoraArgs a{x, reinterpret_cast<const uint16_t*>(A), reinterpret_cast<const uint16_t*>(B), ids, scaling, base,
              out, reinterpret_cast<float*>(ws), reinterpret_cast<uint32_t*>(ws), ldx, ldb, ldo, M, (int)K, (int)N,
-             (int)rank, (int)count, (int)rank};
+             (int)rank, (int)count, (int)rank, 0};
   if (M <= few_rows(rank)) {
     const cudaError_t e = x_bf16 ? launch_shrink_few<true>(a, st) : launch_shrink_few<false>(a, st);
     if (e != cudaSuccess) return e;
@@ -1277,7 +1280,8 @@ cudaError_t launch_add_lora(const void* base, bool bf16, int64_t ldb, const void
     return bf16 ? launch_expand_few<true, 1>(a, err, st) : launch_expand_few<false, 1>(a, err, st);
   }
   a.rp = (int)padded(rank);
-  a.h += M * a.rp;  // (behind the two parts, 2 bytes a rank each)
+  a.numbers = bf16 ? 2 : 3;
+  a.h = reinterpret_cast<float*>(a.parts + a.numbers * M * (a.rp / 2));  // (behind the numbers)
   cudaError_t e = a.rp == 16   ? launch_shrink_many<1>(a, x_bf16, err, st)
                   : a.rp == 32 ? launch_shrink_many<2>(a, x_bf16, err, st)
                   : a.rp == 64 ? launch_shrink_many<4>(a, x_bf16, err, st)

@@ -412,9 +412,9 @@ qg_status qg_gemm_fp8_grouped(const uint8_t* q, const float* scale, int64_t lds,
 /* adapter that follow one another cost least. Few rows (up to 128 of ranks */
 /* up to 32, 32 of ranks up to 64, 16 of higher ranks) are taken one at a   */
 /* time by the fp32 units, more by the tensor cores: scaling * h as the sum */
-/* of two bf16 numbers (off by 2^-17 of itself), fp32 x as the sum of       */
-/* three. A row's bits do not depend on the other rows of its call among    */
-/* calls of few rows, nor among calls of more.                              */
+/* of two bf16 numbers (off by 2^-17 of itself), of three where out is      */
+/* fp32, and fp32 x as the sum of three. A row's bits do not depend on the  */
+/* other rows of its call among calls of few rows, nor among calls of more. */
 /*   base, out [M][ldb], [M][ldo] of dtype, rows of N values, aligned to    */
 /*             their elements (fastest where rows begin and end on 16       */
 /*             bytes). out may be base itself (with ldo = ldb); it overlaps */

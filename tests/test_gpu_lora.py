@@ -6,8 +6,8 @@ h, by tensor cores, bf16 rows: one of eight parts of K, in steps of 64, then 8 s
 fp32: one of 64 shares of K, in steps of 32 with three products a value, then 16 sums.
 A row at a time (few_rows): 64 products a lane at most (K in parts of 1024, K / 1024 of them), 5 sums
 of lanes and K / 1024 of parts.
-scaling * h: 2^-24, and 2^-17 for its two bf16 parts. The second product: twice rank up
-to 16 products. The sum with base rounds once to fp32 and once to the output: half a
+scaling * h: 2^-24, and by tensor cores 2^-17 for its two bf16 numbers (2^-24 for the three of
+fp32 outputs). The second product: that often rank, up to 16, products. The sum with base rounds once to fp32 and once to the output: half a
 step, 2^-8 (bf16) or 2^-24.
 """
 import pytest
@@ -56,7 +56,9 @@ def check(got, base, x, a, b, ids, scaling):
         c1 = 64 * -(-(-(-k // 64)) // 8) + 8
     else:
         c1 = 3 * 32 * -(-(-(-k // 32)) // 64) + 16
-    c2 = 2 * 16 * -(-rank // 16)
+    numbers = 2 if got.dtype == BF16 else 3
+    c2 = numbers * 16 * -(-rank // 16)
+    off = 2.0 ** -16.9 if numbers == 2 else 2.0 ** -23
     half = 2.0 ** -8 if got.dtype == BF16 else 2.0 ** -24
     assert got.shape == base.shape and got.dtype == base.dtype
     for i in range(-1, count):
@@ -70,7 +72,7 @@ def check(got, base, x, a, b, ids, scaling):
         xd, ad, bd = x[rows].double(), a[i].double(), b[i].double()
         h, hm = xd @ ad.t(), xd.abs() @ ad.abs().t()
         y = base[rows].double() + f * (h @ bd.t())
-        bound = f * ((c1 * 2.0 ** -23 * hm + 2.0 ** -16.9 * h.abs()) @ bd.abs().t())
+        bound = f * ((c1 * 2.0 ** -23 * hm + off * h.abs()) @ bd.abs().t())
         bound += c2 * 2.0 ** -23 * f * (h.abs() @ bd.abs().t())
         bound += (half + 2.0 ** -24) * (y.abs() + bound)
         assert bool(((got[rows].double() - y).abs() <= bound).all())

@@ -111,11 +111,11 @@ def test_adapter_refusals(L, kw, status):
 
 def test_adapter_workspace(L):
     up = lambda v: -(-v // 256) * 256  # noqa: E731
-    # few rows: an fp32 sum for each part of K of 1024; more: eight, and two bf16 numbers
+    # few rows: an fp32 sum for each part of K of 1024; more: eight, and three bf16 numbers
     for M, K, r in [(1, 16, 8), (64, 5120, 16), (128, 17408, 32), (7, 1040, 24), (32, 5120, 64), (16, 5120, 128)]:
         assert L.qg_add_lora_workspace_bytes(M, K, r) == up(-(-K // 1024) * M * r * 4)
     for M, K, r, padded in [(129, 16, 8, 16), (4096, 5120, 24, 32), (200, 5120, 72, 128), (33, 1024, 40, 64)]:
-        assert L.qg_add_lora_workspace_bytes(M, K, r) == up(M * padded * 36)
+        assert L.qg_add_lora_workspace_bytes(M, K, r) == up(M * padded * 38)
     # a workspace of many rows is one of fewer
     for K in (16, 5120, 65536):
         for r in (8, 32, 40, 64, 72, 128):
