@@ -974,6 +974,7 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
         n += both;
       }
     }
+    if (!waited) griddep_wait();  // (this kernel's end is that of those before, too)
     // every load has landed before the CTA exits
     for (int i = max(0, loadsH - C::kHRing); i < loadsH; ++i)
       mbar_wait_warp(&h_full[i % C::kHRing], (uint32_t)(i / C::kHRing) & 1u, err);
@@ -1231,13 +1232,13 @@ static cudaError_t launch_expand_few(const LoraArgs& a, uint32_t* err, cudaStrea
   static std::atomic<uint64_t> attr_set{0};
   const cudaError_t e = smem_attr_once_per_device(kern, (kExpandWarps * kExpandRing * 64 + kFewRows * 4) * 128, attr_set);
   if (e != cudaSuccess) return e;
-  // fewer rows a CTA while all of them run at once, with room for as many again (GPU us
-  // of a call, eight rows and by this rule: 16 rows of 16 adapters, 17408 -> 5120, rank 16
-  // 15.5, 9.0; 64 rows 19.8, 13.3)
-  const int64_t columns = ceil_div(a.N, kExpandWarps * 32 * C), fit = 112 * 1024 / smem;
-  const int64_t ctas = num_sms() * (fit < 1 ? 1 : fit > 4 ? 4 : fit);
+  // fewer rows a CTA while all of them still run at once (GPU us of a call: 16 rows of 16
+  // adapters, 17408 -> 5120, rank 16, eight a CTA 15.5, one 9.0; beyond that 16 rows, 5120
+  // -> 17408, rank 32, two a CTA 13.1, four 11.5)
+  const int64_t columns = ceil_div(a.N, kExpandWarps * 32 * C);
+  const int64_t fit = num_sms() * (int64_t)(227 * 1024 / (smem + 2048));
   int group = kFewRows;
-  while (group > 1 && columns * ceil_div(a.M, group) < ctas) group /= 2;
+  while (group > 1 && columns * ceil_div(a.M, group / 2) <= fit) group /= 2;
   return launch_kernel(kern, dim3((unsigned)columns, (unsigned)ceil_div(a.M, group)), dim3(32 * kExpandWarps), smem, st,
                        true, a, group, err);
 }
