@@ -32,11 +32,11 @@ bool make_tmap_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base, 
                   uint32_t box_rows, CUtensorMapSwizzle swizzle);
 
 // Rows that are taken one at a time. GPU us of a call with one adapter and with one of 16
-// each row, one at a time | by tensor cores: 5120 -> 5120, rank 32, 64 rows 11.1, 15.0 |
-// 12.4, 26.6, 128 rows 14.6, 17.7 | 13.5, 27.7; rank 64, 32 rows 13.7, 17.1 | 13.3, 25.3,
-// 64 rows 17.0, 20.5 | 13.6, 27.5; 5120 -> 17408, 32 rows 21.5, 28.3 | 15.0, 27.6, 64
-// rows 35, 42 | 16, 30; 2560 -> 9728, rank 128, 16 rows 14.2, 17.5 | 15.1, 22.7, 32 rows
-// 26, 30 | 16, 27.
+// each row, one at a time | by tensor cores: 5120 -> 5120, rank 32, 96 rows 13.0, 17.1 |
+// 12.7, 27.7, 128 rows 14.6, 17.6 | 13.6, 28.2; rank 64, 32 rows 11.1, 13.6 | 13.3, 25.8,
+// 64 rows 16.9, 20.5 | 13.6, 28.1; 5120 -> 17408, 32 rows 21.0, 28.3 | 14.6, 28.3, 64
+// rows 35, 42 | 16, 31; 2560 -> 9728, rank 128, 16 rows 14.4, 17.7 | 15.1, 23.0, 32 rows
+// 26, 31 | 16, 27.
 static int64_t few_rows(int64_t rank) { return rank <= 32 ? 128 : rank <= 64 ? 32 : 16; }
 constexpr int kManyParts = 8;                      // parts of K of many rows
 
@@ -1249,8 +1249,8 @@ static cudaError_t launch_shrink_few(const LoraArgs& a, cudaStream_t st) {
     const dim3 grid((unsigned)few_parts(a.K), (unsigned)a.M, (unsigned)ceil_div(a.rank, R * kFewWarps));
     kern<<<grid, 32 * kFewWarps, 0, st>>>(a);
   };
-  // (two ranks a warp: of four the loads go out in two turns, 4 rows, 5120 -> 5120, rank
-  // 64 11.3 us, and 7.8)
+  // (two ranks a warp: the loads of four go out in two turns, 4 rows, 5120 -> 5120, rank
+  // 64 11.3 us in place of 7.8)
   if (a.rank <= kFewWarps) launch(lora_shrink_few_kernel<kBf16, 1>, 1);
   else launch(lora_shrink_few_kernel<kBf16, 2>, 2);
   return cudaGetLastError();
