@@ -74,7 +74,7 @@ struct GroupedBars {
 };
 
 template <int R, int BM>
-__global__ void __launch_bounds__(GroupedCfg<R, BM>::kThreads)
+__global__ void __launch_bounds__(GroupedCfg<R, BM>::kThreads, 1)
     gemm_fp8_grouped_kernel(const __grid_constant__ CUtensorMap tmW,
                             const __grid_constant__ CUtensorMap tmQ,
                             const __grid_constant__ CUtensorMap tmS, const Fp8GroupedArgs a) {

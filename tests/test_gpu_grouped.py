@@ -106,6 +106,20 @@ def test_many_experts_and_a_wide_one():
     assert torch.equal(bits(out), bits(want))
 
 
+@pytest.mark.parametrize("e", [31, 32, 33, 127, 128, 129, 256])
+@pytest.mark.parametrize("rows", [3, 40])
+def test_numbers_of_experts(e, rows):
+    # (their offsets are read in groups)
+    counts = [(i * 7) % (2 * rows) for i in range(e)]
+    m = sum(counts)
+    q, scale, w, ws = inputs(e, m, e, 144, 72)
+    off = offsets_of(counts)
+    out = torch.empty(m, 72, device=DEV, dtype=F32)
+    want = by_expert(q, scale, off, w, ws, torch.empty_like(out))
+    qg.gemm_fp8_grouped(q, scale, off, w, ws, out=out)
+    assert torch.equal(bits(out), bits(want))
+
+
 def test_against_64_bits():
     # the bound of gemm_fp8's own tests: (128 + 3 + KB) * 2^-23 of the sum of magnitudes
     counts, k, n = [40, 3, 200], 1296, 390

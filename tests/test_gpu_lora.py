@@ -158,6 +158,15 @@ def test_many_rows_of_many_adapters(n, count, out, rank):
     check(qg.add_lora(base, xs, a, b, runs, scaling), base, xs, a, b, runs, scaling)
 
 
+@pytest.mark.parametrize("rank", [16, 64, 128])
+def test_a_workspace_of_many_rows_is_one_of_fewer(rank):
+    base, xs, a, b, ids, scaling = inputs(9, 300, 2064, 520, rank, 5)
+    ws = torch.full((qg.add_lora_workspace_bytes(300, 2064, rank),), 255, dtype=torch.uint8, device=DEV)
+    for m in (300, 129, 128, 40, 17, 16, 1, 33, 200):
+        got = qg.add_lora(base[:m], xs[:m], a, b, ids[:m].contiguous(), scaling, workspace=ws)
+        assert torch.equal(got, qg.add_lora(base[:m], xs[:m], a, b, ids[:m].contiguous(), scaling))
+
+
 def test_rows_without_an_adapter_keep_their_bits():
     base, xs, a, b, ids, scaling = inputs(4, 50, 256, 96, 8, 3)
     base.view(torch.int16)[:, 5] = 0x7FA3      # a NaN with a payload
