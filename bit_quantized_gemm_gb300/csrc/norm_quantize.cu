@@ -72,8 +72,9 @@ __device__ __forceinline__ float rsqrt_refined(float v) {
 }
 
 // a lane's 16 values quantized to int8 with the row's scale s: bytes, fp16 copy,
-// sums of 32 (a pair of lanes). |y * fl(1/s)| rounds to at most 127, so nothing
-// is clamped. s = 0, NaN or infinite: q is 0.
+// sums of 32 (a pair of lanes). Where s is normal, |y * fl(1/s)| rounds to at most
+// 127; a subnormal s = max|y| / 127 has only a few bits, and quotients by it are
+// clamped (max|y| = 190 * 2^-149 gives s = 2^-149). s = 0, NaN or infinite: q is 0.
 __device__ __forceinline__ void emit_int8(const NormArgs& a, const float2 (&y)[8], int64_t m, int k, bool valid,
                                           float s, float inv) {
   float2 f[8];  // whole numbers + 1.5 * 2^23: the low byte is the int8 value
@@ -85,10 +86,10 @@ __device__ __forceinline__ void emit_int8(const NormArgs& a, const float2 (&y)[8
   } else {
     // s is subnormal (its reciprocal is not exact enough), or there is nothing to divide by
     const bool divide = s > 0.0f && s < 3.4e38f;
+    auto quotient = [&](float v) { return fminf(fmaxf(__fdiv_rn(v, s), -127.0f), 127.0f) + magic; };
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      f[i] = divide ? make_float2(__fdiv_rn(y[i].x, s) + magic, __fdiv_rn(y[i].y, s) + magic)
-                    : make_float2(magic, magic);
+      f[i] = divide ? make_float2(quotient(y[i].x), quotient(y[i].y)) : make_float2(magic, magic);
   }
   if (a.q || a.bsum) {
     uint32_t w[4];

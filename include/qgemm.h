@@ -341,9 +341,11 @@ qg_status qg_linear_fp8(const void* x, qg_dtype x_dtype, int64_t M, int64_t K, i
 /*       a residual: residual and sum both NULL)                            */
 /*   y = (h * (1 / sqrt(sum h^2 / K + eps))) * weight   (fp32)              */
 /*   q = e4m3(y * fl(1/s)), s = max |y| * fl(1/448) over 128 values; or     */
-/*   q = rint(y * fl(1/s)), s = max |y| / 127 over the row (int8)           */
+/*   q = clamp(rint(y * fl(1/s)), -127, 127), s = max |y| / 127 over the    */
+/*       row (int8)                                                         */
 /* with no rounding between y and q. (The quantizers above divide by s; a   */
-/* product differs beside ties alone.) The norm reads h as it is stored: a  */
+/* product differs beside ties alone. A subnormal s is divided by, and has  */
+/* so few bits that the clamp counts.) The norm reads h as it is stored: a  */
 /* call on x and a residual gives the bits of a call on their sum. A row's  */
 /* bits do not depend on the other rows of its call. NaN and infinities     */
 /* spread by IEEE rules: a NaN makes a row's scales NaN; an infinity        */
