@@ -52,3 +52,32 @@ def test_int8_scales_of_a_few_subnormal_units(top):
     s = scale.double()[:, None]
     near = torch.where(s > 0, (y / torch.where(s > 0, s, torch.ones_like(s))).clamp(-127, 127), torch.zeros_like(y))
     assert bool(((q.double() - near).abs() <= 0.5 + 2.0 ** -15).all())
+
+
+@pytest.mark.parametrize("m,k,dtype,wdtype", [(70, 5120, BF16, BF16), (9, 17408, BF16, F32), (64, 2560, F32, BF16),
+                                              (3, 32784, F32, F32)])
+def test_e4m3_is_the_nearest_value_but_beside_ties(m, k, dtype, wdtype):
+    # The root is a factor of every y of a row and of its scale: what is off in y / s is two roundings of y, two of
+    # the largest y, the constant's and the product's of s, fl(1/s) and its product, 8 * 2^-24. (Exact ties are common
+    # with bf16 rows and weights, whose products have few bits: which way one goes is not said.)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(m + k)
+    x = torch.randn(m, k, generator=g, device=DEV).to(dtype)
+    w = (1 + 0.2 * torch.randn(k, generator=g, device=DEV)).to(wdtype)
+    q, _, _ = qg.rmsnorm_quantize_act_fp8(x, w)
+    t = x.double().cpu() * w.double().cpu()
+    kb = -(-k // 128)
+    p = torch.zeros(m, kb * 128, dtype=torch.float64)
+    p[:, :k] = t
+    top = p.view(m, kb, 128).abs().amax(dim=2).repeat_interleave(128, 1)[:, :k]
+    v = 448 * t / top
+    values = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()     # 0 up to 448
+    middles = (values[1:] + values[:-1]) / 2
+    near = values[torch.bucketize(v.abs(), middles)] * v.sign()
+    tie = torch.zeros_like(v, dtype=torch.bool)
+    for i in (0, 1):        # the middle below and the one above
+        at = middles[(torch.bucketize(v.abs(), middles) - 1 + i).clamp(0, len(middles) - 1)]
+        tie |= (v.abs() - at).abs() <= 2.0 ** -21 * at
+    far = q.float().double().cpu() != near
+    assert not bool((far & ~tie).any())
+    assert int(far.sum()) <= int(tie.sum())
