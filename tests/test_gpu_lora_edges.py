@@ -1,0 +1,99 @@
+"""GPU tests of the adapters with many rows (tensor cores) where the other tests take few: strides,
+what lies around the outputs, addresses off 16 bytes; and values at the end of their range on both paths."""
+import pytest
+import torch
+
+import bit_quantized_gemm_gb300 as qg
+from test_gpu_lora import BF16, DEV, F32, check, few_rows, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from bit_quantized_gemm_gb300 import build
+    build.build()
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    yield
+    qg.check_device_error()
+
+
+TYPES = [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)]
+INF = float("inf")
+
+
+def around(m, n, dtype, left):
+    """Outputs [m, n] inside a buffer of sevens, `left` columns in, with a few rows more."""
+    es = 2 if dtype == BF16 else 4
+    ld = (left + n + 16) * es // 16 * 16 // es + 16 // es * (left == 0)
+    room = torch.full((m + 3, ld + (left > 0)), 7.0, device=DEV, dtype=dtype)
+    return room, room[:m, left:left + n]
+
+
+def untouched(room, m, n, left):
+    return (bool((room[:m, :left] == 7.0).all()) and bool((room[:m, left + n:] == 7.0).all())
+            and bool((room[m:] == 7.0).all()))
+
+
+@pytest.mark.parametrize("x,out", TYPES)
+@pytest.mark.parametrize("rank", [16, 64, 72])
+@pytest.mark.parametrize("m,n", [(129, 64), (200, 200), (300, 77), (131, 1000), (257, 2056)])
+def test_strides_in_place_and_what_lies_around(m, n, rank, x, out):
+    base, xs, a, b, ids, scaling = inputs(m + n + rank, m, 512, n, rank, 4, x, out, pad=16)
+    assert base.stride(0) == n + 16 and xs.stride(0) == 528
+    want = qg.add_lora(base, xs, a, b, ids, scaling)
+    check(want, base, xs, a, b, ids, scaling)
+    # the same bits from contiguous inputs
+    assert torch.equal(qg.add_lora(base.contiguous(), xs.contiguous(), a, b, ids, scaling), want)
+    for left in (0, 3):     # rows on 16-byte boundaries (where N allows), and off them
+        room, mine = around(m, n, out, left)
+        got = qg.add_lora(base, xs, a, b, ids, scaling, out=mine)
+        assert torch.equal(got, want) and untouched(room, m, n, left)
+        mine.copy_(base)
+        got = qg.add_lora(mine, xs, a, b, ids, scaling, out=mine)
+        assert torch.equal(got, want) and untouched(room, m, n, left)
+    # an aligned base, outputs off it, and the other way round
+    _, odd = around(m, n, out, 1)
+    odd.copy_(base)
+    assert torch.equal(qg.add_lora(odd, xs, a, b, ids, scaling), want)
+
+
+ROWS = [8, 130, 300]        # one at a time; by tensor cores
+
+
+@pytest.mark.parametrize("x,out", TYPES)
+@pytest.mark.parametrize("rank", [8, 24, 72])
+@pytest.mark.parametrize("m", ROWS)
+def test_non_finite_values_stay_to_their_rows_and_adapters(m, rank, x, out):
+    base, xs, a, b, _, scaling = inputs(m + rank, m, 272, 96, rank, 4, x, out)
+    ids = torch.arange(m, device=DEV) % 5 - 1
+    want = qg.add_lora(base, xs, a, b, ids, scaling)
+    assert bool(want.isfinite().all())
+    # NaN in an adapter's A, in one column's B, in a row of x (row 1 has adapter 0)
+    a[2, rank - 1, 100], b[3, 40, rank // 2], xs[1, 9] = float("nan"), float("nan"), float("nan")
+    got = qg.add_lora(base, xs, a, b, ids, scaling)
+    fine = (ids != 2) & (ids != 3)
+    fine[1] = False
+    assert torch.equal(got[fine], want[fine])
+    assert bool(got[ids == 2].isnan().all()) and bool(got[1].isnan().all())
+    rest = torch.arange(96, device=DEV) != 40
+    assert torch.equal(got[ids == 3][:, rest], want[ids == 3][:, rest]) and bool(got[ids == 3][:, 40].isnan().all())
+
+
+@pytest.mark.parametrize("x,out", TYPES)
+@pytest.mark.parametrize("rank", [8, 24, 72])
+@pytest.mark.parametrize("m", ROWS)
+def test_an_infinite_activation(m, rank, x, out):
+    # every rank's weight of its column is positive: h is +-inf, and every product with B has its sign
+    base, xs, a, b, _, scaling = inputs(m + rank, m, 272, 96, rank, 4, x, out)
+    ids = torch.arange(m, device=DEV) % 5 - 1
+    a[0, :, 100] = a[0, :, 100].abs() + 0.125
+    b[0] = b[0].abs() + 0.125
+    want = qg.add_lora(base, xs, a, b, ids, scaling)
+    xs[1, 100], xs[6, 100] = INF, -INF
+    got = qg.add_lora(base, xs, a, b, ids, scaling)
+    assert bool((got[1] == INF).all()) and bool((got[6] == -INF).all())
+    fine = torch.ones(m, dtype=torch.bool, device=DEV)
+    fine[1] = fine[6] = False
+    assert torch.equal(got[fine], want[fine])
