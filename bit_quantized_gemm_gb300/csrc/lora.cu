@@ -58,6 +58,12 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// the same, rounded towards zero
+__device__ __forceinline__ uint32_t bf16x2_rz(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 
@@ -332,7 +338,8 @@ struct LoraPieces {
 // One step of 32 values of K: A's rows are the MMA's 16, 8 rows of x its columns. A
 // lane has 8 consecutive k of a row of each: k 8t.. of 32, t = lane % 4, in
 // whatever order the MMA sums them. A value of x goes in as the sum of three bf16
-// numbers (24 bits).
+// numbers (24 bits), each rounded towards zero: to the nearest, values above 2^128 -
+// 2^119 would become infinite.
 template <int RT>
 struct ShrinkStep {
   uint4 w[RT][2], x[2];
@@ -346,7 +353,7 @@ struct ShrinkStep {
       uint32_t v[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        v[c] = bf16x2(f[2 * c], f[2 * c + 1]);
+        v[c] = bf16x2_rz(f[2 * c], f[2 * c + 1]);
         // (an infinity's rest would be NaN)
         f[2 * c] = isfinite(bf16_lo(v[c])) ? f[2 * c] - bf16_lo(v[c]) : 0.0f;
         f[2 * c + 1] = isfinite(bf16_hi(v[c])) ? f[2 * c + 1] - bf16_hi(v[c]) : 0.0f;
@@ -539,8 +546,10 @@ __device__ __forceinline__ void put_parts(const LoraArgs& a, int64_t m, int r, f
   v = r < a.rank ? make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale) : make_float4(0, 0, 0, 0);
   auto rest = [](float f, float h) { return isfinite(h) ? f - h : 0.0f; };  // (an infinity's would be NaN)
   uint2* to = reinterpret_cast<uint2*>(a.parts) + (m * a.rp + r) / 4;
+  // (a finite number's nearest is finite, too: bf16's largest for those above 2^128 - 2^119)
+  auto near = [](float f) { return isfinite(f) ? fminf(fmaxf(f, -0x1.FEp127f), 0x1.FEp127f) : f; };
   for (int i = 0; i < a.numbers; ++i, to += a.M * (a.rp / 4)) {
-    const uint2 n = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+    const uint2 n = make_uint2(bf16x2(near(v.x), near(v.y)), bf16x2(near(v.z), near(v.w)));
     *to = n;
     v = make_float4(rest(v.x, bf16_lo(n.x)), rest(v.y, bf16_hi(n.x)), rest(v.z, bf16_lo(n.y)), rest(v.w, bf16_hi(n.y)));
   }

@@ -97,3 +97,24 @@ def test_an_infinite_activation(m, rank, x, out):
     fine = torch.ones(m, dtype=torch.bool, device=DEV)
     fine[1] = fine[6] = False
     assert torch.equal(got[fine], want[fine])
+
+
+@pytest.mark.parametrize("x,out", TYPES)
+@pytest.mark.parametrize("m", ROWS)
+def test_values_at_the_end_of_their_range(m, x, out):
+    # finite numbers that round to infinity as bf16 (above 2^128 - 2^119), as activations and as h: with weights that
+    # bring them back the outputs are ordinary numbers
+    rank, top = 16, torch.finfo(x).max
+    base, xs, a, b, _, scaling = inputs(m, m, 272, 96, rank, 2, x, out)
+    ids = torch.arange(m, device=DEV) % 3 - 1
+    scaling.fill_(1.0)
+    xs[:, 100] = top * torch.where(torch.arange(m, device=DEV) % 2 == 0, 1.0, -1.0)
+    a[:, :, 100] = 2.0 ** -126
+    check(qg.add_lora(base, xs, a, b, ids, scaling), base, xs, a, b, ids, scaling)
+    xs.zero_()
+    xs[:, 3] = 2.0 ** 64
+    a.zero_()
+    a[:, :, 3] = 2.0 ** 63
+    scaling.fill_(2.0 - 2.0 ** -23)         # scaling * h: the largest fp32 number
+    b.mul_(2.0 ** -100)
+    check(qg.add_lora(base, xs, a, b, ids, scaling), base, xs, a, b, ids, scaling)
