@@ -497,8 +497,12 @@ def _norm_inputs(x, weight, residual):
     return M, K, ldx, ldr, dev
 
 
-def _norm_sum(total, x, M, K, stream, dev):
-    """(sum, its row stride): checked, allocated when None."""
+def _norm_sum(total, residual, x, M, K, stream, dev):
+    """(sum, its row stride): checked, allocated when None; (None, 0) without a residual."""
+    if residual is None:
+        if total is not None:
+            raise ValueError("sum is written where there is a residual only")
+        return None, 0
     if total is None:
         return _empty((M, K), x.dtype, x.device, stream), K
     m, k, ld = _rows(total, "sum", (x.dtype,), dev)
@@ -515,7 +519,8 @@ def rmsnorm_quantize_act_fp8(x, weight, eps=1e-6, residual=None, out=None, strea
     """Norm of the rows of x (cuda [M, K] bf16/fp32, rows may be strided; K % 16 == 0), or of
     x + residual, times weight (bf16/fp32 [K]), quantized in the layout of quantize_act_fp8, by products
     with 1/s -> (q float8_e4m3fn [M, K], scale fp32 [ceil(K/128), M], x + residual in x's dtype or
-    None). `out` may supply preallocated (q, scale, sum); sum may be residual or x itself."""
+    None). `out` may supply preallocated (q, scale, sum); sum may be residual or x itself, and is None
+    without a residual."""
     M, K, ldx, ldr, dev = _norm_inputs(x, weight, residual)
     _device(x, stream)
     if out is None:
@@ -528,7 +533,7 @@ def rmsnorm_quantize_act_fp8(x, weight, eps=1e-6, residual=None, out=None, strea
         if _rows(q, "q", (_FP8,), dev) != (M, K, K):
             raise ValueError("q must be contiguous and of the shape of x")
         lds = _fp8_scale(scale, M, K, dev)
-    total, ldsum = (None, 0) if residual is None else _norm_sum(total, x, M, K, stream, dev)
+    total, ldsum = _norm_sum(total, residual, x, M, K, stream, dev)
     if dev != _current_device():
         with torch.cuda.device(dev):
             return rmsnorm_quantize_act_fp8(x, weight, eps, residual, (q, scale, total), stream)
@@ -562,7 +567,7 @@ def rmsnorm_quantize_act(x, weight, eps=1e-6, residual=None, block_sums=False, q
                                   or not t.is_contiguous()):
                 raise ValueError("%s must be a contiguous %s tensor of shape %s on x's device" %
                                  (name, dtype, shape))
-    total, ldsum = (None, 0) if residual is None else _norm_sum(total, x, M, K, stream, dev)
+    total, ldsum = _norm_sum(total, residual, x, M, K, stream, dev)
     if dev != _current_device():
         with torch.cuda.device(dev):
             return rmsnorm_quantize_act(x, weight, eps, residual, out=(q, scale, bs, h, total), stream=stream)
