@@ -417,6 +417,10 @@ qg_status qg_gemm_fp8_grouped(const uint8_t* q, const float* scale, int64_t lds,
 /* of two bf16 numbers (off by 2^-17 of itself), of three where out is      */
 /* fp32, and fp32 x as the sum of three. A row's bits do not depend on the  */
 /* other rows of its call among calls of few rows, nor among calls of more. */
+/* NaN and infinities of x and base spread by IEEE rules, to their row      */
+/* alone; an infinite weight of an adapter leaves what it reaches infinite  */
+/* with few rows, infinite or NaN with more (its products with the numbers  */
+/* of such a sum are added up).                                             */
 /*   base, out [M][ldb], [M][ldo] of dtype, rows of N values, aligned to    */
 /*             their elements (fastest where rows begin and end on 16       */
 /*             bytes). out may be base itself (with ldo = ldb); it overlaps */

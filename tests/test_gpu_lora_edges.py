@@ -118,3 +118,32 @@ def test_values_at_the_end_of_their_range(m, x, out):
     scaling.fill_(2.0 - 2.0 ** -23)         # scaling * h: the largest fp32 number
     b.mul_(2.0 ** -100)
     check(qg.add_lora(base, xs, a, b, ids, scaling), base, xs, a, b, ids, scaling)
+
+
+@pytest.mark.parametrize("x,out", TYPES)
+@pytest.mark.parametrize("rank", [8, 24, 72])
+@pytest.mark.parametrize("m", ROWS)
+def test_an_infinite_weight_of_an_adapter(m, rank, x, out):
+    # few rows: the sign of the sum's terms; many: not finite. Everything else keeps its bits
+    base, xs, a, b, _, scaling = inputs(m + rank, m, 272, 96, rank, 4, x, out)
+    ids = torch.arange(m, device=DEV) % 5 - 1
+    xs[:, 100] = torch.where(torch.arange(m, device=DEV) % 2 == 0, 1.5, -1.5)
+    b[2] = b[2].abs() + 0.125
+    a[3, rank // 2] = 0
+    a[3, rank // 2, 100] = 1.0
+    want = qg.add_lora(base, xs, a, b, ids, scaling)
+    a[2, :, 100] = INF              # adapter 2: h = +-inf
+    b[3, 40, rank // 2] = -INF      # adapter 3: one column
+    got = qg.add_lora(base, xs, a, b, ids, scaling)
+    fine = (ids != 2) & (ids != 3)
+    rest = torch.arange(96, device=DEV) != 40
+    assert torch.equal(got[fine], want[fine]) and torch.equal(got[ids == 3][:, rest], want[ids == 3][:, rest])
+    two, three = got[ids == 2], got[ids == 3][:, 40]
+    if m <= few_rows(rank) or x == BF16:        # (one product for a bf16 activation)
+        assert torch.equal(two, (xs[ids == 2][:, 100:101] * INF).to(out).expand_as(two))
+    else:
+        assert not bool(two.isfinite().any())
+    if m <= few_rows(rank):
+        assert torch.equal(three, (xs[ids == 3][:, 100] * -INF).to(out))
+    else:
+        assert not bool(three.isfinite().any())
