@@ -63,6 +63,7 @@ def load():
         "qg_debug_prefill_plan_q8_0": ([I64, I64, I, P, P, P], I),
         "qg_debug_prefill_tile_q4k": ([I64, I64, I, P, P], I),
         "qg_debug_gemm_fp8_tile": ([I64, I64, I, P, P], I),
+        "qg_debug_gemm_fp8_grouped_tile": ([I64, I64, I64, I, P, P], I),
         "qg_debug_logprobs_pieces": ([I64, I64, I, P], I),
         "qg_linear_w8a8_q8_0": ([P, I, I64, I64, I64, P, I64, P, I, I64, P, P, SZ, P], I),
         "qg_linear_w4a8_q4k": ([P, I, I64, I64, I64, P, I64, P, I, I64, P, P, SZ, P], I),
@@ -737,6 +738,13 @@ def gemm_fp8_tile(M, N, sms):
     """Test support (host-only): (tokens, weight rows) of gemm_fp8's tile for M x N on `sms` SMs."""
     tokens, rows = ctypes.c_int(), ctypes.c_int()
     _check(load().qg_debug_gemm_fp8_tile(M, N, sms, ctypes.byref(tokens), ctypes.byref(rows)))
+    return tokens.value, rows.value
+
+
+def gemm_fp8_grouped_tile(M, N, experts, sms):
+    """Test support (host-only): (rows, weight rows) of gemm_fp8_grouped's tile for M rows of `experts` on `sms` SMs."""
+    tokens, rows = ctypes.c_int(), ctypes.c_int()
+    _check(load().qg_debug_gemm_fp8_grouped_tile(M, N, experts, sms, ctypes.byref(tokens), ctypes.byref(rows)))
     return tokens.value, rows.value
 
 

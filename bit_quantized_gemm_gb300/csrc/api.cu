@@ -55,6 +55,7 @@ cudaError_t launch_token_logprobs(const void* logits, bool bf16, int64_t M, int6
                                   const int64_t* ids, int64_t G, float* logprobs, float* entropy,
                                   int top, int64_t* top_ids, float* top_logprobs, cudaStream_t st);
 void fp8_tile(int64_t M, int64_t N, int sms, int* tokens, int* rows);
+void fp8_grouped_tile(int64_t M, int64_t N, int64_t E, int sms, int* tokens, int* rows);
 cudaError_t launch_norm_quantize(const void* x, const void* res, bool bf16, int64_t M, int64_t K,
                                  int64_t ldx, int64_t ldr, const void* weight, bool weight_bf16,
                                  float eps, void* sum, int64_t ldsum, bool fp8, uint8_t* q,
@@ -406,6 +407,17 @@ qg_status qg_debug_gemm_fp8_tile(int64_t M, int64_t N, int sms, int* tokens, int
     return fail(QG_EINVAL, "M, N out of range [1, 2^24]");
   if (sms < 1 || sms > 4096) return fail(QG_EINVAL, "sms=%d out of range [1, 4096]", sms);
   fp8_tile(M, N, sms, tokens, rows);
+  return QG_OK;
+}
+
+qg_status qg_debug_gemm_fp8_grouped_tile(int64_t M, int64_t N, int64_t experts, int sms, int* tokens, int* rows) {
+  if (!tokens || !rows) return fail(QG_EINVAL, "null pointer argument");
+  if (M < 1 || M > kMaxM || N < 1 || N > kMaxN)
+    return fail(QG_EINVAL, "M, N out of range [1, 2^24]");
+  if (experts < 1 || experts > kMaxExperts)
+    return fail(QG_EINVAL, "experts=%lld out of range [1, %lld]", (long long)experts, (long long)kMaxExperts);
+  if (sms < 1 || sms > 4096) return fail(QG_EINVAL, "sms=%d out of range [1, 4096]", sms);
+  fp8_grouped_tile(M, N, experts, sms, tokens, rows);
   return QG_OK;
 }
 

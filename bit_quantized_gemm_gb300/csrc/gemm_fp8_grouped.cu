@@ -36,6 +36,7 @@ cudaError_t launch_gemm_fp8_grouped_large(const uint8_t* q, const float* scale, 
                                           const int64_t* offsets, int64_t E, const uint8_t* w, int64_t ldw,
                                           int64_t lde, const float* w_scale, int64_t N, void* out, bool out_f32,
                                           int64_t ldo, uint32_t* err, cudaStream_t st);
+void fp8_grouped_large_tile(int64_t M, int64_t N, int64_t E, int sms, int* tokens, int* rows);
 
 struct Fp8GroupedArgs {
   const int64_t* offsets;  // [E + 1]
@@ -333,23 +334,36 @@ static cudaError_t launch_grouped(const uint8_t* q, const float* scale, int64_t 
   return cudaGetLastError();
 }
 
+// Tiles of 16 columns while all of them run at once (at most one more than the full
+// ones for every expert with rows): weights in 64 rows, 1 row of 64 experts, 17408 ->
+// 2560 18.7 us (128 rows 24.7), else in 128, 100 rows of 2 experts, 2560 -> 2432 7.9
+// (32 columns 8.7; the prefill kernel 9.9). Then by the mean rows of an expert: 512
+// rows of 64 experts 64.0, 65.6, 70.1; 2048 rows 78.8, 71.1, 73.8; 3000 rows 99, 83,
+// 72.8; 160 rows of 8 13.8, 14.8, 14.1. (Measured with nearly even experts: their rows
+// are not known here, and any tile is right for any of them.)
+void fp8_grouped_tile(int64_t M, int64_t N, int64_t E, int sms, int* tokens, int* rows) {
+  const int64_t tiles = (M < E ? M : E) + M / 16, mean = M / E;
+  *tokens = 16;
+  *rows = 64;
+  if (ceil_div(N, 64) * tiles <= sms) return;
+  *rows = 128;
+  if (ceil_div(N, 128) * tiles <= sms || mean <= 12) return;
+  *tokens = 32;
+  if (mean <= 32) return;
+  fp8_grouped_large_tile(M, N, E, sms, tokens, rows);
+}
+
 cudaError_t launch_gemm_fp8_grouped(const uint8_t* q, const float* scale, int64_t lds, int64_t M, int64_t K,
                                     const int64_t* offsets, int64_t E, const uint8_t* w, int64_t ldw, int64_t lde,
                                     const float* w_scale, int64_t N, void* out, bool out_f32, int64_t ldo,
                                     uint32_t* err, cudaStream_t st) {
   const Fp8GroupedArgs a{offsets, w_scale, out, ldo, (int)M, (int)N, (int)E, (int)ceil_div(K, 128),
                          (int)ceil_div(N, 128), 0, out_f32, err};
-  // Tiles of 16 columns while all of them run at once (at most one more than the full
-  // ones for every expert with rows): weights in 64 rows, 1 row of 64 experts, 17408 ->
-  // 2560 18.7 us (128 rows 24.7), else in 128, 100 rows of 2 experts, 2560 -> 2432 7.9
-  // (32 columns 8.7; the prefill kernel 9.9). Then by the mean rows of an expert: 512
-  // rows of 64 experts 64.0, 65.6, 70.1; 2048 rows 78.8, 71.1, 73.8; 3000 rows 99, 83,
-  // 72.8; 160 rows of 8 13.8, 14.8, 14.1.
-  const int64_t tiles = (M < E ? M : E) + M / 16, mean = M / E;
-  if (ceil_div(N, 64) * tiles <= num_sms()) return launch_grouped<64, 16>(q, scale, lds, K, w, ldw, lde, a, st);
-  if (ceil_div(N, 128) * tiles <= num_sms() || mean <= 12)
-    return launch_grouped<128, 16>(q, scale, lds, K, w, ldw, lde, a, st);
-  if (mean <= 32) return launch_grouped<128, 32>(q, scale, lds, K, w, ldw, lde, a, st);
+  int tokens, rows;
+  fp8_grouped_tile(M, N, E, num_sms(), &tokens, &rows);
+  if (tokens == 16 && rows == 64) return launch_grouped<64, 16>(q, scale, lds, K, w, ldw, lde, a, st);
+  if (tokens == 16) return launch_grouped<128, 16>(q, scale, lds, K, w, ldw, lde, a, st);
+  if (tokens == 32) return launch_grouped<128, 32>(q, scale, lds, K, w, ldw, lde, a, st);
   return launch_gemm_fp8_grouped_large(q, scale, lds, M, K, offsets, E, w, ldw, lde, w_scale, N, out, out_f32, ldo, err,
                                        st);
 }

@@ -719,11 +719,16 @@ static int fp8_large_choice(int64_t M, int64_t N, int sms, int64_t experts) {
   return best;
 }
 
-void fp8_tile(int64_t M, int64_t N, int sms, int* tokens, int* rows) {
-  if (M <= kFp8SmallM) return fp8_small_tile(M, N, sms, tokens, rows);
-  const Fp8LargeChoice& c = kChoices[fp8_large_choice(M, N, sms, 0)];
+// (experts: 0 where the product is not grouped)
+void fp8_grouped_large_tile(int64_t M, int64_t N, int64_t experts, int sms, int* tokens, int* rows) {
+  const Fp8LargeChoice& c = kChoices[fp8_large_choice(M, N, sms, experts)];
   *tokens = c.pair ? 256 : 128;
   *rows = c.w;
+}
+
+void fp8_tile(int64_t M, int64_t N, int sms, int* tokens, int* rows) {
+  if (M <= kFp8SmallM) return fp8_small_tile(M, N, sms, tokens, rows);
+  fp8_grouped_large_tile(M, N, 0, sms, tokens, rows);
 }
 
 template <bool kF32, bool kGrouped>

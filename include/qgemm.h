@@ -517,6 +517,12 @@ qg_status qg_debug_prefill_tile_q4k(int64_t M, int64_t N, int sms, int* kind, in
  * above) x *rows weight rows. Host-only. The tile never changes a bit. */
 qg_status qg_debug_gemm_fp8_tile(int64_t M, int64_t N, int sms, int* tokens, int* rows);
 
+/* Test support: the tile of qg_gemm_fp8_grouped for M rows of `experts` on a GPU of
+ * `sms` SMs: *tokens (16 or 32 for few rows an expert; 128 of a CTA or 256 of a pair)
+ * x *rows weight rows. Host-only. The tile never changes a bit. */
+qg_status qg_debug_gemm_fp8_grouped_tile(int64_t M, int64_t N, int64_t experts, int sms, int* tokens,
+                                         int* rows);
+
 /* Test support: the pieces that qg_token_logprobs cuts a row into, for M rows of
  * V values on a GPU of `sms` SMs. Host-only. */
 qg_status qg_debug_logprobs_pieces(int64_t M, int64_t V, int sms, int* pieces);
