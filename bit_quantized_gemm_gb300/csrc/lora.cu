@@ -1107,10 +1107,12 @@ __global__ void __launch_bounds__(ExpandMany<kBf16, kHalves>::kThreads, 1)
         }
         if (!ok) break;
         if (!aligned) {
-          // base and out in whole rows of the tile, element by element, all loads ahead of
-          // the first store (eight rows at a time: 4096 rows of 16 runs, 1024 -> 4099, rank
-          // 64, fp32 110 us in place of 85, bf16 79 and 71; loads ahead of the products 137
-          // and 71)
+          // base and out in whole rows of the tile, element by element, all 32 rows' loads ahead
+          // of the first store (4096 rows of 16 runs, 1024 -> 4099, rank 64: fp32 85 us, bf16
+          // 71; with eight rows' loads ahead of their stores 110 and 79, with all of them ahead
+          // of the products 137 and 71). The loop has one trip at most; without it the compiler
+          // forms every row's address ahead of the loads (in turn, buffers in L2: fp32 84.2 us in
+          // place of 77.8, bf16 62.6 and 60.4)
           __syncwarp();
           const uint32_t with = __ballot_sync(0xffffffffu, mine >= 0);
           const int rows = (int)min((int64_t)32, a.M - w0);
