@@ -46,7 +46,9 @@ struct GroupedTiles {
       }
     }
   }
-  __device__ int total() const { return before[E] * NT; }
+  // (ascending offsets have less than 2^30 tiles in any memory; others may claim rows
+  // hundreds of times over, and their tiles' numbers must not pass 2^31)
+  __device__ int total() const { return (int)min((int64_t)before[E] * NT, (int64_t)1 << 30); }
   // the expert of tile t, the number of its tile of rows and of weight rows; by a
   // whole warp (a 32-way search)
   __device__ void at(int t, int& e, int& mi, int& ni) const {

@@ -394,7 +394,8 @@ qg_status qg_silu_mul_quantize_act_fp8(const void* x, qg_dtype x_dtype, int64_t 
 /*             that nothing waits for the host. Values outside 0..M are     */
 /*             taken as 0 or M, an expert that ends before it begins has no */
 /*             rows; where two experts claim a row, either's result may     */
-/*             stand.                                                       */
+/*             stand (and rows claimed so often that 2^30 tiles do not hold */
+/*             them are left).                                              */
 /*   w         [experts] matrices [N][ldw] of e4m3, lde bytes from one to   */
 /*             the next (a multiple of 16, no overlap).                     */
 /*   w_scale   [experts][ceil(N/128)][ceil(K/128)] fp32, 4-byte aligned.    */
