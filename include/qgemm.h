@@ -347,11 +347,12 @@ qg_status qg_linear_fp8(const void* x, qg_dtype x_dtype, int64_t M, int64_t K, i
 /* product differs beside ties alone. A subnormal s is divided by, and has  */
 /* so few bits that the clamp counts.) The norm reads h as it is stored: a  */
 /* call on x and a residual gives the bits of a call on their sum. A row's  */
-/* bits do not depend on the other rows of its call. NaN and infinities     */
-/* spread by IEEE rules: a NaN makes a row's scales NaN; an infinity        */
-/* (1/sqrt is 0 then) makes its block's scale NaN (int8: the row's), and    */
-/* the row's products with it. int8: q is 0 where the scale is 0 or not     */
-/* finite.                                                                  */
+/* bits do not depend on the other rows of its call. sum h^2 is formed in   */
+/* fp32: where it leaves that range, 1/sqrt is 0 or (eps 0) infinite. NaN   */
+/* and infinities spread by IEEE rules: a NaN makes a row's scales NaN; an  */
+/* infinity (1/sqrt is 0 then) makes its block's scale NaN (int8: the       */
+/* row's), and the row's products with it. int8: q is 0 where the scale is  */
+/* 0 or not finite.                                                         */
 /*   x, residual, sum  [M][ld*] of x_dtype, rows of K values, 16-byte       */
 /*             aligned, ld* >= K, ld*elem_size % 16 == 0. sum may be x or   */
 /*             residual itself.                                             */

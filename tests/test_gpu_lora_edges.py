@@ -147,3 +147,32 @@ def test_an_infinite_weight_of_an_adapter(m, rank, x, out):
         assert torch.equal(three, (xs[ids == 3][:, 100] * -INF).to(out))
     else:
         assert not bool(three.isfinite().any())
+
+
+@pytest.mark.parametrize("x,out,rank", [(BF16, BF16, 16), (F32, F32, 64), (BF16, F32, 72), (F32, BF16, 128)])
+@pytest.mark.parametrize("m,n", [(130, 77), (700, 1000), (2100, 328)])
+def test_captured_and_replayed_with_other_ids(m, n, x, out, rank):
+    # two graphs of many rows that share a workspace, replayed in turn on other inputs and ids
+    base, xs, a, b, ids, scaling = inputs(m, m, 528, n, rank, 9, x, out)
+    ws = torch.full((qg.add_lora_workspace_bytes(m, 528, rank),), 255, dtype=torch.uint8, device=DEV)
+    outs = [torch.empty_like(base) for _ in range(2)]
+    qg.add_lora(base, xs, a, b, ids, scaling, out=outs[0], workspace=ws)
+    torch.cuda.synchronize()
+    graphs = []
+    for o in outs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            qg.add_lora(base, xs, a, b, ids, scaling, out=o, workspace=ws)
+        graphs.append(g)
+    turn = torch.arange(m, device=DEV)
+    for other in (turn % 9, torch.full_like(ids, -1), torch.full_like(ids, 8), turn // 100 % 11 - 1, turn * 37 % 40 - 3):
+        ids.copy_(other)
+        base.neg_()
+        xs.mul_(-1.0)
+        for g, o in zip(graphs, outs):
+            o.fill_(7.0)
+            g.replay()
+        torch.cuda.synchronize()
+        want = qg.add_lora(base, xs, a, b, ids, scaling)
+        check(want, base, xs, a, b, torch.where(ids < 9, ids, -1).clamp(min=-1), scaling)
+        assert all(torch.equal(o, want) for o in outs)

@@ -81,3 +81,22 @@ def test_e4m3_is_the_nearest_value_but_beside_ties(m, k, dtype, wdtype):
     far = q.float().double().cpu() != near
     assert not bool((far & ~tie).any())
     assert int(far.sum()) <= int(tie.sum())
+
+
+def test_sums_of_squares_beyond_fp32():
+    # (their sum is fp32: 1 / sqrt is 0 or, with eps 0, infinite; the rows beside keep their bits)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    x = torch.randn(6, 640, generator=g, device=DEV)
+    w = 1 + 0.2 * torch.randn(640, generator=g, device=DEV)
+    want, ws, _ = qg.rmsnorm_quantize_act_fp8(x, w, 0.0)
+    want8, ws8 = qg.rmsnorm_quantize_act(x, w, 0.0)[:2]
+    x[1] *= 2.0 ** 70
+    x[4] *= 2.0 ** -90
+    q, s, _ = qg.rmsnorm_quantize_act_fp8(x, w, 0.0)
+    q8, s8 = qg.rmsnorm_quantize_act(x, w, 0.0)[:2]
+    rest = [0, 2, 3, 5]
+    assert torch.equal(q[rest].view(torch.uint8), want[rest].view(torch.uint8)) and torch.equal(s[:, rest], ws[:, rest])
+    assert torch.equal(q8[rest], want8[rest]) and torch.equal(s8[rest], ws8[rest])
+    assert bool((s[:, 1] == 0).all()) and not bool(q[1].float().any()) and s8[1] == 0 and not bool(q8[1].any())
+    assert not bool(s[:, 4].isfinite().any()) and not bool(s8[4].isfinite())
