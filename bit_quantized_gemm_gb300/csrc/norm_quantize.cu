@@ -15,13 +15,17 @@
 // (512 values) as a butterfly, a row's units by their number -- whichever warps
 // hold them. So a row's bits depend neither on its batch nor on the launch.
 //
-// HBM-bound: 2 + 2 bytes read and 2 + 1 written a value (bf16, residual). Every
-// value is read once and held in registers over the row's barrier; several rows'
-// CTAs on an SM fill one another's waits. 8192 x 5120 bf16 with a residual: 47.2 us,
-// 6.25 TB/s (a plain copy: 6.77). A ring of bulk copies in shared memory instead of
-// the registers was slower. One row: 2.1 us, a launch and two trips to memory.
-// The gate reads 4 bytes and writes 1 a value: 8192 x 17408 116.5 us, 6.15 TB/s;
-// beside memory, the two special-function results a value are what it issues most.
+// With a residual HBM-bound: 2 + 2 bytes read and 2 + 1 written a value (bf16). Every
+// value is read once and held by its lane over the row's barrier -- in registers with
+// one unit a warp and weights of the rows' type, partly in local memory (spills of 32
+// to 208 bytes a thread with two units a warp or fp32 weights of bf16 rows, up to 980
+// with four, K > 17408); several rows' CTAs on an SM fill one another's waits. 8192 x
+// 5120 bf16 with a residual: 47.2 us, 6.25 TB/s (a plain copy: 6.77). A ring of bulk
+// copies in shared memory instead of the registers was slower. Without a residual the
+// same instructions move half the bytes, and they and the barrier are what bounds it:
+// 31.8 us, 3.95 TB/s. One row: 2.1 us, a launch and two trips to memory. The gate reads
+// 4 bytes and writes 1 a value: 8192 x 17408 116.5 us, 6.15 TB/s; beside memory, the
+// two special-function results a value are what it issues most.
 #include "quantize_fp8.cuh"
 
 namespace qg {
@@ -129,7 +133,8 @@ constexpr int kNormMaxWarps = 32, kNormMaxUnits = kMaxK / 512;
 // Registers decide how many rows an SM works on at once: 8192 x 5120 bf16 with a
 // residual 48.2 us with 40 (five CTAs), 51.4 with 52 (three); without one 31.0 and
 // 36.8. Rows in two units a warp, 8192 x 17408 bf16 without a residual: 132 us with
-// 56 (two CTAs), 145 with 77 (one).
+// 56 (two CTAs), 145 with 77 (one). (Measured with bf16 weights: fp32 weights of bf16
+// rows have the same registers, spill, and take 58.3 us where those take 45.8.)
 template <bool kBf16, bool kWBf16, int kU>
 constexpr int kNormRegs = kU == 4 ? 64 : kU == 2 ? (kBf16 ? 56 : 96) : kBf16 ? 40 : kWBf16 ? 48 : 56;
 

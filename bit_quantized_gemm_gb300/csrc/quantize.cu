@@ -194,8 +194,8 @@ static void launch_q_k(const QArgs& a, cudaStream_t st) {
   // * many rows (M >= 1024, throughput): a thread holds one 8-value chunk and
   //   re-reads the rest of the row for the quantize pass (from L2), so that
   //   many rows are in flight per SM: 8192 x 5120 47.8 (row held: 51.8),
-  //   8192 x 17408 144 (held: 236), 2048 x 9728 31.3 (33.4); rows up to 3072
-  //   stay held (2048 x 2560: 15.0 both ways);
+  //   8192 x 17408 144 (held: 236), 2048 x 9728 31.3 (33.4); rows of
+  //   three chunks a thread or less stay held (2048 x 2560: 15.0 both ways);
   // * few rows (decode sizes, latency): the row is held in registers between
   //   its two passes with threads x chunks x 8 >= K (64 x 5120: 8.8 against
   //   10.9 re-read), and rows longer than 10240 take the 256-thread re-read
