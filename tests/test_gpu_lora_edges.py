@@ -176,3 +176,21 @@ def test_captured_and_replayed_with_other_ids(m, n, x, out, rank):
         want = qg.add_lora(base, xs, a, b, ids, scaling)
         check(want, base, xs, a, b, torch.where(ids < 9, ids, -1).clamp(min=-1), scaling)
         assert all(torch.equal(o, want) for o in outs)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("n", [96, 77])
+def test_rows_without_an_adapter_keep_their_bits_among_others(n, out):
+    # many rows, every second one without an adapter: NaN with payloads, -0, subnormal numbers of base stay
+    base, xs, a, b, ids, scaling = inputs(n, 300, 256, n, 16, 3, BF16, out)
+    word = torch.int16 if out == BF16 else torch.int32
+    shift = 0 if out == BF16 else 16
+    for col, v in ((5, 0x7FA3), (6, -0x8000), (7, 0x0001), (8, -0x7FFF)):
+        base.view(word)[:, col] = v << shift
+    ids[::2] = torch.tensor([-1, 3, 2 ** 40, -2 ** 40, 99] * 30, device=DEV)
+    ids[1::2] = torch.arange(150, device=DEV) % 3
+    for mine in (None, base.clone()):       # to other memory, and in place
+        got = qg.add_lora(base if mine is None else mine, xs, a, b, ids, scaling, out=mine)
+        assert torch.equal(got.view(word)[::2], base.view(word)[::2])
+        assert bool(got[1::2, 5].isnan().all()) and bool(got[1::2, 9:].isfinite().all())
+        assert not bool((got[1::2, 9:] == base[1::2, 9:]).all())
